@@ -22,13 +22,13 @@ IGNORE = -100
 def listed():
     return [
         # the smallest product, where the launches count: 256 tokens, 512 -> 256
-        dict(name="fp8 fprop 256x512x256", op="fp8_linear", which="fprop", M=256, K=512, N=256, out="f32"),
-        # the QKV projection of a layer at 8192 tokens, its activation going on in bf16
-        dict(name="fp8 fprop 8192x4096x6144", op="fp8_linear", which="fprop", M=8192, K=4096, N=6144, out="bf16"),
+        dict(name="fp8 fprop 256x512x256", op="fp8_linear", which="fprop", M=256, K=512, N=256),
+        # the QKV projection of a layer at 8192 tokens
+        dict(name="fp8 fprop 8192x4096x6144", op="fp8_linear", which="fprop", M=8192, K=4096, N=6144),
         # a ragged batch through odd feature sizes: nothing is a multiple of a block
-        dict(name="fp8 dgrad 1111x1000x2001", op="fp8_linear", which="dgrad", M=1111, K=1000, N=2001, out="bf16"),
-        # the down projection's weight gradient, added up in FP32
-        dict(name="fp8 wgrad 8192x14336x4096", op="fp8_linear", which="wgrad", M=8192, K=14336, N=4096, out="f32"),
+        dict(name="fp8 dgrad 1111x1000x2001", op="fp8_linear", which="dgrad", M=1111, K=1000, N=2001),
+        # the down projection's weight gradient over a step's 8192 tokens
+        dict(name="fp8 wgrad 8192x14336x4096", op="fp8_linear", which="wgrad", M=8192, K=14336, N=4096),
         # a small model's head, one short sequence
         dict(name="xent 128x512x1000", op="xent", T=128, K=512, V=1000, train=True),
         # evaluation: the loss alone, over a medium vocabulary with an odd size
@@ -61,7 +61,7 @@ def draw(rng):
     while True:
         if op == "fp8_linear":
             c = dict(op=op, which=rng.choice(["fprop", "dgrad", "wgrad"]), M=_size(rng, 1, 16384), K=_size(rng, 32, 14336),
-                     N=_size(rng, 32, 14336), out=rng.choice(["f32", "bf16"]))
+                     N=_size(rng, 32, 14336))
             if c["M"] * c["K"] * c["N"] <= 8192 * 14336 * 4096:
                 return c
         elif op == "xent":
@@ -100,7 +100,7 @@ def prepare(case, seed):
         w = (0.02 * torch.randn(N, K, generator=g, device="cuda")).to(bf16)
         dy = _heavy(g, M, N, 1e-3).to(bf16)
         a, b = {"fprop": (x, w), "dgrad": (dy, w), "wgrad": (dy, x)}[case["which"]]
-        return dict(case=case, a=a, b=b, dtype=torch.float32 if case["out"] == "f32" else bf16)
+        return dict(case=case, a=a, b=b)
     if case["op"] == "xent":
         T, K, V = case["T"], case["K"], case["V"]
         w = (0.02 * torch.randn(V, K, generator=g, device="cuda")).to(bf16)
@@ -144,7 +144,7 @@ def _plain_fp8(s):
         y = _blocks(a, False) @ _blocks(b, True)
     else:
         y = _blocks(a.t(), False) @ _blocks(b.t(), False).t()
-    return y.to(s["dtype"])
+    return y.to(torch.bfloat16)
 
 
 def _plain_xent(s):
@@ -185,7 +185,7 @@ def _own(s):
     op = s["case"]["op"]
     if op == "fp8_linear":
         call = {"fprop": mx.fp8_linear_fprop, "dgrad": mx.fp8_linear_dgrad, "wgrad": mx.fp8_linear_wgrad}[s["case"]["which"]]
-        return call(s["a"], s["b"], out_dtype=s["dtype"])
+        return call(s["a"], s["b"], out_dtype=torch.bfloat16)
     if op == "xent":
         loss, lse = mx.linear_xent_forward(s["x"], s["w"], s["target"], ignore_index=IGNORE)
         if not s["case"]["train"]:
@@ -205,9 +205,8 @@ def run(state):
 def work(case):
     if case["op"] == "fp8_linear":
         M, K, N = case["M"], case["K"], case["N"]
-        out = 4 if case["out"] == "f32" else 2
         ins, outs = {"fprop": (M * K + N * K, M * N), "dgrad": (M * N + N * K, M * K), "wgrad": (M * N + M * K, N * K)}[case["which"]]
-        return {"bytes": 2 * ins + out * outs, "flops": 2 * M * K * N}
+        return {"bytes": 2 * ins + 2 * outs, "flops": 2 * M * K * N}
     if case["op"] == "xent":
         T, K, V = case["T"], case["K"], case["V"]
         ins = 2 * (T * K + V * K) + 8 * T
