@@ -17,7 +17,7 @@ __all__ = [
     "Mxfp4Error", "RHT", "ORTHO", "SCALE_NOCLIP", "quantize", "quantize_dual", "gemm", "linear_fprop",
     "linear_dgrad", "linear_wgrad", "linear_forward", "linear_backward", "step_workspace_bytes", "workspace_bytes", "library_path", "lib", "RNE", "SR", "FPROP", "DGRAD", "WGRAD", "ROWS", "TILED",
     "tiled_sizes", "gemm_workspace_bytes", "linear_fprop_noalloc", "NOALLOC_SCRATCH_BYTES",
-]
+]  # and those of train.py, below
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmxfp4.so")
@@ -523,3 +523,10 @@ def linear_backward(dy, K, workspace, hadamard=16, fprop="rne", dgrad="rne", wgr
                                      workspace.numel(), dx.data_ptr(), dw.data_ptr(), _stream(stream))
     _check(st, "mxfp4_linear_backward")
     return dx, dw
+
+
+# 8-bit linear products, the head's loss and the orthogonalised update (libmxfp4_train.so)
+from . import train as _train  # noqa: E402
+from .train import *  # noqa: E402,F401,F403
+
+__all__ += _train.__all__
