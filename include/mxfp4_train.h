@@ -103,7 +103,7 @@ mxfp4_status_t mxfp4_fp8_linear_wgrad(const void *dy_bf16, const void *x_bf16, i
  *   z = X W^T (bf16 operands, FP32 products, never stored),  lse_t = log sum_v exp z_tv,
  *   loss_t = lse_t - z_t,target(t)   (0 where target(t) == ignore_index; NaN where it is no index)
  *
- * X[T][ldx], W[V][ldw] bf16; target int64 [T]; loss and lse FP32 [T]. With K % 32 == 0 both are read in
+ * X[T][ldx], W[V][ldw] bf16; target int64 [T]; loss and lse FP32 [T]. With K % 64 == 0 both are read in
  * place and need 16-byte aligned rows (pointer, and ldx, ldw multiples of 8); any other K is copied
  * into the workspace first, padded, and needs no alignment. A row of logits with a NaN or +infinity
  * gives NaN. The caller reduces the losses as it likes: the backward
@@ -114,8 +114,10 @@ mxfp4_status_t mxfp4_fp8_linear_wgrad(const void *dy_bf16, const void *x_bf16, i
  *
  * dloss, dlse FP32 [T], either may be NULL (zeros); a row whose target is ignore_index or no index
  * counts with dloss_t = 0. A row with dloss_t = dlse_t = 0 adds nothing, whatever it holds (NaN in X
- * included). lse is the forward call's. G is rounded to bf16 once, before the products (one more
- * rounding of 2^-9 on each term of dX and dW). dx [T][K] and dw [V][K], dense, FP32 or bf16; either
+ * included). lse is the forward call's. The products of the gradients take FP16 operands, G, X and W each
+ * scaled by a power of two to FP16's range: an entry of G is rounded to half a step of FP16 (2^-11 of
+ * itself), and entries of G, X and W below 2^-28 of the largest (of |dloss| + |dloss + dlse| for G) to
+ * 2^-39 of that. dx [T][K] and dw [V][K], dense, FP32 or bf16; either
  * may be NULL, and is then not computed.
  * Requirements: T >= 0, K, V >= 1, below 2^21 (T, K) and 2^31 (V); ldx, ldw >= K and below 2^21.
  * T == 0 returns MXFP4_OK after setting dw, if given, to zero.

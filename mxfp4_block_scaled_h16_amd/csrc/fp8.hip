@@ -257,7 +257,7 @@ hipError_t launch_fp8_gemm(const uint8_t *aq, int64_t lda, const uint8_t *as, in
     op.ldbs = ldbs;
     op.M = (int)M;
     op.N = (int)N;
-    op.nk = (int)(round_up(K, 128) / 64);
+    op.nk = (int)(round_up(K, 128) / 128);
     const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
     auto run = [&](const auto &epi) {
         return big > kComputeUnits / 2 ? launch_product<E4M3, Big>(op, epi, 1, stream)

@@ -28,7 +28,7 @@ constexpr float kLoScale = 2048.0f, kLoUnscale = 1.0f / 2048.0f;   // the remain
 
 __device__ __forceinline__ uint16_t f16_bits(float x) { return __builtin_bit_cast(uint16_t, (_Float16)x); }
 __device__ __forceinline__ float f16_float(uint16_t b) { return (float)__builtin_bit_cast(_Float16, b); }
-__device__ __forceinline__ f32x4 f16_quad(const uint16_t *p)
+[[maybe_unused]] __device__ __forceinline__ f32x4 f16_quad(const uint16_t *p)
 {
     const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
     // copied out first: a bit cast of a vector's element reads the vector's first one
@@ -44,14 +44,11 @@ struct GramEpi {
     uint16_t *out;
     int64_t ld, batch_out;
     template <class G>
-    __device__ __forceinline__ void run(v16f (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
     {
         uint16_t *o = out + w.batch * batch_out;
         store_tile16<G>(w, lds, [](float a, float b) { return pack_f16(a, b); },
-                        [&](int i, int j, int q) {
-                            return f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]} *
-                                   kUnscale;
-                        },
+                        [&](int i, int j) { return acc[i][j] * kUnscale; },
                         o, ld, w.m0 == w.n0 ? nullptr : o, ld);
     }
 };
@@ -64,18 +61,17 @@ struct PolyEpi {
     int64_t ld, batch_out;
     float b, c;
     template <class G>
-    __device__ __forceinline__ void run(v16f (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
     {
         const uint16_t *in = gram + w.batch * batch_out;
         uint16_t *o = out + w.batch * batch_out;
-        const int r = w.lane & 31, half = w.lane >> 5;
+        const int r = w.lane & 15, q = w.lane >> 4;
         const float cs = c * kUnscale;
         store_tile16<G>(w, lds, [](float x, float y) { return pack_f16(x, y); },
-                        [&](int i, int j, int q) {
-                            const f32x4 g = f16_quad(in + (int64_t)(w.m0 + w.row0 + 32 * i + r) * ld + w.n0 + w.col0 + 32 * j +
-                                                     8 * q + 4 * half);
-                            return b * g + cs * f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                                                      acc[i][j][4 * q + 3]};
+                        [&](int i, int j) {
+                            const f32x4 g =
+                                f16_quad(in + (int64_t)(w.m0 + w.row0 + 16 * i + r) * ld + w.n0 + w.col0 + 16 * j + 4 * q);
+                            return b * g + cs * acc[i][j];
                         },
                         o, ld, w.m0 == w.n0 ? nullptr : o, ld);
     }
@@ -90,33 +86,25 @@ struct UpdateEpi {
     int64_t ld, ld_turned, batch_x;
     float a;
     template <class G>
-    __device__ __forceinline__ void run(v16f (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
     {
-        const int r = w.lane & 31, half = w.lane >> 5;
+        const int r = w.lane & 15, q = w.lane >> 4;
         const uint16_t *h = hi + w.batch * batch_x;
         uint16_t *l = lo + w.batch * batch_x;
 #pragma unroll
         for (int i = 0; i < G::FI; ++i)
 #pragma unroll
-            for (int j = 0; j < G::FJ; ++j)
+            for (int j = 0; j < G::FJ; ++j) {
+                const int64_t at = (int64_t)(w.m0 + w.row0 + 16 * i + r) * ld + w.n0 + w.col0 + 16 * j + 4 * q;
+                const f32x4 x = f16_quad(h + at) + f16_quad(l + at) * kLoUnscale;
+                const f32x4 v = a * x + kUnscale * acc[i][j];
+                f32x4 rem;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t at = (int64_t)(w.m0 + w.row0 + 32 * i + r) * ld + w.n0 + w.col0 + 32 * j + 8 * q + 4 * half;
-                    const f32x4 x = f16_quad(h + at) + f16_quad(l + at) * kLoUnscale;
-                    const f32x4 v = a * x + kUnscale * f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                                                             acc[i][j][4 * q + 3]};
-                    f32x4 rem;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        acc[i][j][4 * q + t] = v[t];
-                        rem[t] = (v[t] - f16_float(f16_bits(v[t]))) * kLoScale;
-                    }
-                    *reinterpret_cast<u32x2 *>(l + at) = u32x2{pack_f16(rem[0], rem[1]), pack_f16(rem[2], rem[3])};
-                }
-        store_tile16<G>(w, lds, [](float x, float y) { return pack_f16(x, y); },
-                        [&](int i, int j, int q) {
-                            return f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                        },
+                for (int t = 0; t < 4; ++t) rem[t] = (v[t] - f16_float(f16_bits(v[t]))) * kLoScale;
+                acc[i][j] = v;
+                *reinterpret_cast<u32x2 *>(l + at) = u32x2{pack_f16(rem[0], rem[1]), pack_f16(rem[2], rem[3])};
+            }
+        store_tile16<G>(w, lds, [](float x, float y) { return pack_f16(x, y); }, [&](int i, int j) { return acc[i][j]; },
                         hi_out + w.batch * batch_x, ld, turned + w.batch * batch_x, ld_turned);
     }
 };
@@ -130,22 +118,14 @@ struct LastEpi {
     float a;
     StoreEpi<BF16_OUT> store;   // alpha covers X's 2^10
     template <class G>
-    __device__ __forceinline__ void run(v16f (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
     {
-        const int r = w.lane & 31, half = w.lane >> 5;
+        const int r = w.lane & 15, q = w.lane >> 4;
         const uint16_t *h = hi + w.batch * batch_x, *l = lo + w.batch * batch_x;
-#pragma unroll
-        for (int i = 0; i < G::FI; ++i)
-#pragma unroll
-            for (int j = 0; j < G::FJ; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t at = (int64_t)(w.m0 + w.row0 + 32 * i + r) * ld + w.n0 + w.col0 + 32 * j + 8 * q + 4 * half;
-                    const f32x4 x = f16_quad(h + at) + f16_quad(l + at) * kLoUnscale;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) acc[i][j][4 * q + t] = a * x[t] + kUnscale * acc[i][j][4 * q + t];
-                }
-        store.template run<G>(acc, w, op, lds);
+        store.template run_with<G>(w, op, lds, [&](int i, int j) {
+            const int64_t at = (int64_t)(w.m0 + w.row0 + 16 * i + r) * ld + w.n0 + w.col0 + 16 * j + 4 * q;
+            return a * (f16_quad(h + at) + f16_quad(l + at) * kLoUnscale) + kUnscale * acc[i][j];
+        });
     }
 };
 
@@ -324,12 +304,12 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
         op.a = op.b = reinterpret_cast<const uint8_t *>(wide ? x : t);
         op.lda = op.ldb = 2 * (wide ? z.np : z.mp);
         op.M = op.N = (int)z.sp;
-        op.nk = (int)((wide ? z.np : z.mp) / 32);
+        op.nk = (int)((wide ? z.np : z.mp) / 64);
         op.batch_a = op.batch_b = 2 * bx;
         if ((e = product(z.big, op, GramEpi{s.gram, z.sp, ba}, p.batch, stream))) return e;
         op.a = op.b = reinterpret_cast<const uint8_t *>(s.gram);
         op.lda = op.ldb = 2 * z.sp;
-        op.nk = (int)(z.sp / 32);
+        op.nk = (int)(z.sp / 64);
         op.batch_a = op.batch_b = 2 * ba;
         if ((e = product(z.big, op, PolyEpi{s.gram, s.poly, z.sp, ba, p.b, p.c}, p.batch, stream))) return e;
         // the update in X's orientation: poly X for wide, X poly for tall (poly is symmetric)
@@ -339,7 +319,7 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
         op.b = reinterpret_cast<const uint8_t *>(wide ? t : s.poly);
         op.ldb = 2 * (wide ? z.mp : z.sp);
         op.batch_b = 2 * (wide ? bx : ba);
-        op.nk = (int)(z.sp / 32);
+        op.nk = (int)(z.sp / 64);
         op.M = (int)z.mp;
         op.N = (int)z.np;
         if (k + 1 < p.steps) {

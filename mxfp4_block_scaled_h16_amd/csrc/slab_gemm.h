@@ -1,19 +1,26 @@
 // Matrix products C[m][n] = sum_k A[m][k] B[n][k] on gfx950's matrix cores, for 8- and 16-bit
 // elements and with an epilogue of the caller's (device code, header only).
 //
-// Both operands are row-major along k. A stage is 64 bytes of every row of the workgroup's tile
-// (32 values of 16 bits, 64 of 8 bits), brought from memory to the LDS by direct 16-byte-per-lane
-// loads into a ring of four stage buffers, three stages ahead. In units of 64-byte rows every element
-// type costs the same: per stage and 32 x 32 output tile two v_mfma_f32_32x32x16 (16-bit) or one
-// v_mfma_scale_f32_32x32x64_f8f6f4 (8-bit), 64 matrix-core cycles either way, so one tiling and
-// one pipeline serve them all. The rows of a stage buffer hold their four 16-byte chunks
-// XOR-permuted by bits 2-3 of the row: the 16 lanes that the LDS serves at a time then read 16
-// distinct bank groups.
+// Both operands are row-major along k. A stage is 128 bytes of every row of the workgroup's tile
+// (64 values of 16 bits, 128 of 8 bits: a whole cache line, and with 8 bits a whole scale block),
+// brought from memory to the LDS by direct 16-byte-per-lane loads into two stage buffers. In
+// units of 128-byte rows every element type costs the same: per stage and 16 x 16 output tile two
+// v_mfma_f32_16x16x32 (16-bit) or one v_mfma_scale_f32_16x16x128_f8f6f4 (8-bit), 32 matrix-core
+// cycles either way, so one tiling and one pipeline serve them all.
+//
+// Measured at 8192 x 8192 x 8192 in bf16 (TFLOP/s in turn on one card): stages of 64 bytes in a ring
+// of four, which ask the L1 for every line twice: 1213; of 128 bytes: 1348; with buffer loads, whose
+// addresses are one register and a scalar: 1390. 32 x 32 MFMAs instead of 16 x 16: 1274. Loads spread
+// over the second half of a stage instead of bunched behind the barrier: 1360; a second barrier
+// that leaves them half a stage longer: 1340.
+//
+// The rows of a stage buffer hold their eight 16-byte chunks XOR-permuted by bits 1-3 of the row: the
+// 16 lanes that the LDS serves at a time read one chunk of 16 rows, and so 16 distinct bank groups.
 //
 // The product is formed transposed (B as the first operand of the MFMA), so a lane ends with
-// one row of C per 32-row tile and runs of four consecutive columns: register 4 q + t of
-// acc[i][j] in lane (r, half) is C[m0 + row0 + 32 i + r][n0 + col0 + 32 j + 8 q + 4 half + t].
-// Row statistics (a softmax) then need one cross-lane step, and the output goes through the LDS
+// one row of C per 16-row tile and runs of four consecutive columns: register t of acc[i][j] in lane
+// (r, q), r = lane % 16, q = lane / 16, is C[m0 + row0 + 16 i + r][n0 + col0 + 16 j + 4 q + t].
+// Row statistics (a softmax) then need two cross-lane steps, and the output goes through the LDS
 // so that stores cover whole lines.
 #pragma once
 
@@ -27,7 +34,6 @@ namespace slab {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -36,38 +42,37 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef const __attribute__((address_space(1))) void gbl_void_t;
 
-constexpr int kRowBytes = 64;    // bytes of a row per stage
-constexpr int kNumBuf = 4;       // stage ring
-constexpr int kRowsPerDma = 16;  // a wave-wide 16-byte-per-lane load covers 16 rows of a stage
+constexpr int kRowBytes = 128;   // bytes of a row per stage
+constexpr int kRowsPerDma = 8;   // a wave-wide 16-byte-per-lane load covers 8 rows of a stage
 constexpr int kComputeUnits = 256;
 
 // ------------------------------------------------------------------------- element types ------
 struct BF16 {
     static constexpr bool kScaled = false;
-    static __device__ __forceinline__ void mfma(v16f &acc, const u32x4 &b, const u32x4 &a)
+    static __device__ __forceinline__ void mfma(f32x4 &acc, const u32x4 &b, const u32x4 &a)
     {
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a),
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a),
                                                       acc, 0, 0, 0);
     }
 };
 struct F16 {
     static constexpr bool kScaled = false;
-    static __device__ __forceinline__ void mfma(v16f &acc, const u32x4 &b, const u32x4 &a)
+    static __device__ __forceinline__ void mfma(f32x4 &acc, const u32x4 &b, const u32x4 &a)
     {
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a),
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a),
                                                      acc, 0, 0, 0);
     }
 };
-// E4M3 codes with an E8M0 scale byte for each 128 values of a row. A lane supplies 32 of the 64
+// E4M3 codes with an E8M0 scale byte for each 128 values of a row. A lane supplies 32 of the 128
 // values of a stage; which 32 does not matter, as A and B take the same ones and all share a scale.
 struct E4M3 {
     static constexpr bool kScaled = true;
-    static __device__ __forceinline__ void mfma(v16f &acc, const u32x4 &b0, const u32x4 &b1, const u32x4 &a0,
+    static __device__ __forceinline__ void mfma(f32x4 &acc, const u32x4 &b0, const u32x4 &b1, const u32x4 &a0,
                                                 const u32x4 &a1, uint32_t sb, uint32_t sa)
     {
         const v8i vb = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
         const v8i va = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(vb, va, acc, 0, 0, 0, (int)sb, 0, (int)sa);
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, acc, 0, 0, 0, (int)sb, 0, (int)sa);
     }
 };
 
@@ -86,7 +91,7 @@ __device__ __forceinline__ void barrier()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-__device__ __forceinline__ int chunk_perm(int row) { return (row >> 2) & 3; }
+__device__ __forceinline__ int chunk_perm(int row) { return (row >> 1) & 7; }
 
 // ------------------------------------------------------------------------------ geometry ------
 // NW_ wavefronts on a TM x TN tile, arranged WM x (NW_ / WM).
@@ -95,11 +100,11 @@ struct Geo {
     static constexpr int NW = NW_, kTileM = TM, kTileN = TN;
     static constexpr int kABytes = TM * kRowBytes;
     static constexpr int kStageBytes = (TM + TN) * kRowBytes;
-    static constexpr int kRingBytes = kNumBuf * kStageBytes;
-    static constexpr int kScaleSlot = (TM + TN) * 16;             // 16 scale bytes per row: 2048 values
+    static constexpr int kRingBytes = 2 * kStageBytes;
+    static constexpr int kScaleSlot = (TM + TN) * 16;             // 16 scale bytes per row: 16 stages
     static constexpr int kWavesM = WM, kWavesN = NW / WM;
     static constexpr int kWaveRows = TM / kWavesM, kWaveCols = TN / kWavesN;
-    static constexpr int FI = kWaveRows / 32, FJ = kWaveCols / 32;
+    static constexpr int FI = kWaveRows / 16, FJ = kWaveCols / 16;
     static constexpr int kDmaA = TM / kRowsPerDma / NW, kDmaB = TN / kRowsPerDma / NW;
     static constexpr int kDmaPerStage = kDmaA + kDmaB;
     static_assert(kDmaA * kRowsPerDma * NW == TM && kDmaB * kRowsPerDma * NW == TN, "whole loads per wavefront");
@@ -119,7 +124,7 @@ using Small = Geo<4, 128, 128, 2>;   // wave tiles 64 x 64, two workgroups per C
 
 // --------------------------------------------------------------------------------- operands ---
 // Rows past M and N are read as row M - 1 and N - 1 (their results are the epilogue's to drop).
-// Every row is readable, and zero past its length, up to nk stages; 16-byte aligned.
+// Every row is readable, and zero past its length, up to nk whole stages; 16-byte aligned.
 struct Operands {
     const uint8_t *a, *b;
     int64_t lda, ldb;          // bytes
@@ -165,11 +170,19 @@ __device__ __forceinline__ void locate(int v, int tiles_m, int tiles_n, int &m0,
 
 // -------------------------------------------------------------------------------- the kernel --
 // Epi: a trivially copyable functor with kSym and
-//   template <class G> __device__ void run(v16f (&acc)[FI][FJ], const Where &, const Operands &, uint8_t *lds)
-// called by every wavefront once the ring is free.
+//   template <class G> __device__ void run(f32x4 (&acc)[FI][FJ], const Where &, const Operands &, uint8_t *lds)
+// called by every wavefront once the stage buffers are free.
+//
+// A stage is worked in two halves of its MFMAs. During the first, the fragments of the second are
+// read from the LDS; then nothing of the stage is left to read, and one barrier says both that its
+// buffer is free, for the loads of stage s + 2, and that stage s + 1 has landed, whose first
+// fragments are read during the second half. (16-bit: the halves are those of the row's 128
+// bytes. 8-bit: one MFMA takes a lane's part of all 128, so the halves are the upper and lower
+// rows of the wavefront's tile, and B's fragments give way to the next stage's column by column.)
 template <class E, class G, class Epi>
 __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Operands op, Epi epi)
 {
+#if defined(__HIP_DEVICE_COMPILE__)   // the buffer-resource builtins do not exist in the host's pass
     constexpr int FI = G::FI, FJ = G::FJ;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[G::template lds_bytes<E>()];
 
@@ -181,40 +194,41 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
     const int wm = w.wave % G::kWavesM, wn = w.wave / G::kWavesM;
     w.row0 = wm * G::kWaveRows;
     w.col0 = wn * G::kWaveCols;
-    const int lane = w.lane, r = lane & 31, half = lane >> 5;
+    const int lane = w.lane, r = lane & 15, q = lane >> 4;
 
-    // load u of this wavefront fills rows [16 (kDma wave + u), + 16) of the stage: lane L the 16 bytes at
-    // row L / 4, physical chunk L % 4, from the row's chunk (L % 4) ^ perm(row)
+    // load u of this wavefront fills rows [8 (kDma wave + u), + 8) of the stage: lane L the 16 bytes at
+    // row L / 8, physical chunk L % 8, from the row's chunk (L % 8) ^ perm(row)
     const uint8_t *abase = op.a + w.batch * op.batch_a + (int64_t)w.m0 * op.lda;
     const uint8_t *bbase = op.b + w.batch * op.batch_b + (int64_t)w.n0 * op.ldb;
+    const auto arsrc = __builtin_amdgcn_make_buffer_rsrc((void *)abase, 0, 0xFFFFFFFFu, 0x00027000);
+    const auto brsrc = __builtin_amdgcn_make_buffer_rsrc((void *)bbase, 0, 0xFFFFFFFFu, 0x00027000);
     const int a_row0 = kRowsPerDma * G::kDmaA * w.wave, b_row0 = kRowsPerDma * G::kDmaB * w.wave;
     uint32_t aoff[G::kDmaA], boff[G::kDmaB];
 #pragma unroll
     for (int u = 0; u < G::kDmaA; ++u) {
-        const int row = a_row0 + kRowsPerDma * u + lane / 4;
-        aoff[u] = (uint32_t)min(row, op.M - 1 - w.m0) * (uint32_t)op.lda + 16u * ((lane % 4) ^ chunk_perm(row));
+        const int row = a_row0 + kRowsPerDma * u + lane / 8;
+        aoff[u] = (uint32_t)min(row, op.M - 1 - w.m0) * (uint32_t)op.lda + 16u * ((lane % 8) ^ chunk_perm(row));
     }
 #pragma unroll
     for (int u = 0; u < G::kDmaB; ++u) {
-        const int row = b_row0 + kRowsPerDma * u + lane / 4;
-        boff[u] = (uint32_t)min(row, op.N - 1 - w.n0) * (uint32_t)op.ldb + 16u * ((lane % 4) ^ chunk_perm(row));
+        const int row = b_row0 + kRowsPerDma * u + lane / 8;
+        boff[u] = (uint32_t)min(row, op.N - 1 - w.n0) * (uint32_t)op.ldb + 16u * ((lane % 8) ^ chunk_perm(row));
     }
     const int nk = op.nk;
     auto dma = [&](int stage) {
-        // past the last stage the last one again (into a free buffer), so that every wait counts alike
-        const int64_t at = (int64_t)min(stage, nk - 1) * kRowBytes;
-        uint8_t *dst = lds + (stage & (kNumBuf - 1)) * G::kStageBytes;
+        // past the last stage the last one again, into a free buffer
+        const int at = min(stage, nk - 1) * kRowBytes;
+        uint8_t *dst = lds + (stage & 1) * G::kStageBytes;
 #pragma unroll
         for (int u = 0; u < G::kDmaA; ++u)
-            __builtin_amdgcn_global_load_lds((gbl_void_t *)(abase + at + aoff[u]),
-                                             (lds_void_t *)(dst + a_row0 * kRowBytes + u * 1024), 16, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(arsrc, (lds_void_t *)(dst + a_row0 * kRowBytes + u * 1024), 16, aoff[u],
+                                                     at, 0, 0);
 #pragma unroll
         for (int u = 0; u < G::kDmaB; ++u)
-            __builtin_amdgcn_global_load_lds((gbl_void_t *)(bbase + at + boff[u]),
-                                             (lds_void_t *)(dst + G::kABytes + b_row0 * kRowBytes + u * 1024), 16, 0,
-                                             0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(brsrc, (lds_void_t *)(dst + G::kABytes + b_row0 * kRowBytes + u * 1024),
+                                                     16, boff[u], at, 0, 0);
     };
-    // E4M3: the scales of 32 stages (16 bytes of every row) per load, wavefront w those of the tile's rows
+    // E4M3: the scales of 16 stages (16 bytes of every row) per load, wavefront w those of the tile's rows
     // [64 w, + 64) (A's first, then B's)
     const uint8_t *sbase = nullptr;
     uint32_t soff = 0;
@@ -225,7 +239,7 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
         soff = is_b ? (uint32_t)min(row, op.N - 1 - w.n0) * (uint32_t)op.ldbs
                     : (uint32_t)min(row, op.M - 1 - w.m0) * (uint32_t)op.ldas;
     }
-    const int last_group = (nk - 1) / 32;
+    const int last_group = (nk - 1) / 16;
     auto dma_scales = [&](int g) {
         __builtin_amdgcn_global_load_lds((gbl_void_t *)(sbase + (int64_t)min(g, last_group) * 16 + soff),
                                          (lds_void_t *)(lds + G::kRingBytes + (g & 1) * G::kScaleSlot + w.wave * 1024),
@@ -234,130 +248,128 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
 
     const int perm = chunk_perm(r);
     const int a_frag = (w.row0 + r) * kRowBytes, b_frag = G::kABytes + (w.col0 + r) * kRowBytes;
-    const int chunk0 = 16 * (half ^ perm), chunk1 = 16 * ((2 + half) ^ perm);
-    auto read_frags = [&](int stage, int chunk, u32x4 (&fa)[FI], u32x4 (&fb)[FJ]) {
-        const uint8_t *src = lds + (stage & (kNumBuf - 1)) * G::kStageBytes + chunk;
-#pragma unroll
-        for (int j = 0; j < FJ; ++j) fb[j] = *reinterpret_cast<const u32x4 *>(src + b_frag + 32 * j * kRowBytes);
-#pragma unroll
-        for (int i = 0; i < FI; ++i) fa[i] = *reinterpret_cast<const u32x4 *>(src + a_frag + 32 * i * kRowBytes);
-    };
-    const int sa_at = G::kRingBytes + 16 * (w.row0 + r), sb_at = G::kRingBytes + 16 * (G::kTileM + w.col0 + r);
-    auto read_scales = [&](int stage, uint32_t (&sa)[FI], uint32_t (&sb)[FJ]) {
-        const uint8_t *src = lds + ((stage >> 5) & 1) * G::kScaleSlot + ((stage >> 1) & 15);
-#pragma unroll
-        for (int i = 0; i < FI; ++i) sa[i] = src[sa_at + 512 * i];
-#pragma unroll
-        for (int j = 0; j < FJ; ++j) sb[j] = src[sb_at + 512 * j];
-    };
+    const int chunk0 = 16 * (q ^ perm), chunk1 = 16 * ((4 + q) ^ perm);
+    auto buffer = [&](int stage) { return lds + (stage & 1) * G::kStageBytes; };
+    auto read_a = [&](const uint8_t *src, int i) { return *reinterpret_cast<const u32x4 *>(src + a_frag + 16 * i * kRowBytes); };
+    auto read_b = [&](const uint8_t *src, int j) { return *reinterpret_cast<const u32x4 *>(src + b_frag + 16 * j * kRowBytes); };
 
-    v16f acc[FI][FJ];
+    f32x4 acc[FI][FJ];
 #pragma unroll
     for (int i = 0; i < FI; ++i)
 #pragma unroll
-        for (int j = 0; j < FJ; ++j) acc[i][j] = v16f{};
+        for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{};
 
     if constexpr (E::kScaled) dma_scales(0);
     dma(0);
     dma(1);
-    dma(2);
-    wait_vmcnt<2 * G::kDmaPerStage>();
+    wait_vmcnt<G::kDmaPerStage>();
     barrier();
 
     if constexpr (!E::kScaled) {
         u32x4 fa0[FI], fb0[FJ], fa1[FI], fb1[FJ];
-        read_frags(0, chunk0, fa0, fb0);
+        auto read = [&](const uint8_t *src, u32x4 (&fa)[FI], u32x4 (&fb)[FJ]) {
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) fb[j] = read_b(src, j);
+#pragma unroll
+            for (int i = 0; i < FI; ++i) fa[i] = read_a(src, i);
+        };
         auto mfmas = [&](const u32x4 (&fa)[FI], const u32x4 (&fb)[FJ]) {
 #pragma unroll
             for (int i = 0; i < FI; ++i)
 #pragma unroll
                 for (int j = 0; j < FJ; ++j) E::mfma(acc[i][j], fb[j], fa[i]);
         };
-        constexpr int kMfma = FI * FJ, kReads = FI + FJ;
+        read(buffer(0) + chunk0, fa0, fb0);
+        constexpr int kMfma = FI * FJ, kReads = FI + FJ, kLoads = G::kDmaPerStage;
+        constexpr int kPer = kMfma / kReads;   // MFMAs per read in the first half
         for (int s = 0; s < nk; ++s) {
-            // first half of the stage: the second half's fragments are read between the MFMAs
-            read_frags(s, chunk1, fa1, fb1);
+            read(buffer(s) + chunk1, fa1, fb1);
             mfmas(fa0, fb0);
-            constexpr int lead0 = (kReads + 1) / 2;
 #pragma unroll
-            for (int k = 0; k < lead0; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // DS read
+            for (int k = 0; k < kReads; ++k) {
+                __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);  // MFMA
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // DS read
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, kMfma - lead0, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, kMfma - kPer * kReads, 0);
             __builtin_amdgcn_sched_barrier(0);
-            // stage s + 1 has landed for every wavefront (only stage s + 2's loads are younger), and
-            // stage s - 1's buffer, which stage s + 3 overwrites, has been read by all
-            wait_vmcnt<G::kDmaPerStage>();
+            __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the stage has been read
+            wait_vmcnt<0>();                      // stage s + 1 has landed
             barrier();
-            dma(s + 3);
-            read_frags(s + 1, chunk0, fa0, fb0);
+            dma(s + 2);
+            read(buffer(s + 1) + chunk0, fa0, fb0);
             mfmas(fa1, fb1);
-            constexpr int lv = (G::kDmaPerStage + 1) / 2;
-            constexpr int lead1 = lv + lead0 < kMfma ? lv + lead0 : kMfma;
+            // the loads at once: they have the longest way to go
+            constexpr int kBoth = kLoads + kReads <= kMfma ? 1 : 2;
 #pragma unroll
-            for (int k = 0; k < lv; ++k) {
+            for (int k = 0; k < kLoads / kBoth; ++k) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);  // VMEM read
+                __builtin_amdgcn_sched_group_barrier(0x020, kBoth, 0);  // VMEM read
             }
 #pragma unroll
-            for (int k = 0; k < lead0; ++k) {
+            for (int k = 0; k < kReads / kBoth; ++k) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, kBoth, 0);
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, kMfma - lead1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, kMfma - (kLoads + kReads) / kBoth, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     } else {
-        u32x4 fa0[FI], fb0[FJ], fa1[FI], fb1[FJ];
+        constexpr int H = FI / 2;
+        u32x4 fa[FI][2], fb[FJ][2];
         uint32_t sa[FI], sb[FJ];
-        read_frags(0, chunk0, fa0, fb0);
-        read_frags(0, chunk1, fa1, fb1);
-        read_scales(0, sa, sb);
+        const int sa_at = G::kRingBytes + 16 * (w.row0 + r), sb_at = G::kRingBytes + 16 * (G::kTileM + w.col0 + r);
+        auto scales = [&](int stage) { return lds + ((stage >> 4) & 1) * G::kScaleSlot + (stage & 15); };
+        auto take_a = [&](int stage, int i) {
+            fa[i][0] = read_a(buffer(stage) + chunk0, i);
+            fa[i][1] = read_a(buffer(stage) + chunk1, i);
+            sa[i] = scales(stage)[sa_at + 256 * i];
+        };
+        auto take_b = [&](int stage, int j) {
+            fb[j][0] = read_b(buffer(stage) + chunk0, j);
+            fb[j][1] = read_b(buffer(stage) + chunk1, j);
+            sb[j] = scales(stage)[sb_at + 256 * j];
+        };
+        auto mfma = [&](int i, int j) { E::mfma(acc[i][j], fb[j][0], fb[j][1], fa[i][0], fa[i][1], sb[j], sa[i]); };
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) take_b(0, j);
+#pragma unroll
+        for (int i = 0; i < H; ++i) take_a(0, i);
         for (int s = 0; s < nk; ++s) {
-            // stage s + 1 has landed for every wavefront, and stage s - 1's buffer is free
-            wait_vmcnt<G::kDmaPerStage>();
+            // the upper rows; the lower rows' fragments are read behind each group of MFMAs
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                take_a(s, H + i);
+#pragma unroll
+                for (int j = 0; j < FJ; ++j) mfma(i, j);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, FJ - 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+            wait_vmcnt<0>();
             barrier();
-            // before the stage's own loads, so that the next wait covers them
-            if ((s & 31) == 0) dma_scales((s >> 5) + 1);
-            dma(s + 3);
-            u32x4 ga0[FI], gb0[FJ], ga1[FI], gb1[FJ];
-            uint32_t ta[FI], tb[FJ];
-            const uint8_t *src = lds + ((s + 1) & (kNumBuf - 1)) * G::kStageBytes;
-            // MFMAs row by row; row i's fragments are replaced by the next stage's behind them
+            if ((s & 15) == 0) dma_scales((s >> 4) + 1);
+            dma(s + 2);
+            // the lower rows column by column; column j's fragments and those of upper row j follow it
 #pragma unroll
             for (int j = 0; j < FJ; ++j) {
-                gb0[j] = *reinterpret_cast<const u32x4 *>(src + chunk0 + b_frag + 32 * j * kRowBytes);
-                gb1[j] = *reinterpret_cast<const u32x4 *>(src + chunk1 + b_frag + 32 * j * kRowBytes);
-            }
-            read_scales(s + 1, ta, tb);
 #pragma unroll
-            for (int i = 0; i < FI; ++i) {
-#pragma unroll
-                for (int j = 0; j < FJ; ++j) E::mfma(acc[i][j], fb0[j], fb1[j], fa0[i], fa1[i], sb[j], sa[i]);
+                for (int i = 0; i < H; ++i) mfma(H + i, j);
                 __builtin_amdgcn_sched_barrier(0);
-                ga0[i] = *reinterpret_cast<const u32x4 *>(src + chunk0 + a_frag + 32 * i * kRowBytes);
-                ga1[i] = *reinterpret_cast<const u32x4 *>(src + chunk1 + a_frag + 32 * i * kRowBytes);
+                take_b(s + 1, j);
+                if (j < H) take_a(s + 1, j);
             }
-#pragma unroll
-            for (int i = 0; i < FI; ++i) {
-                fa0[i] = ga0[i];
-                fa1[i] = ga1[i];
-                sa[i] = ta[i];
-            }
-#pragma unroll
-            for (int j = 0; j < FJ; ++j) {
-                fb0[j] = gb0[j];
-                fb1[j] = gb1[j];
-                sb[j] = tb[j];
-            }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        static_assert(H <= FJ, "an upper row for each column");
     }
-    // the ring is free for the epilogue: every load has landed and every wavefront is past its reads
+    // the stage buffers are free for the epilogue: every load has landed and every wavefront is past its reads
     wait_vmcnt<0>();
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     barrier();
     epi.template run<G>(acc, w, op, lds);
+#endif
 }
 
 // ------------------------------------------------------------------------- plain epilogue -----
@@ -375,7 +387,7 @@ __device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_fl
 
 // c = alpha * A B^T + beta * c (+ add) in FP32 or bf16 (rounded once, after the sums); c is read only when
 // beta != 0, add (FP32 [M][ld_add], 16-byte aligned rows, readable up to a multiple of 4 columns) only
-// when it is not NULL.
+// when it is not NULL. factors: NULL, or two powers of two in device memory that alpha is multiplied by.
 template <bool BF16_OUT>
 struct StoreEpi {
     static constexpr bool kSym = false;
@@ -384,32 +396,41 @@ struct StoreEpi {
     float alpha, beta;
     const float *add = nullptr;
     int64_t ld_add = 0;
+    const float *factors = nullptr;
 
     template <class G>
-    __device__ __forceinline__ void run(v16f (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
     {
-        const int r = w.lane & 31, half = w.lane >> 5;
+        run_with<G>(w, op, lds, [&](int i, int j) { return acc[i][j]; });
+    }
+
+    // val(i, j): what takes the place of acc[i][j]
+    template <class G, class Val>
+    __device__ __forceinline__ void run_with(const Where &w, const Operands &op, uint8_t *lds, Val val) const
+    {
+        const int r = w.lane & 15, q = w.lane >> 4;
         uint8_t *epi = lds + w.wave * G::kEpiWave;
         constexpr int kLanesPerRow = G::kWaveCols / 4, kRowsPerStore = 64 / kLanesPerRow;
         constexpr int kElem = BF16_OUT ? 2 : 4;
         const bool vec = ldc % 4 == 0 && (uintptr_t)c % (4 * kElem) == 0 && (batch_c % 4 == 0 || w.batch == 0);
         const int cc = 4 * (w.lane % kLanesPerRow);
+        // one after the other: their product may leave FP32's range where the result does not
+        const float f0 = factors ? alpha * factors[0] : alpha, f1 = factors ? factors[1] : 1.0f;
         const int n = w.n0 + w.col0 + cc;
 #pragma unroll
-        for (int i = 0; i < G::FI; ++i) {
+        for (int i = 0; i < G::FI; i += 2) {
             // 32 rows of the wavefront's columns through the LDS (its own part of it: no barrier),
             // so that a store instruction writes whole rows
 #pragma unroll
-            for (int j = 0; j < G::FJ; ++j)
+            for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<f32x4 *>(epi + r * G::kEpiRow + (32 * j + 8 * q + 4 * half) * 4) =
-                        f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                for (int j = 0; j < G::FJ; ++j)
+                    *reinterpret_cast<f32x4 *>(epi + (16 * ii + r) * G::kEpiRow + (16 * j + 4 * q) * 4) = val(i + ii, j);
 #pragma unroll
             for (int p = 0; p < 32 / kRowsPerStore; ++p) {
                 const int rr = kRowsPerStore * p + w.lane / kLanesPerRow;
-                f32x4 v = *reinterpret_cast<const f32x4 *>(epi + rr * G::kEpiRow + cc * 4) * alpha;
-                const int m = w.m0 + w.row0 + 32 * i + rr;
+                f32x4 v = *reinterpret_cast<const f32x4 *>(epi + rr * G::kEpiRow + cc * 4) * f0 * f1;
+                const int m = w.m0 + w.row0 + 16 * i + rr;
                 if (m < op.M && n < op.N && add) v += *reinterpret_cast<const f32x4 *>(add + (int64_t)m * ld_add + n);
                 if (m < op.M && n < op.N) put(w.batch * batch_c + (int64_t)m * ldc + n, v, vec && n + 4 <= op.N, op.N - n);
             }
@@ -452,46 +473,44 @@ struct StoreEpi {
 // ------------------------------------------------------------------- 16-bit tiles, two ways ---
 // Writes the wavefront's part of the tile as 16-bit values, row-major at rows[m][ld_rows] and (cols !=
 // nullptr) transposed at cols[n][ld_cols], m and n counted from the matrix' origin; every element of
-// the tile has its place in both. PACK makes two values one word; val(i, j, q) gives the four
-// values of registers 4 q .. 4 q + 3 of acc[i][j]. 64 x 64 blocks pass through the LDS in both
-// orientations, 8 KB each, so that a store instruction writes whole 128-byte lines of either. For
-// the transposed block a lane swaps two of its four columns against its neighbour's row, so that
-// it holds two rows of two columns and writes words.
+// the tile has its place in both. pack makes two values one word; val(i, j) gives the four
+// values of acc[i][j]. 64 x 64 blocks pass through the LDS in both orientations, 8 KB each, so that
+// a store instruction writes whole 128-byte lines of either. For the transposed block a lane
+// swaps two of its four columns against its neighbour's row, so that it holds two rows of two
+// columns and writes words.
 template <class G, class Pack, class Val>
 __device__ __forceinline__ void store_tile16(const Where &w, uint8_t *lds, Pack pack, Val val, uint16_t *rows, int64_t ld_rows,
                                              uint16_t *cols, int64_t ld_cols)
 {
-    static_assert(G::FJ == 2 && G::FI % 2 == 0, "64 x 64 blocks");
+    static_assert(G::FJ == 4 && G::FI % 4 == 0, "64 x 64 blocks");
     static_assert(G::NW * 16384 <= G::kRingBytes, "two staged blocks per wavefront");
-    const int r = w.lane & 31, half = w.lane >> 5;
+    const int r = w.lane & 15, q = w.lane >> 4;
     const bool odd = r & 1;
     uint8_t *tile = lds + w.wave * 16384, *turned = tile + 8192;
 #pragma unroll
-    for (int blk = 0; blk < G::FI / 2; ++blk) {
+    for (int blk = 0; blk < G::FI / 4; ++blk) {
 #pragma unroll
-        for (int ii = 0; ii < 2; ++ii)
+        for (int ii = 0; ii < 4; ++ii)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x4 v = val(2 * blk + ii, j, q);
-                    const uint32_t lo = pack(v[0], v[1]), hi = pack(v[2], v[3]);
-                    const int row = 32 * ii + r, col = 32 * j + 8 * q + 4 * half;
-                    *reinterpret_cast<u32x2 *>(tile + row * 128 + 16 * ((col >> 3) ^ ((row >> 1) & 7)) + 8 * half) =
-                        u32x2{lo, hi};
-                    if (cols) {
-                        const uint32_t give = odd ? lo : hi;
-                        const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
-                        // even lanes: columns 0, 1 of rows r, r + 1; odd lanes: columns 2, 3 of rows r - 1, r
-                        const uint32_t up = odd ? got : lo, dn = odd ? hi : got;   // the upper and the lower row's pair
-                        const uint32_t c0 = __builtin_amdgcn_perm(dn, up, 0x05040100u);
-                        const uint32_t c1 = __builtin_amdgcn_perm(dn, up, 0x07060302u);
-                        const int c = col + (odd ? 2 : 0), at = 2 * (row & ~1);
-                        *reinterpret_cast<uint32_t *>(turned + c * 128 + ((at & 15) | (((at >> 4) ^ ((c >> 1) & 7)) << 4))) = c0;
-                        *reinterpret_cast<uint32_t *>(turned + (c + 1) * 128 +
-                                                      ((at & 15) | (((at >> 4) ^ ((c >> 1) & 7)) << 4))) = c1;
-                    }
+            for (int j = 0; j < 4; ++j) {
+                const f32x4 v = val(4 * blk + ii, j);
+                const uint32_t lo = pack(v[0], v[1]), hi = pack(v[2], v[3]);
+                const int row = 16 * ii + r, col = 16 * j + 4 * q;
+                *reinterpret_cast<u32x2 *>(tile + row * 128 + 16 * ((col >> 3) ^ ((row >> 1) & 7)) + 8 * (q & 1)) =
+                    u32x2{lo, hi};
+                if (cols) {
+                    const uint32_t give = odd ? lo : hi;
+                    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
+                    // even lanes: columns 0, 1 of rows r, r + 1; odd lanes: columns 2, 3 of rows r - 1, r
+                    const uint32_t up = odd ? got : lo, dn = odd ? hi : got;   // the upper and the lower row's pair
+                    const uint32_t c0 = __builtin_amdgcn_perm(dn, up, 0x05040100u);
+                    const uint32_t c1 = __builtin_amdgcn_perm(dn, up, 0x07060302u);
+                    const int c = col + (odd ? 2 : 0), at = 2 * (row & ~1);
+                    const int swizzled = (at & 15) | (((at >> 4) ^ ((c >> 1) & 7)) << 4);   // c and c + 1 alike: c is even
+                    *reinterpret_cast<uint32_t *>(turned + c * 128 + swizzled) = c0;
+                    *reinterpret_cast<uint32_t *>(turned + (c + 1) * 128 + swizzled) = c1;
                 }
+            }
         const int64_t m = w.m0 + w.row0 + 64 * blk, n = w.n0 + w.col0;
 #pragma unroll
         for (int p = 0; p < 8; ++p) {

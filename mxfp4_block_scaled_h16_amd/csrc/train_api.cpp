@@ -122,7 +122,7 @@ mxfp4_status_t check_xent(const void *x, int64_t ldx, const void *w, int64_t ldw
     if (T == 0) return MXFP4_OK;
     if (!x || !w || !target) return MXFP4_ERR_NULL;
     if (!aligned(x, 2) || !aligned(w, 2) || !aligned(target, 8)) return MXFP4_ERR_ALIGN;
-    if (K % 32 == 0 && (!aligned(x, 16) || !aligned(w, 16) || ldx % 8 != 0 || ldw % 8 != 0)) return MXFP4_ERR_ALIGN;
+    if (K % 64 == 0 && (!aligned(x, 16) || !aligned(w, 16) || ldx % 8 != 0 || ldw % 8 != 0)) return MXFP4_ERR_ALIGN;
     return MXFP4_OK;
 }
 

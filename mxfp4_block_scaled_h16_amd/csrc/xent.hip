@@ -5,8 +5,10 @@
 //
 // Forward: one product whose epilogue leaves a maximum and a sum of exponentials per row and
 // column tile, and a kernel that joins them. Backward: for each piece of the vocabulary the logits
-// are formed again and leave the product's epilogue as G, in bf16 and in both orientations; dX
-// adds up over the pieces in FP32, dW's rows of the piece are written once.
+// are formed again and leave the product's epilogue as G, in FP16 (scaled to its range) and in both
+// orientations; dX = G W adds up over the pieces in FP32, dW = G^T X has its rows of the piece written
+// once. The second operands of these are FP16 copies of W's piece and of X, transposed, so that every
+// product contracts along rows.
 #include "mx_device.h"
 #include "slab_gemm.h"
 #include "train_internal.h"
@@ -22,9 +24,9 @@ __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_ex
 
 // ------------------------------------------------------------------------ the loss' product ---
 // Per row of the tile: the largest z and the sum of exp(z - largest) over the tile's columns
-// (statistics in base 2, times log2 e), and the target's z where the tile holds it. A lane holds 32
-// columns of a row per 32-row tile, its partner in the other half-wave the other 32 of the
-// wavefront's 64; the wavefronts of a row join through the LDS.
+// (statistics in base 2, times log2 e), and the target's z where the tile holds it. A lane holds 16
+// columns of a row per 16-row tile, the lanes 16, 32 and 48 further the others of the wavefront's 64;
+// the wavefronts of a row join through the LDS.
 struct StatsEpi {
     static constexpr bool kSym = false;
     float2 *part;            // [tiles_n][T]
@@ -32,18 +34,18 @@ struct StatsEpi {
     const int64_t *target;
 
     template <class G>
-    __device__ __forceinline__ void run(v16f (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
     {
-        const int r = w.lane & 31, half = w.lane >> 5;
+        const int r = w.lane & 15, q = w.lane >> 4;
         float2 *slots = reinterpret_cast<float2 *>(lds);   // [wave column][row of the tile]
         const int wn = w.wave / G::kWavesM;
-        const int nleft = op.N - (w.n0 + w.col0 + 4 * half);   // valid: 32 j + 8 q + t < nleft
+        const int nleft = op.N - (w.n0 + w.col0 + 4 * q);   // valid: 16 j + t < nleft
 #pragma unroll
         for (int i = 0; i < G::FI; ++i) {
-            const int row = w.row0 + 32 * i + r;
+            const int row = w.row0 + 16 * i + r;
             const int m = min(w.m0 + row, op.M - 1);
             // the target's place among this lane's columns; far outside when it is not an index
-            const int64_t tc = target[m] - (w.n0 + w.col0 + 4 * half);
+            const int64_t tc = target[m] - (w.n0 + w.col0 + 4 * q);
             const int want = tc >= 0 && tc < 64 ? (int)tc : -1;
             float top = -INFINITY;
             float hit = 0.0f;
@@ -51,27 +53,29 @@ struct StatsEpi {
 #pragma unroll
             for (int j = 0; j < G::FJ; ++j)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int c = 32 * j + 8 * (e / 4) + (e % 4);
-                    float z = acc[i][j][e];
+                for (int t = 0; t < 4; ++t) {
+                    const int c = 16 * j + t;
+                    float z = acc[i][j][t];
                     if (c == want) {
                         hit = z;
                         found = true;
                     }
                     z = c < nleft ? z * kLog2e : -INFINITY;
-                    acc[i][j][e] = z;
+                    acc[i][j][t] = z;
                     top = fmaxf(top, z);
                 }
             if (found && w.m0 + row < op.M && want < nleft) zt[m] = hit;
+            top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             const float ref = top == -INFINITY ? 0.0f : top;
             float sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < G::FJ; ++j)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) sum += fast_exp2(acc[i][j][e] - ref);
+                for (int t = 0; t < 4; ++t) sum += fast_exp2(acc[i][j][t] - ref);
+            sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            if (half == 0) slots[wn * G::kTileM + row] = make_float2(top, sum);
+            if (q == 0) slots[wn * G::kTileM + row] = make_float2(top, sum);
         }
         __syncthreads();
         for (int row = threadIdx.x; row < G::kTileM; row += 64 * G::NW) {
@@ -117,87 +121,203 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const float2 *__restrict
 }
 
 // -------------------------------------------------------------------- the gradient's product --
-// G of the tile in bf16 (one rounding: the products that read it take bf16), zero in rows past T, in
-// columns past V and in rows whose target is ignored or no index (their dlse still counts: lse is
-// an output of every row).
-struct GradEpi {
-    static constexpr bool kSym = false;
-    const float *dloss, *dlse, *lse;
-    const int64_t *target;
-    int64_t ignore_index, V, v0;   // the piece's first column
-    uint16_t *g, *gt;              // [Tp][ldg], [Vc][ldt]
-    int64_t ldg, ldt;
-
-    template <class G>
-    __device__ __forceinline__ void run(v16f (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
-    {
-        const int r = w.lane & 31, half = w.lane >> 5;
-        const int nbase = w.n0 + w.col0 + 4 * half;
-        const int nleft = op.N - nbase;
-#pragma unroll
-        for (int i = 0; i < G::FI; ++i) {
-            const int m = w.m0 + w.row0 + 32 * i + r;
-            const bool live = m < op.M;
-            const int mm = live ? m : op.M - 1;
-            const int64_t tg = target[mm];
-            const bool counts = live && tg != ignore_index && tg >= 0 && tg < V;
-            const float dl = counts && dloss ? dloss[mm] : 0.0f;
-            const float dp = dl + (live && dlse ? dlse[mm] : 0.0f);
-            const float ref = lse[mm] * kLog2e;
-            const int64_t tc = tg - v0 - nbase;
-            const int want = counts && tc >= 0 && tc < 64 ? (int)tc : -1;
-#pragma unroll
-            for (int j = 0; j < G::FJ; ++j)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int c = 32 * j + 8 * (e / 4) + (e % 4);
-                    float v = fast_exp2(fmaf(acc[i][j][e], kLog2e, -ref)) * dp;
-                    if (c == want) v -= dl;
-                    // dp == 0: the row's gradient is zero whatever its logits are
-                    acc[i][j][e] = c < nleft && dp != 0.0f ? v : (c == want ? -dl : 0.0f);
-                }
-        }
-        store_tile16<G>(w, lds, [](float a, float b) { return pack_bf16(a, b); },
-                        [&](int i, int j, int q) {
-                            return f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                        },
-                        g, ldg, gt, ldt);
-    }
+// How far the FP16 operands of the gradients' products are scaled: powers of two that bring the
+// largest |G|, |X| and |W| to [2^14, 2^15), and their reciprocals.
+struct Ranges {
+    float g, x, w;
+    float inv_gw[2], inv_gx[2];   // 1 / g, 1 / w and 1 / g, 1 / x
 };
 
-// ------------------------------------------------------------------------------- copies -------
+// 2^k with 2^14 <= 2^k top < 2^15, k within [-120, 120]; 1 for zero and for what is not finite
+__device__ __forceinline__ float range_scale(float top)
+{
+    const uint32_t bits = __float_as_uint(top);
+    if (bits == 0u || bits >= 0x7F800000u) return 1.0f;
+    const int k = 14 - ((int)(bits >> 23) - 127);   // a subnormal top counts as 2^-127
+    return __uint_as_float((uint32_t)(127 + max(-120, min(120, k))) << 23);
+}
+
 // Which rows of X add something to the gradients: the others are taken as zeros in the transposed
 // copy, so that what a padded position holds (a NaN) meets no zero of G.
 struct RowWeights {
     const float *dloss, *dlse;   // NULL: zeros
     const int64_t *target;       // NULL: every row counts
     int64_t ignore_index, V;
+    // the gradients of the row's loss and of the row's exponentials
+    __device__ __forceinline__ void of(int64_t t, float &dl, float &dp) const
+    {
+        const int64_t tg = target[t];
+        dl = dloss && tg != ignore_index && tg >= 0 && tg < V ? dloss[t] : 0.0f;
+        dp = dl + (dlse ? dlse[t] : 0.0f);
+    }
     __device__ __forceinline__ bool live(int64_t t) const
     {
         if (!target) return true;
-        const int64_t tg = target[t];
-        return (dlse && dlse[t] != 0.0f) || (dloss && tg != ignore_index && tg >= 0 && tg < V && dloss[t] != 0.0f);
+        float dl, dp;
+        of(t, dl, dp);
+        return dl != 0.0f || dp != 0.0f;
     }
 };
 
-// out[c][r] = in[r][c] (16-bit), r < rows, c < cols; zero for rows <= r < rows_padded
-__global__ __launch_bounds__(256) void transpose16_kernel(const uint16_t *__restrict__ in, int64_t ld_in, int64_t rows,
-                                                          int64_t cols, uint16_t *__restrict__ out, int64_t ld_out,
-                                                          int64_t rows_padded, RowWeights weights)
-{
-    __shared__ uint16_t tile[64][64 + 2];
-    const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+// G of the tile, scaled to FP16's range and rounded to it once (11 bits: an eighth of what a bf16 result
+// loses in its own rounding), zero in rows past T and in columns past V.
+struct GradEpi {
+    static constexpr bool kSym = false;
+    RowWeights weights;
+    const float *lse;
+    int64_t v0;                    // the piece's first column
+    const Ranges *ranges;
+    uint16_t *g, *gt;              // [Tp][ldg], [Vc][ldt]
+    int64_t ldg, ldt;
+
+    template <class G>
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
+    {
+        const int r = w.lane & 15, q = w.lane >> 4;
+        const int nbase = w.n0 + w.col0 + 4 * q;
+        const int nleft = op.N - nbase;
+        const float scale = ranges->g;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        const int64_t r = r0 + ty + 4 * k, c = c0 + tx;
-        tile[ty + 4 * k][tx] = r < rows && c < cols && weights.live(r) ? in[r * ld_in + c] : (uint16_t)0;
+        for (int i = 0; i < G::FI; ++i) {
+            const int m = w.m0 + w.row0 + 16 * i + r;
+            const bool live = m < op.M;
+            const int mm = live ? m : op.M - 1;
+            float dl, dp;
+            weights.of(mm, dl, dp);
+            dl = live ? dl * scale : 0.0f;
+            dp = live ? dp * scale : 0.0f;
+            const float ref = lse[mm] * kLog2e;
+            const int64_t tc = weights.target[mm] - v0 - nbase;
+            const int want = dl != 0.0f && tc >= 0 && tc < 64 ? (int)tc : -1;
+#pragma unroll
+            for (int j = 0; j < G::FJ; ++j)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const int c = 16 * j + t;
+                    float v = fast_exp2(fmaf(acc[i][j][t], kLog2e, -ref)) * dp;
+                    // dp == 0: nothing of the exponentials counts, whatever they are
+                    v = c < nleft && dp != 0.0f ? v : 0.0f;
+                    acc[i][j][t] = c == want ? v - dl : v;
+                }
+        }
+        store_tile16<G>(w, lds, [](float a, float b) { return pack_f16(a, b); }, [&](int i, int j) { return acc[i][j]; }, g, ldg,
+                        gt, ldt);
+    }
+};
+
+// ---------------------------------------------------------------------------- ranges ----------
+constexpr int kRangeBlocks = 256;   // partial maxima of each of the three
+
+__device__ __forceinline__ float block_max(float v)
+{
+    __shared__ float slots[4];
+    for (int k = 32; k >= 1; k >>= 1) v = fmaxf(v, __shfl_xor(v, k));
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return fmaxf(fmaxf(slots[0], slots[1]), fmaxf(slots[2], slots[3]));
+}
+
+// largest |value| of a bf16 matrix over this workgroup's rows; a NaN or infinity counts as infinity
+__device__ __forceinline__ float rows_max(const uint16_t *p, int64_t ld, int64_t rows, int64_t cols, int64_t block, int64_t blocks,
+                                          bool vec, const RowWeights &weights)
+{
+    uint32_t top = 0;
+    if (vec) {   // 16-byte aligned rows of whole 16 bytes: a wavefront's lanes read consecutive ones
+        const int64_t per_row = cols / 8, total = rows * per_row;
+        for (int64_t i = block * 256 + threadIdx.x; i < total; i += blocks * 256) {
+            const int64_t row = i / per_row;
+            if (!weights.live(row)) continue;
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(p + row * ld + (i - row * per_row) * 8);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(max(top, v[e] & 0x7FFFu), (v[e] >> 16) & 0x7FFFu);
+        }
+    } else {
+        for (int64_t i = block * 256 + threadIdx.x; i < rows * cols; i += blocks * 256) {
+            const int64_t row = i / cols;
+            if (weights.live(row)) top = max(top, (uint32_t)p[row * ld + i - row * cols] & 0x7FFFu);
+        }
+    }
+    return __uint_as_float(min(top, 0x7F80u) << 16);
+}
+
+// part[0 ..]: the largest |dloss| + |dloss + dlse|, part[kRangeBlocks ..]: |X| in live rows, then |W|
+__global__ __launch_bounds__(256) void range_kernel(const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw, int64_t T,
+                                                    int64_t K, int64_t V, int vec, RowWeights weights, float *part)
+{
+    const int64_t b = blockIdx.x;
+    float top = 0.0f;
+    for (int64_t t = b * 256 + threadIdx.x; t < T; t += (int64_t)gridDim.x * 256) {
+        float dl, dp;
+        weights.of(t, dl, dp);
+        top = fmaxf(top, fabsf(dl) + fabsf(dp));
+    }
+    top = block_max(top);
+    if (threadIdx.x == 0) part[b] = top;
+    __syncthreads();
+    top = block_max(rows_max(x, ldx, T, K, b, gridDim.x, vec, weights));
+    if (threadIdx.x == 0) part[kRangeBlocks + b] = top;
+    __syncthreads();
+    top = block_max(rows_max(w, ldw, V, K, b, gridDim.x, vec, RowWeights{}));
+    if (threadIdx.x == 0) part[2 * kRangeBlocks + b] = top;
+}
+
+__global__ __launch_bounds__(256) void join_ranges_kernel(const float *part, int blocks, Ranges *out)
+{
+    float s[3];
+    for (int k = 0; k < 3; ++k) {
+        s[k] = range_scale(block_max((int)threadIdx.x < blocks ? part[k * kRangeBlocks + threadIdx.x] : 0.0f));
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) *out = Ranges{s[0], s[1], s[2], {1.0f / s[0], 1.0f / s[2]}, {1.0f / s[0], 1.0f / s[1]}};
+}
+
+// ------------------------------------------------------------------------------- copies -------
+// out[c][r] = in[r][c] * *scale, bf16 to FP16; r < rows (zero for rows up to rows_padded, a multiple of
+// 64, and for rows that add nothing), c < cols. 128 x 128 tiles: a thread transposes 8 x 8 values in
+// registers, then 256-byte lines are put together in the LDS. Bound by memory: 2 bytes in, 2 out.
+__global__ __launch_bounds__(256) void turn_kernel(const uint16_t *__restrict__ in, int64_t ld_in, int64_t rows, int64_t cols,
+                                                   int vec, const float *__restrict__ scale, uint16_t *__restrict__ out,
+                                                   int64_t ld_out, int64_t rows_padded, RowWeights weights)
+{
+    __shared__ __attribute__((aligned(16))) uint16_t tile[128 * 128];   // [column][row], 16-byte pieces permuted
+    const int64_t r0 = (int64_t)blockIdx.x * 128, c0 = (int64_t)blockIdx.y * 128;
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+    const float s = *scale;
+    u32x4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + 8 * rg + i, c = c0 + 8 * cg;
+        v[i] = u32x4{0u, 0u, 0u, 0u};
+        if (r < rows && weights.live(r)) {
+            const uint16_t *p = in + r * ld_in + c;
+            if (vec && c + 8 <= cols) {
+                v[i] = *reinterpret_cast<const u32x4 *>(p);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < cols) v[i][e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        u32x4 o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t a = v[2 * k][e / 2], b = v[2 * k + 1][e / 2];
+            o[k] = e & 1 ? pack_f16(bf16_hi(a) * s, bf16_hi(b) * s) : pack_f16(bf16_lo(a) * s, bf16_lo(b) * s);
+        }
+        const int c = 8 * cg + e;
+        *reinterpret_cast<u32x4 *>(tile + c * 128 + 8 * (rg ^ (cg & 15))) = o;
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        const int64_t c = c0 + ty + 4 * k, r = r0 + tx;
-        if (c < cols && r < rows_padded) out[c * ld_out + r] = tile[tx][ty + 4 * k];
+    for (int p = 0; p < 8; ++p) {
+        const int c = 16 * p + (threadIdx.x >> 4), piece = threadIdx.x & 15;
+        const int64_t oc = c0 + c, r = r0 + 8 * piece;
+        if (oc < cols && r < rows_padded)
+            *reinterpret_cast<u32x4 *>(out + oc * ld_out + r) =
+                *reinterpret_cast<const u32x4 *>(tile + c * 128 + 8 * (piece ^ ((c >> 3) & 15)));
     }
 }
 
@@ -212,11 +332,12 @@ __global__ __launch_bounds__(256) void pad16_kernel(const uint16_t *__restrict__
     }
 }
 
-hipError_t transpose16(const void *in, int64_t ld_in, int64_t rows, int64_t cols, uint16_t *out, int64_t ld_out,
-                       int64_t rows_padded, const RowWeights &weights, hipStream_t stream)
+hipError_t turn(const void *in, int64_t ld_in, int64_t rows, int64_t cols, const float *scale, uint16_t *out, int64_t ld_out,
+                int64_t rows_padded, const RowWeights &weights, hipStream_t stream)
 {
-    return launch(transpose16_kernel, dim3((unsigned)((rows_padded + 63) / 64), (unsigned)((cols + 63) / 64)), dim3(256), 0,
-                  stream, static_cast<const uint16_t *>(in), ld_in, rows, cols, out, ld_out, rows_padded, weights);
+    const int vec = (uintptr_t)in % 16 == 0 && ld_in % 8 == 0;
+    return launch(turn_kernel, dim3((unsigned)((rows_padded + 127) / 128), (unsigned)((cols + 127) / 128)), dim3(256), 0, stream,
+                  static_cast<const uint16_t *>(in), ld_in, rows, cols, vec, scale, out, ld_out, rows_padded, weights);
 }
 
 // ------------------------------------------------------------------------------ workspace -----
@@ -246,17 +367,19 @@ struct Carve {
 };
 
 struct Layout {
-    uint16_t *xp, *wp;   // copies of X and W with rows padded to whole stages (K % 32 != 0)
+    uint16_t *xp, *wp;   // copies of X and W with rows padded to whole stages (K % 64 != 0)
     float2 *part;
     float *zt;
+    float *range_part;
+    Ranges *ranges;
     uint16_t *xt, *wt, *g, *gt;
     float *dx;
 };
 Layout carve(Carve &c, int64_t T, int64_t K, int64_t V, bool backward)
 {
     Layout l{};
-    const int64_t kp = round_up(K, 32);
-    if (K % 32 != 0) {
+    const int64_t kp = round_up(K, 64);
+    if (K % 64 != 0) {
         l.xp = static_cast<uint16_t *>(c.take(2 * T * kp));
         l.wp = static_cast<uint16_t *>(c.take(2 * V * kp));
     }
@@ -266,6 +389,8 @@ Layout carve(Carve &c, int64_t T, int64_t K, int64_t V, bool backward)
         return l;
     }
     const int64_t tp = round_up(T, 256), vc = piece_columns(T, V);
+    l.range_part = static_cast<float *>(c.take(4 * 3 * kRangeBlocks));
+    l.ranges = static_cast<Ranges *>(c.take(sizeof(Ranges)));
     l.xt = static_cast<uint16_t *>(c.take(2 * K * tp));
     l.wt = static_cast<uint16_t *>(c.take(2 * K * vc));
     l.g = static_cast<uint16_t *>(c.take(2 * tp * vc));
@@ -284,14 +409,14 @@ hipError_t pad16(const void *in, int64_t ld_in, int64_t rows, int64_t cols, uint
 // X and W as operands of the logits' product (padded copies in ws where needed)
 hipError_t logits_operands(const XentProblem &p, const Layout &l, Operands &op, hipStream_t stream)
 {
-    const int64_t kp = round_up(p.K, 32);
-    op.nk = (int)(kp / 32);
+    const int64_t kp = round_up(p.K, 64);
+    op.nk = (int)(kp / 64);
     op.M = (int)p.T;
     op.a = static_cast<const uint8_t *>(p.x);
     op.lda = 2 * p.ldx;
     op.b = static_cast<const uint8_t *>(p.w);
     op.ldb = 2 * p.ldw;
-    if (p.K % 32 != 0) {
+    if (p.K % 64 != 0) {
         if (hipError_t e = pad16(p.x, p.ldx, p.T, p.K, l.xp, kp, stream)) return e;
         if (hipError_t e = pad16(p.w, p.ldw, p.V, p.K, l.wp, kp, stream)) return e;
         op.a = reinterpret_cast<const uint8_t *>(l.xp);
@@ -340,10 +465,16 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
     const int64_t tp = round_up(p.T, 256), vc = piece_columns(p.T, p.V);
     Operands lo{};
     if (hipError_t e = logits_operands(p, l, lo, stream)) return e;
+    const RowWeights weights{dloss, dlse, p.target, p.ignore_index, p.V};
+    const bool vec = p.K % 8 == 0 && p.ldx % 8 == 0 && p.ldw % 8 == 0 && (uintptr_t)p.x % 16 == 0 && (uintptr_t)p.w % 16 == 0;
+    const int64_t work = (p.T + p.V) * p.K;
+    const int blocks = (int)(work > 4096 * kRangeBlocks ? kRangeBlocks : work / 4096 + 1);
+    if (hipError_t e = launch(range_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, static_cast<const uint16_t *>(p.x), p.ldx,
+                              static_cast<const uint16_t *>(p.w), p.ldw, p.T, p.K, p.V, vec ? 1 : 0, weights, l.range_part))
+        return e;
+    if (hipError_t e = launch(join_ranges_kernel, dim3(1), dim3(256), 0, stream, l.range_part, blocks, l.ranges)) return e;
     if (dw)
-        if (hipError_t e = transpose16(p.x, p.ldx, p.T, p.K, l.xt, tp, tp,
-                                       RowWeights{dloss, dlse, p.target, p.ignore_index, p.V}, stream))
-            return e;
+        if (hipError_t e = turn(p.x, p.ldx, p.T, p.K, &l.ranges->x, l.xt, tp, tp, weights, stream)) return e;
     const int64_t ld_acc = round_up(p.K, 4);
     for (int64_t v0 = 0; v0 < p.V; v0 += vc) {
         const int64_t cols = p.V - v0 < vc ? p.V - v0 : vc;
@@ -351,7 +482,7 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
         Operands op = lo;
         op.b = lo.b + v0 * lo.ldb;
         op.N = (int)cols;
-        const GradEpi epi{dloss, dlse, lse, p.target, p.ignore_index, p.V, v0, l.g, l.gt, vc, tp};
+        const GradEpi epi{weights, lse, v0, l.ranges, l.g, l.gt, vc, tp};
         const bool big = big_tiles(p.T, cols);
         if (hipError_t e = big ? launch_product<BF16, Big>(op, epi, 1, stream) : launch_product<BF16, Small>(op, epi, 1, stream))
             return e;
@@ -359,8 +490,8 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
         const int64_t step = big ? 256 : 128;
         const int64_t cols_done = round_up(cols, step), rows_done = round_up(p.T, step);
         if (dx) {
-            if (hipError_t e = transpose16(static_cast<const uint16_t *>(p.w) + v0 * p.ldw, p.ldw, cols, p.K, l.wt, vc,
-                                           cols_done, RowWeights{}, stream))
+            if (hipError_t e = turn(static_cast<const uint16_t *>(p.w) + v0 * p.ldw, p.ldw, cols, p.K, &l.ranges->w, l.wt, vc,
+                                    cols_done, RowWeights{}, stream))
                 return e;
             Operands q{};
             q.a = reinterpret_cast<const uint8_t *>(l.g);
@@ -369,19 +500,19 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             q.ldb = 2 * vc;
             q.M = (int)p.T;
             q.N = (int)p.K;
-            q.nk = (int)(cols_done / 32);
+            q.nk = (int)(cols_done / 64);
             auto run = [&](const auto &e) {
-                return big_tiles(p.T, p.K) ? launch_product<BF16, Big>(q, e, 1, stream)
-                                           : launch_product<BF16, Small>(q, e, 1, stream);
+                return big_tiles(p.T, p.K) ? launch_product<F16, Big>(q, e, 1, stream)
+                                           : launch_product<F16, Small>(q, e, 1, stream);
             };
             const float *add = first ? nullptr : l.dx;
             hipError_t e;
             if (!last)
-                e = run(StoreEpi<false>{l.dx, ld_acc, 0, 1.0f, 0.0f, add, ld_acc});
+                e = run(StoreEpi<false>{l.dx, ld_acc, 0, 1.0f, 0.0f, add, ld_acc, l.ranges->inv_gw});
             else if (dx_bf16)
-                e = run(StoreEpi<true>{dx, p.K, 0, 1.0f, 0.0f, add, ld_acc});
+                e = run(StoreEpi<true>{dx, p.K, 0, 1.0f, 0.0f, add, ld_acc, l.ranges->inv_gw});
             else
-                e = run(StoreEpi<false>{dx, p.K, 0, 1.0f, 0.0f, add, ld_acc});
+                e = run(StoreEpi<false>{dx, p.K, 0, 1.0f, 0.0f, add, ld_acc, l.ranges->inv_gw});
             if (e) return e;
         }
         if (dw) {
@@ -392,14 +523,14 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             q.ldb = 2 * tp;
             q.M = (int)cols;
             q.N = (int)p.K;
-            q.nk = (int)(rows_done / 32);
+            q.nk = (int)(rows_done / 64);
             auto run = [&](const auto &e) {
-                return big_tiles(cols, p.K) ? launch_product<BF16, Big>(q, e, 1, stream)
-                                            : launch_product<BF16, Small>(q, e, 1, stream);
+                return big_tiles(cols, p.K) ? launch_product<F16, Big>(q, e, 1, stream)
+                                            : launch_product<F16, Small>(q, e, 1, stream);
             };
             const hipError_t e =
-                dw_bf16 ? run(StoreEpi<true>{static_cast<uint16_t *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f})
-                        : run(StoreEpi<false>{static_cast<float *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f});
+                dw_bf16 ? run(StoreEpi<true>{static_cast<uint16_t *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, l.ranges->inv_gx})
+                        : run(StoreEpi<false>{static_cast<float *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, l.ranges->inv_gx});
             if (e) return e;
         }
     }
