@@ -53,30 +53,33 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v)
     return max(v, dpp<0x140>(v));  // row_mirror
 }
 
-template <bool F32, bool VEC>
+// rows that are aligned to their elements only: the 16-byte loads then go to any even address, which
+// gfx950 serves (unaligned access is on for every HIP process), at up to twice the lines a load
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+template <bool F32>
 __device__ __forceinline__ void load8(const Fp8Input &it, int64_t row, int64_t col, float (&v)[8])
 {
-    if constexpr (VEC) {
-        if (row < it.rows && col + 8 <= it.cols) {
-            if constexpr (F32) {
-                const float *p = static_cast<const float *>(it.x) + row * it.ldx + col;
-                const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+    if (row < it.rows && col + 8 <= it.cols) {
+        if constexpr (F32) {
+            const float *p = static_cast<const float *>(it.x) + row * it.ldx + col;
+            const f32x4 a = *reinterpret_cast<const f32x4_any *>(p), b = *reinterpret_cast<const f32x4_any *>(p + 4);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = a[e];
-                    v[4 + e] = b[e];
-                }
-            } else {
-                const u32x4 a =
-                    *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(it.x) + row * it.ldx + col);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[2 * e] = bf16_lo(a[e]);
-                    v[2 * e + 1] = bf16_hi(a[e]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                v[e] = a[e];
+                v[4 + e] = b[e];
             }
-            return;
+        } else {
+            const u32x4 a =
+                *reinterpret_cast<const u32x4_any *>(static_cast<const uint16_t *>(it.x) + row * it.ldx + col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = bf16_lo(a[e]);
+                v[2 * e + 1] = bf16_hi(a[e]);
+            }
         }
+        return;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -104,22 +107,12 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(Fp8Args args)
     const int64_t row0 = tm * 128 + 8 * rg, col0 = tn * 128 + 8 * cg;
 
     float v[8][8];
-    const bool vec = ((uintptr_t)it.x % 16) == 0 && (it.ldx * (it.f32 ? 4 : 2)) % 16 == 0;
-    // the tile's own branch is uniform: one of four copies of the loads
     if (it.f32) {
-        if (vec)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) load8<true, true>(it, row0 + i, col0, v[i]);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) load8<true, false>(it, row0 + i, col0, v[i]);
+        for (int i = 0; i < 8; ++i) load8<true>(it, row0 + i, col0, v[i]);
     } else {
-        if (vec)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) load8<false, true>(it, row0 + i, col0, v[i]);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) load8<false, false>(it, row0 + i, col0, v[i]);
+        for (int i = 0; i < 8; ++i) load8<false>(it, row0 + i, col0, v[i]);
     }
     uint32_t rmax[8];
 #pragma unroll
@@ -239,11 +232,15 @@ hipError_t launch_fp8_quantize(const Fp8Input *items, int count, hipStream_t str
     return launch(fp8_quantize_kernel, dim3((unsigned)total), dim3(256), 0, stream, args);
 }
 
-size_t fp8_gemm_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    return slab::plan_product(M, N, round_up(K, 128) / 128, false, 1, true).partial_bytes;
+}
 
 hipError_t launch_fp8_gemm(const uint8_t *aq, int64_t lda, const uint8_t *as, int64_t ldas, const uint8_t *bq,
                            int64_t ldb, const uint8_t *bs, int64_t ldbs, int64_t M, int64_t N, int64_t K, float alpha,
-                           float beta, void *c, bool bf16, int64_t ldc, void *, size_t, hipStream_t stream)
+                           float beta, void *c, bool bf16, int64_t ldc, void *workspace, size_t ws_bytes,
+                           hipStream_t stream)
 {
     using namespace slab;
     Operands op{};
@@ -258,11 +255,9 @@ hipError_t launch_fp8_gemm(const uint8_t *aq, int64_t lda, const uint8_t *as, in
     op.M = (int)M;
     op.N = (int)N;
     op.nk = (int)(round_up(K, 128) / 128);
-    const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-    auto run = [&](const auto &epi) {
-        return big > kComputeUnits / 2 ? launch_product<E4M3, Big>(op, epi, 1, stream)
-                                       : launch_product<E4M3, Small>(op, epi, 1, stream);
-    };
+    Plan plan = plan_product(M, N, op.nk, false, 1, true);
+    if (plan.partial_bytes > ws_bytes || !workspace) plan = plan_product(M, N, op.nk, false, 1, false);
+    auto run = [&](const auto &epi) { return launch_product<E4M3>(op, epi, 1, plan, workspace, stream); };
     return bf16 ? run(StoreEpi<true>{c, ldc, 0, alpha, beta}) : run(StoreEpi<false>{c, ldc, 0, alpha, beta});
 }
 

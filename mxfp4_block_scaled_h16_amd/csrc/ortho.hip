@@ -15,6 +15,8 @@
 // Per step three launches: A (symmetric: the lower triangle of tiles, written twice), b A + c A A
 // (symmetric too), and the update, which writes X in both orientations for the next step's
 // products, each of which contracts along rows.
+#include <algorithm>
+
 #include "slab_gemm.h"
 #include "train_internal.h"
 
@@ -63,17 +65,33 @@ struct PolyEpi {
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
     {
+        using B = Block16<G>;
+        const int r = w.lane & 15, q = w.lane >> 4;
+        uint8_t *tile = lds + w.wave * 2 * B::kBytes, *turned = tile + B::kBytes;
+        const int64_t n = w.n0 + w.col0;
         const uint16_t *in = gram + w.batch * batch_out;
         uint16_t *o = out + w.batch * batch_out;
-        const int r = w.lane & 15, q = w.lane >> 4;
         const float cs = c * kUnscale;
-        store_tile16<G>(w, lds, [](float x, float y) { return pack_f16(x, y); },
-                        [&](int i, int j) {
-                            const f32x4 g =
-                                f16_quad(in + (int64_t)(w.m0 + w.row0 + 16 * i + r) * ld + w.n0 + w.col0 + 16 * j + 4 * q);
-                            return b * g + cs * acc[i][j];
-                        },
-                        o, ld, w.m0 == w.n0 ? nullptr : o, ld);
+#pragma unroll
+        for (int blk = 0; blk < B::kBlocks; ++blk) {
+            const int64_t m = w.m0 + w.row0 + B::kRows * blk;
+            u32x4 v[B::kPasses];
+            B::from_memory(v, w.lane, in + m * ld + n, ld);
+            B::put(tile, w.lane, v);
+#pragma unroll
+            for (int ii = 0; ii < B::BI; ++ii)
+#pragma unroll
+                for (int j = 0; j < G::FJ; ++j) {
+                    const int row = 16 * ii + r, col = 16 * j + 4 * q;
+                    uint8_t *place = tile + B::quad(row, col);   // read and written by this lane alone
+                    const f32x4 p = b * f16_quad(reinterpret_cast<const uint16_t *>(place)) + cs * acc[B::BI * blk + ii][j];
+                    const uint32_t lo = pack_f16(p[0], p[1]), hi = pack_f16(p[2], p[3]);
+                    *reinterpret_cast<u32x2 *>(place) = u32x2{lo, hi};
+                    if (w.m0 != w.n0) B::put_turned(turned, row, col, lo, hi);
+                }
+            B::to_memory(tile, w.lane, o + m * ld + n, ld);
+            if (w.m0 != w.n0) B::to_memory(turned, w.lane, o + n * ld + m, ld);
+        }
     }
 };
 
@@ -82,30 +100,50 @@ struct UpdateEpi {
     static constexpr bool kSym = false;
     const uint16_t *hi;      // X [mp][np]
     uint16_t *lo;            // read and written
-    uint16_t *hi_out, *turned;
+    uint16_t *hi_out, *turned_out;
     int64_t ld, ld_turned, batch_x;
     float a;
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
     {
+        using B = Block16<G>;
         const int r = w.lane & 15, q = w.lane >> 4;
-        const uint16_t *h = hi + w.batch * batch_x;
-        uint16_t *l = lo + w.batch * batch_x;
+        uint8_t *tile = lds + w.wave * 2 * B::kBytes, *turned = tile + B::kBytes;
+        const int64_t base = w.batch * batch_x, n = w.n0 + w.col0;
 #pragma unroll
-        for (int i = 0; i < G::FI; ++i)
+        for (int blk = 0; blk < B::kBlocks; ++blk) {
+            const int64_t m = w.m0 + w.row0 + B::kRows * blk, at = base + m * ld + n;
+            u32x4 h[B::kPasses], l[B::kPasses];
+            B::from_memory(h, w.lane, hi + at, ld);
+            B::from_memory(l, w.lane, lo + at, ld);
+            B::put(tile, w.lane, h);
+            B::put(turned, w.lane, l);   // not turned yet: the remainders, row by row
 #pragma unroll
-            for (int j = 0; j < G::FJ; ++j) {
-                const int64_t at = (int64_t)(w.m0 + w.row0 + 16 * i + r) * ld + w.n0 + w.col0 + 16 * j + 4 * q;
-                const f32x4 x = f16_quad(h + at) + f16_quad(l + at) * kLoUnscale;
-                const f32x4 v = a * x + kUnscale * acc[i][j];
-                f32x4 rem;
+            for (int ii = 0; ii < B::BI; ++ii)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) rem[t] = (v[t] - f16_float(f16_bits(v[t]))) * kLoScale;
-                acc[i][j] = v;
-                *reinterpret_cast<u32x2 *>(l + at) = u32x2{pack_f16(rem[0], rem[1]), pack_f16(rem[2], rem[3])};
-            }
-        store_tile16<G>(w, lds, [](float x, float y) { return pack_f16(x, y); }, [&](int i, int j) { return acc[i][j]; },
-                        hi_out + w.batch * batch_x, ld, turned + w.batch * batch_x, ld_turned);
+                for (int j = 0; j < G::FJ; ++j) {
+                    const int place = B::quad(16 * ii + r, 16 * j + 4 * q);   // read and written by this lane alone
+                    const f32x4 x = f16_quad(reinterpret_cast<const uint16_t *>(tile + place)) +
+                                    f16_quad(reinterpret_cast<const uint16_t *>(turned + place)) * kLoUnscale;
+                    const f32x4 v = a * x + kUnscale * acc[B::BI * blk + ii][j];
+                    f32x4 rest;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) rest[t] = (v[t] - f16_float(f16_bits(v[t]))) * kLoScale;
+                    *reinterpret_cast<u32x2 *>(tile + place) = u32x2{pack_f16(v[0], v[1]), pack_f16(v[2], v[3])};
+                    *reinterpret_cast<u32x2 *>(turned + place) = u32x2{pack_f16(rest[0], rest[1]), pack_f16(rest[2], rest[3])};
+                }
+            B::to_memory(tile, w.lane, hi_out + at, ld);
+            B::to_memory(turned, w.lane, lo + at, ld);
+#pragma unroll
+            for (int ii = 0; ii < B::BI; ++ii)
+#pragma unroll
+                for (int j = 0; j < G::FJ; ++j) {
+                    const int row = 16 * ii + r, col = 16 * j + 4 * q;
+                    const u32x2 v = *reinterpret_cast<const u32x2 *>(tile + B::quad(row, col));
+                    B::put_turned(turned, row, col, v.x, v.y);
+                }
+            B::to_memory(turned, w.lane, turned_out + base + n * ld_turned + m, ld_turned);
+        }
     }
 };
 
@@ -120,17 +158,36 @@ struct LastEpi {
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
     {
+        using B = Block16<G>;
         const int r = w.lane & 15, q = w.lane >> 4;
-        const uint16_t *h = hi + w.batch * batch_x, *l = lo + w.batch * batch_x;
-        store.template run_with<G>(w, op, lds, [&](int i, int j) {
-            const int64_t at = (int64_t)(w.m0 + w.row0 + 16 * i + r) * ld + w.n0 + w.col0 + 16 * j + 4 * q;
-            return a * (f16_quad(h + at) + f16_quad(l + at) * kLoUnscale) + kUnscale * acc[i][j];
-        });
+        uint8_t *tile = lds + w.wave * 2 * B::kBytes, *rests = tile + B::kBytes;
+#pragma unroll
+        for (int blk = 0; blk < B::kBlocks; ++blk) {
+            const int64_t at = w.batch * batch_x + (w.m0 + w.row0 + B::kRows * blk) * ld + w.n0 + w.col0;
+            u32x4 v[B::kPasses];
+            B::from_memory(v, w.lane, hi + at, ld);
+            B::put(tile, w.lane, v);
+            B::from_memory(v, w.lane, lo + at, ld);
+            B::put(rests, w.lane, v);
+#pragma unroll
+            for (int ii = 0; ii < B::BI; ++ii)
+#pragma unroll
+                for (int j = 0; j < G::FJ; ++j) {
+                    const int place = B::quad(16 * ii + r, 16 * j + 4 * q);
+                    const f32x4 x = f16_quad(reinterpret_cast<const uint16_t *>(tile + place)) +
+                                    f16_quad(reinterpret_cast<const uint16_t *>(rests + place)) * kLoUnscale;
+                    acc[B::BI * blk + ii][j] = a * x + kUnscale * acc[B::BI * blk + ii][j];
+                }
+        }
+        // the staged rows below reuse the LDS, part of it another wavefront's blocks until now
+        __syncthreads();
+        store.template run<G>(acc, w, op, lds);
     }
 };
 
 // ----------------------------------------------------------------- norm and first operands ----
-constexpr int kNormBlocks = 512;
+constexpr int kNormBlocks = 1024;   // at most so many partial sums of a matrix
+constexpr int kNormTile = 8192;     // values a workgroup should at least have
 
 template <bool F32>
 __device__ __forceinline__ float read_g(const void *g, int64_t at)
@@ -141,60 +198,121 @@ __device__ __forceinline__ float read_g(const void *g, int64_t at)
         return bf16_float(static_cast<const uint16_t *>(g)[at]);
 }
 
-// sums of squares, one per workgroup, in 64 bits (the squares of FP32 numbers leave FP32's range)
+// eight consecutive values; 16-byte aligned
+template <bool F32>
+__device__ __forceinline__ void read_g8(const void *g, int64_t at, float (&v)[8])
+{
+    if constexpr (F32) {
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(g) + at);
+        const f32x4 b = *reinterpret_cast<const f32x4 *>(static_cast<const float *>(g) + at + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = a[e];
+            v[4 + e] = b[e];
+        }
+    } else {
+        const u32x4 a = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(g) + at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t word = a[e];
+            v[2 * e] = bf16_float(word & 0xFFFFu);
+            v[2 * e + 1] = bf16_float(word >> 16);
+        }
+    }
+}
+
+// Sums of squares, one per workgroup, in 64 bits (the squares of FP32 numbers leave FP32's range). Bound by
+// memory. vec: 16-byte aligned rows of whole eights.
 template <bool F32>
 __global__ __launch_bounds__(256) void norm_kernel(const void *__restrict__ g, int64_t m, int64_t n, int64_t ldg, int64_t batch_g,
-                                                   double *__restrict__ part)
+                                                   int vec, double *__restrict__ part)
 {
     __shared__ double slots[4];
     const int64_t base = blockIdx.z * batch_g;
     double sum = 0.0;
-    for (int64_t row = blockIdx.x; row < m; row += gridDim.x)
-        for (int64_t col = threadIdx.x; col < n; col += 256) {
-            const double v = (double)read_g<F32>(g, base + row * ldg + col);
-            sum += v * v;
-        }
+    if (vec) {
+        const int64_t per_row = n / 8;
+        // a thread's eights of its row run on by 256; rows of fewer than that share the workgroup
+        const int64_t across = per_row < 256 ? per_row : 256, rows_at_once = 256 / across;
+        const int64_t lane_row = threadIdx.x / across, lane_col = threadIdx.x % across;
+        if (lane_row < rows_at_once)
+            for (int64_t row = blockIdx.x * rows_at_once + lane_row; row < m; row += (int64_t)gridDim.x * rows_at_once)
+                for (int64_t c = lane_col; c < per_row; c += across) {
+                    float v[8];
+                    read_g8<F32>(g, base + row * ldg + 8 * c, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum += (double)v[e] * (double)v[e];
+                }
+    } else {
+        for (int64_t row = blockIdx.x; row < m; row += gridDim.x)
+            for (int64_t col = threadIdx.x; col < n; col += 256) {
+                const double v = (double)read_g<F32>(g, base + row * ldg + col);
+                sum += v * v;
+            }
+    }
     for (int k = 32; k >= 1; k >>= 1) sum += __shfl_xor(sum, k);
     if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = sum;
     __syncthreads();
     if (threadIdx.x == 0) part[blockIdx.z * kNormBlocks + blockIdx.x] = (slots[0] + slots[1]) + (slots[2] + slots[3]);
 }
 
-// X = G / (|G| + eps), times 2^10, in value and remainder and (the value) transposed, with zeros around it
+// X = G / (|G| + eps), times 2^10, in value and remainder and (the value) transposed, with zeros around it.
+// 128 x 128 tiles: a thread takes 8 x 8 values and transposes them in registers; 256-byte lines of
+// the transposed are put together in the LDS. Bound by memory: 4 (or 2) bytes in, 6 out.
 template <bool F32>
 __global__ __launch_bounds__(256) void first_kernel(const void *__restrict__ g, int64_t m, int64_t n, int64_t ldg, int64_t batch_g,
-                                                    const double *__restrict__ part, int parts, float eps,
+                                                    int vec, const double *__restrict__ part, int parts, float eps,
                                                     uint16_t *__restrict__ hi, uint16_t *__restrict__ lo,
                                                     uint16_t *__restrict__ turned, int64_t mp, int64_t np, int64_t batch_x)
 {
-    __shared__ uint16_t tile[64][64 + 2];
-    __shared__ float inv_shared;
-    if (threadIdx.x < 64) {
-        double sum = 0.0;
-        for (int k = threadIdx.x; k < parts; k += 64) sum += part[blockIdx.z * kNormBlocks + k];
-        for (int k = 32; k >= 1; k >>= 1) sum += __shfl_xor(sum, k);
-        if (threadIdx.x == 0) inv_shared = (float)(1024.0 / (sqrt(sum) + (double)eps));
-    }
+    __shared__ __attribute__((aligned(16))) uint16_t tile[128 * 128];   // [column][row], 16-byte pieces permuted
+    __shared__ double slots[4];
+    double sum = 0.0;
+    for (int k = threadIdx.x; k < parts; k += 256) sum += part[blockIdx.z * kNormBlocks + k];
+    for (int k = 32; k >= 1; k >>= 1) sum += __shfl_xor(sum, k);
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = sum;
     __syncthreads();
-    const float inv = inv_shared;
-    const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-    const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+    const float inv = (float)(1024.0 / (sqrt((slots[0] + slots[1]) + (slots[2] + slots[3])) + (double)eps));
+
+    const int64_t r0 = (int64_t)blockIdx.x * 128, c0 = (int64_t)blockIdx.y * 128;
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+    const int64_t c = c0 + 8 * cg;
+    uint16_t h[8][8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        const int64_t r = r0 + ty + 4 * k, c = c0 + tx;
-        const float v = r < m && c < n ? read_g<F32>(g, blockIdx.z * batch_g + r * ldg + c) * inv : 0.0f;
-        const uint16_t h = f16_bits(v);
-        tile[ty + 4 * k][tx] = h;
-        if (r < mp && c < np) {
-            hi[blockIdx.z * batch_x + r * np + c] = h;
-            lo[blockIdx.z * batch_x + r * np + c] = f16_bits((v - f16_float(h)) * kLoScale);
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + 8 * rg + i, at = blockIdx.z * batch_g + r * ldg + c;
+        float v[8];
+        if (vec && r < m && c + 8 <= n) {
+            read_g8<F32>(g, at, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = r < m && c + e < n ? read_g<F32>(g, at + e) : 0.0f;
         }
+        u32x4 value, rest;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = v[2 * e] * inv, b = v[2 * e + 1] * inv;
+            h[i][2 * e] = f16_bits(a);
+            h[i][2 * e + 1] = f16_bits(b);
+            value[e] = (uint32_t)h[i][2 * e] | (uint32_t)h[i][2 * e + 1] << 16;
+            rest[e] = pack_f16((a - f16_float(h[i][2 * e])) * kLoScale, (b - f16_float(h[i][2 * e + 1])) * kLoScale);
+        }
+        *reinterpret_cast<u32x4 *>(hi + blockIdx.z * batch_x + r * np + c) = value;
+        *reinterpret_cast<u32x4 *>(lo + blockIdx.z * batch_x + r * np + c) = rest;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        u32x4 o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = (uint32_t)h[2 * k][e] | (uint32_t)h[2 * k + 1][e] << 16;
+        *reinterpret_cast<u32x4 *>(tile + (8 * cg + e) * 128 + 8 * (rg ^ cg)) = o;
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        const int64_t c = c0 + ty + 4 * k, r = r0 + tx;
-        if (c < np && r < mp) turned[blockIdx.z * batch_x + c * mp + r] = tile[tx][ty + 4 * k];
+    for (int p = 0; p < 8; ++p) {
+        const int col = 16 * p + (threadIdx.x >> 4), piece = threadIdx.x & 15;
+        *reinterpret_cast<u32x4 *>(turned + blockIdx.z * batch_x + (c0 + col) * mp + r0 + 8 * piece) =
+            *reinterpret_cast<const u32x4 *>(tile + col * 128 + 8 * (piece ^ (col >> 3)));
     }
 }
 
@@ -221,25 +339,41 @@ __global__ __launch_bounds__(256) void copy_out_kernel(const uint16_t *__restric
 
 // ------------------------------------------------------------------------------ workspace -----
 struct Sizes {
-    int64_t mp, np, sp;   // padded rows, columns, shorter side
-    bool big;
+    int64_t mp, np, sp, lp;   // rows, columns, shorter and longer side, padded
+    slab::Plan gram, poly, update, last;
+    size_t partial_bytes;
 };
-// Tiles of 256 x 256 once the Gram matrix has more of them than half the CUs, else 128 x 128.
+// Every product covers whole tiles of its operands: with 256 x 256 tiles the sides are padded to 256, with
+// smaller ones to 128.
 Sizes sizes_of(int64_t batch, int64_t m, int64_t n)
 {
-    const int64_t s = m < n ? m : n, l = m < n ? n : m;
     Sizes z;
-    z.big = batch * ((s + 255) / 256) * ((l + 255) / 256) > kComputeUnits / 2;
-    const int64_t t = z.big ? 256 : 128;
-    z.mp = round_up(m, t);
-    z.np = round_up(n, t);
-    z.sp = m <= n ? z.mp : z.np;
+    const auto plans = [&](int64_t pad) {
+        z.mp = round_up(m, pad);
+        z.np = round_up(n, pad);
+        z.sp = m <= n ? z.mp : z.np;
+        z.lp = m <= n ? z.np : z.mp;
+        z.gram = plan_product(z.sp, z.sp, z.lp / 64, true, batch, true);
+        z.poly = plan_product(z.sp, z.sp, z.sp / 64, true, batch, true);
+        z.update = plan_product(z.mp, z.np, z.sp / 64, false, batch, true);
+        z.last = plan_product(m, n, z.sp / 64, false, batch, true);
+    };
+    plans(256);
+    const bool big = z.gram.geo == 0 || z.poly.geo == 0 || z.update.geo == 0 || z.last.geo == 0;
+    if (!big) {
+        plans(128);
+        // smaller sides may tip a plan: 256 x 256 tiles need their padding
+        if (z.gram.geo == 0 || z.poly.geo == 0 || z.update.geo == 0 || z.last.geo == 0) plans(256);
+    }
+    z.partial_bytes = std::max(std::max(z.gram.partial_bytes, z.poly.partial_bytes),
+                               std::max(z.update.partial_bytes, z.last.partial_bytes));
     return z;
 }
 
 struct Space {
     double *part;
     uint16_t *hi[2], *turned[2], *lo, *gram, *poly;
+    void *partials;
     size_t bytes;
 };
 Space carve(uint8_t *base, int64_t batch, const Sizes &z)
@@ -258,14 +392,15 @@ Space carve(uint8_t *base, int64_t batch, const Sizes &z)
     s.lo = reinterpret_cast<uint16_t *>(take(x));
     s.gram = reinterpret_cast<uint16_t *>(take(a));
     s.poly = reinterpret_cast<uint16_t *>(take(a));
+    s.partials = take(z.partial_bytes);
     s.bytes = at;
     return s;
 }
 
 template <class Epi>
-hipError_t product(bool big, const Operands &op, const Epi &epi, int64_t batch, hipStream_t stream)
+hipError_t product(const Plan &plan, const Operands &op, const Epi &epi, int64_t batch, const Space &s, hipStream_t stream)
 {
-    return big ? launch_product<F16, Big>(op, epi, (int)batch, stream) : launch_product<F16, Small>(op, epi, (int)batch, stream);
+    return launch_product<F16>(op, epi, (int)batch, plan, s.partials, stream);
 }
 
 }  // namespace
@@ -280,15 +415,18 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
     const Sizes z = sizes_of(p.batch, p.m, p.n);
     const Space s = carve(static_cast<uint8_t *>(ws), p.batch, z);
     const int64_t bx = z.mp * z.np, ba = z.sp * z.sp;
-    const int parts = (int)(p.m < kNormBlocks ? p.m : kNormBlocks);
+    const int64_t esize = p.f32 ? 4 : 2;
+    const int vec = p.n % 8 == 0 && (uintptr_t)p.g % 16 == 0 && p.ldg * esize % 16 == 0 && (p.batch == 1 || p.batch_g * esize % 16 == 0);
+    const int64_t want = p.m * p.n / kNormTile + 1, most = p.m < kNormBlocks ? p.m : kNormBlocks;
+    const int parts = (int)(want < most ? want : most);
     const dim3 ngrid((unsigned)parts, 1, (unsigned)p.batch);
-    const dim3 fgrid((unsigned)(z.mp / 64), (unsigned)(z.np / 64), (unsigned)p.batch);
-    hipError_t e = p.f32 ? launch(norm_kernel<true>, ngrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, s.part)
-                         : launch(norm_kernel<false>, ngrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, s.part);
+    const dim3 fgrid((unsigned)(z.mp / 128), (unsigned)(z.np / 128), (unsigned)p.batch);
+    hipError_t e = p.f32 ? launch(norm_kernel<true>, ngrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, vec, s.part)
+                         : launch(norm_kernel<false>, ngrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, vec, s.part);
     if (e) return e;
-    e = p.f32 ? launch(first_kernel<true>, fgrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, s.part, parts, p.eps,
+    e = p.f32 ? launch(first_kernel<true>, fgrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, vec, s.part, parts, p.eps,
                        s.hi[0], s.lo, s.turned[0], z.mp, z.np, bx)
-              : launch(first_kernel<false>, fgrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, s.part, parts, p.eps,
+              : launch(first_kernel<false>, fgrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, vec, s.part, parts, p.eps,
                        s.hi[0], s.lo, s.turned[0], z.mp, z.np, bx);
     if (e) return e;
     if (p.steps == 0) {
@@ -306,12 +444,12 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
         op.M = op.N = (int)z.sp;
         op.nk = (int)((wide ? z.np : z.mp) / 64);
         op.batch_a = op.batch_b = 2 * bx;
-        if ((e = product(z.big, op, GramEpi{s.gram, z.sp, ba}, p.batch, stream))) return e;
+        if ((e = product(z.gram, op, GramEpi{s.gram, z.sp, ba}, p.batch, s, stream))) return e;
         op.a = op.b = reinterpret_cast<const uint8_t *>(s.gram);
         op.lda = op.ldb = 2 * z.sp;
         op.nk = (int)(z.sp / 64);
         op.batch_a = op.batch_b = 2 * ba;
-        if ((e = product(z.big, op, PolyEpi{s.gram, s.poly, z.sp, ba, p.b, p.c}, p.batch, stream))) return e;
+        if ((e = product(z.poly, op, PolyEpi{s.gram, s.poly, z.sp, ba, p.b, p.c}, p.batch, s, stream))) return e;
         // the update in X's orientation: poly X for wide, X poly for tall (poly is symmetric)
         op.a = reinterpret_cast<const uint8_t *>(wide ? s.poly : x);
         op.lda = 2 * (wide ? z.sp : z.np);
@@ -324,17 +462,17 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
         op.N = (int)z.np;
         if (k + 1 < p.steps) {
             const UpdateEpi epi{x, s.lo, s.hi[(k + 1) & 1], s.turned[(k + 1) & 1], z.np, z.mp, bx, p.a};
-            if ((e = product(z.big, op, epi, p.batch, stream))) return e;
+            if ((e = product(z.update, op, epi, p.batch, s, stream))) return e;
         } else {
             op.M = (int)p.m;
             op.N = (int)p.n;
             const float alpha = p.alpha * kUnscale;
-            e = p.out_bf16 ? product(z.big, op, LastEpi<true>{x, s.lo, z.np, bx, p.a,
+            e = p.out_bf16 ? product(z.last, op, LastEpi<true>{x, s.lo, z.np, bx, p.a,
                                                               StoreEpi<true>{p.out, p.ldo, p.batch_o, alpha, p.beta}},
-                                     p.batch, stream)
-                           : product(z.big, op, LastEpi<false>{x, s.lo, z.np, bx, p.a,
+                                     p.batch, s, stream)
+                           : product(z.last, op, LastEpi<false>{x, s.lo, z.np, bx, p.a,
                                                                StoreEpi<false>{p.out, p.ldo, p.batch_o, alpha, p.beta}},
-                                     p.batch, stream);
+                                     p.batch, s, stream);
             if (e) return e;
         }
     }

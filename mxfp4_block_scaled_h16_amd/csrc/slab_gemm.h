@@ -24,7 +24,7 @@
 // so that stores cover whole lines.
 #pragma once
 
-#include <type_traits>
+#include <climits>
 
 #include "internal.h"
 
@@ -94,13 +94,14 @@ __device__ __forceinline__ void barrier()
 __device__ __forceinline__ int chunk_perm(int row) { return (row >> 1) & 7; }
 
 // ------------------------------------------------------------------------------ geometry ------
-// NW_ wavefronts on a TM x TN tile, arranged WM x (NW_ / WM).
-template <int NW_, int TM, int TN, int WM>
+// NW_ wavefronts on a TM x TN tile, arranged WM x (NW_ / WM); NB stage buffers.
+template <int NW_, int TM, int TN, int WM, int NB = 2>
 struct Geo {
-    static constexpr int NW = NW_, kTileM = TM, kTileN = TN;
+    static constexpr int NW = NW_, kTileM = TM, kTileN = TN, kBuffers = NB;
+    static_assert(NB == 2 || NB == 4, "the buffer of a stage is its low bits");
     static constexpr int kABytes = TM * kRowBytes;
     static constexpr int kStageBytes = (TM + TN) * kRowBytes;
-    static constexpr int kRingBytes = 2 * kStageBytes;
+    static constexpr int kRingBytes = NB * kStageBytes;
     static constexpr int kScaleSlot = (TM + TN) * 16;             // 16 scale bytes per row: 16 stages
     static constexpr int kWavesM = WM, kWavesN = NW / WM;
     static constexpr int kWaveRows = TM / kWavesM, kWaveCols = TN / kWavesN;
@@ -108,7 +109,7 @@ struct Geo {
     static constexpr int kDmaA = TM / kRowsPerDma / NW, kDmaB = TN / kRowsPerDma / NW;
     static constexpr int kDmaPerStage = kDmaA + kDmaB;
     static_assert(kDmaA * kRowsPerDma * NW == TM && kDmaB * kRowsPerDma * NW == TN, "whole loads per wavefront");
-    static_assert((TM + TN) / 64 == NW, "one scale load per wavefront and group");
+    static_assert((TM + TN) / 64 <= NW, "at most one scale load per wavefront and group");
     // LDS for staging the output: 32 rows of the wavefront's columns, rows 16 bytes apart
     static constexpr int kEpiRow = kWaveCols * 4 + 16, kEpiWave = 32 * kEpiRow;
     template <class E>
@@ -119,8 +120,9 @@ struct Geo {
     static_assert(NW * kEpiWave <= kRingBytes, "the staged output reuses the ring");
     static constexpr int kMinBlocks = kRingBytes + 2 * kScaleSlot <= 80 * 1024 ? 2 : 1;   // workgroups per CU
 };
-using Big = Geo<8, 256, 256, 2>;     // wave tiles 128 x 64, 128 accumulator registers
-using Small = Geo<4, 128, 128, 2>;   // wave tiles 64 x 64, two workgroups per CU
+using Big = Geo<8, 256, 256, 2>;       // wave tiles 128 x 64, 128 accumulator registers
+using Small = Geo<4, 128, 128, 2>;     // wave tiles 64 x 64, two workgroups per CU
+using Tiny = Geo<4, 64, 64, 2, 4>;     // wave tiles 32 x 32, loads three stages ahead: where latency is all
 
 // --------------------------------------------------------------------------------- operands ---
 // Rows past M and N are read as row M - 1 and N - 1 (their results are the epilogue's to drop).
@@ -133,6 +135,10 @@ struct Operands {
     int M, N, nk;
     int tiles_m, tiles_n;
     int64_t batch_a, batch_b;  // bytes from one product of a batch (blockIdx.z) to the next
+    // A contraction worked by several workgroups (blockIdx.y), stages [y per, y per + per) each: with splits > 1
+    // they leave their sums in partials, in the order of their registers, and finish_kernel adds them up.
+    int splits = 1, per = 0;
+    f32x4 *partials = nullptr;
 };
 
 struct Where {
@@ -166,6 +172,13 @@ __device__ __forceinline__ void locate(int v, int tiles_m, int tiles_n, int &m0,
         m0 = (g0 + (t % group) % gm) * G::kTileM;
         n0 = ((t % group) / gm) * G::kTileN;
     }
+}
+
+// where this workgroup's tile keeps its sums over split y
+template <class G>
+__device__ __forceinline__ int64_t partial_at(const Operands &op, int y)
+{
+    return (((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * op.splits + y) * (G::kTileM * G::kTileN / 4);
 }
 
 // -------------------------------------------------------------------------------- the kernel --
@@ -214,11 +227,13 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
         const int row = b_row0 + kRowsPerDma * u + lane / 8;
         boff[u] = (uint32_t)min(row, op.N - 1 - w.n0) * (uint32_t)op.ldb + 16u * ((lane % 8) ^ chunk_perm(row));
     }
-    const int nk = op.nk;
+    const int first = op.splits > 1 ? blockIdx.y * op.per : 0;
+    const int end = op.splits > 1 ? min(op.nk, first + op.per) : op.nk;
+    constexpr int NB = G::kBuffers;
     auto dma = [&](int stage) {
         // past the last stage the last one again, into a free buffer
-        const int at = min(stage, nk - 1) * kRowBytes;
-        uint8_t *dst = lds + (stage & 1) * G::kStageBytes;
+        const int at = min(stage, end - 1) * kRowBytes;
+        uint8_t *dst = lds + (stage & (NB - 1)) * G::kStageBytes;
 #pragma unroll
         for (int u = 0; u < G::kDmaA; ++u)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(arsrc, (lds_void_t *)(dst + a_row0 * kRowBytes + u * 1024), 16, aoff[u],
@@ -229,7 +244,7 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
                                                      16, boff[u], at, 0, 0);
     };
     // E4M3: the scales of 16 stages (16 bytes of every row) per load, wavefront w those of the tile's rows
-    // [64 w, + 64) (A's first, then B's)
+    // [64 w, + 64) (A's first, then B's; wavefronts past the last of them none)
     const uint8_t *sbase = nullptr;
     uint32_t soff = 0;
     if constexpr (E::kScaled) {
@@ -239,8 +254,9 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
         soff = is_b ? (uint32_t)min(row, op.N - 1 - w.n0) * (uint32_t)op.ldbs
                     : (uint32_t)min(row, op.M - 1 - w.m0) * (uint32_t)op.ldas;
     }
-    const int last_group = (nk - 1) / 16;
+    const int last_group = (end - 1) / 16;
     auto dma_scales = [&](int g) {
+        if ((G::kTileM + G::kTileN) / 64 < G::NW && w.wave >= (G::kTileM + G::kTileN) / 64) return;
         __builtin_amdgcn_global_load_lds((gbl_void_t *)(sbase + (int64_t)min(g, last_group) * 16 + soff),
                                          (lds_void_t *)(lds + G::kRingBytes + (g & 1) * G::kScaleSlot + w.wave * 1024),
                                          16, 0, 0);
@@ -249,7 +265,7 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
     const int perm = chunk_perm(r);
     const int a_frag = (w.row0 + r) * kRowBytes, b_frag = G::kABytes + (w.col0 + r) * kRowBytes;
     const int chunk0 = 16 * (q ^ perm), chunk1 = 16 * ((4 + q) ^ perm);
-    auto buffer = [&](int stage) { return lds + (stage & 1) * G::kStageBytes; };
+    auto buffer = [&](int stage) { return lds + (stage & (NB - 1)) * G::kStageBytes; };
     auto read_a = [&](const uint8_t *src, int i) { return *reinterpret_cast<const u32x4 *>(src + a_frag + 16 * i * kRowBytes); };
     auto read_b = [&](const uint8_t *src, int j) { return *reinterpret_cast<const u32x4 *>(src + b_frag + 16 * j * kRowBytes); };
 
@@ -259,10 +275,14 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
 #pragma unroll
         for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{};
 
-    if constexpr (E::kScaled) dma_scales(0);
-    dma(0);
-    dma(1);
-    wait_vmcnt<G::kDmaPerStage>();
+    // a wavefront may load no scales: its waits then cover a load more than they have to
+    if constexpr (E::kScaled) {
+        dma_scales(first >> 4);
+        dma_scales((first >> 4) + 1);
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) dma(first + k);
+    wait_vmcnt<(NB - 1) * G::kDmaPerStage>();
     barrier();
 
     if constexpr (!E::kScaled) {
@@ -279,38 +299,41 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
 #pragma unroll
                 for (int j = 0; j < FJ; ++j) E::mfma(acc[i][j], fb[j], fa[i]);
         };
-        read(buffer(0) + chunk0, fa0, fb0);
+        read(buffer(first) + chunk0, fa0, fb0);
         constexpr int kMfma = FI * FJ, kReads = FI + FJ, kLoads = G::kDmaPerStage;
         constexpr int kPer = kMfma / kReads;   // MFMAs per read in the first half
-        for (int s = 0; s < nk; ++s) {
+        for (int s = first; s < end; ++s) {
             read(buffer(s) + chunk1, fa1, fb1);
             mfmas(fa0, fb0);
+            if constexpr (kPer > 0) {
 #pragma unroll
-            for (int k = 0; k < kReads; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);  // MFMA
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // DS read
+                for (int k = 0; k < kReads; ++k) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);  // MFMA
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // DS read
+                }
+                __builtin_amdgcn_sched_group_barrier(0x008, kMfma - kPer * kReads, 0);
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, kMfma - kPer * kReads, 0);
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the stage has been read
-            wait_vmcnt<0>();                      // stage s + 1 has landed
+            wait_vmcnt<(NB - 2) * G::kDmaPerStage>();   // stage s + 1 has landed
             barrier();
-            dma(s + 2);
+            dma(s + NB);
             read(buffer(s + 1) + chunk0, fa0, fb0);
             mfmas(fa1, fb1);
             // the loads at once: they have the longest way to go
-            constexpr int kBoth = kLoads + kReads <= kMfma ? 1 : 2;
+            if constexpr (kLoads + kReads <= kMfma) {
 #pragma unroll
-            for (int k = 0; k < kLoads / kBoth; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x020, kBoth, 0);  // VMEM read
-            }
+                for (int k = 0; k < kLoads; ++k) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // VMEM read
+                }
 #pragma unroll
-            for (int k = 0; k < kReads / kBoth; ++k) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, kBoth, 0);
+                for (int k = 0; k < kReads; ++k) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                }
+                __builtin_amdgcn_sched_group_barrier(0x008, kMfma - kLoads - kReads, 0);
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, kMfma - (kLoads + kReads) / kBoth, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
     } else {
@@ -331,10 +354,10 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
         };
         auto mfma = [&](int i, int j) { E::mfma(acc[i][j], fb[j][0], fb[j][1], fa[i][0], fa[i][1], sb[j], sa[i]); };
 #pragma unroll
-        for (int j = 0; j < FJ; ++j) take_b(0, j);
+        for (int j = 0; j < FJ; ++j) take_b(first, j);
 #pragma unroll
-        for (int i = 0; i < H; ++i) take_a(0, i);
-        for (int s = 0; s < nk; ++s) {
+        for (int i = 0; i < H; ++i) take_a(first, i);
+        for (int s = first; s < end; ++s) {
             // the upper rows; the lower rows' fragments are read behind each group of MFMAs
 #pragma unroll
             for (int i = 0; i < H; ++i) {
@@ -347,10 +370,10 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
             }
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-            wait_vmcnt<0>();
+            wait_vmcnt<(NB - 2) * G::kDmaPerStage>();
             barrier();
             if ((s & 15) == 0) dma_scales((s >> 4) + 1);
-            dma(s + 2);
+            dma(s + NB);
             // the lower rows column by column; column j's fragments and those of upper row j follow it
 #pragma unroll
             for (int j = 0; j < FJ; ++j) {
@@ -368,8 +391,43 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
     wait_vmcnt<0>();
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     barrier();
+    if (op.splits > 1) {
+        f32x4 *out = op.partials + partial_at<G>(op, blockIdx.y) + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) out[(i * FJ + j) * 64 * G::NW] = acc[i][j];
+        return;
+    }
     epi.template run<G>(acc, w, op, lds);
 #endif
+}
+
+// The sums of a split contraction, in their order (so that the result does not depend on which workgroup
+// came first), and the epilogue.
+template <class G, class Epi>
+__global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void finish_kernel(Operands op, Epi epi)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kRingBytes];
+    Where w;
+    locate<G, Epi::kSym>(blockIdx.x, op.tiles_m, op.tiles_n, w.m0, w.n0);
+    w.batch = blockIdx.z;
+    w.lane = threadIdx.x & 63;
+    w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    w.row0 = w.wave % G::kWavesM * G::kWaveRows;
+    w.col0 = w.wave / G::kWavesM * G::kWaveCols;
+    f32x4 acc[G::FI][G::FJ];
+    for (int y = 0; y < op.splits; ++y) {
+        const f32x4 *in = op.partials + partial_at<G>(op, y) + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < G::FI; ++i)
+#pragma unroll
+            for (int j = 0; j < G::FJ; ++j) {
+                const f32x4 v = in[(i * G::FJ + j) * 64 * G::NW];
+                acc[i][j] = y == 0 ? v : acc[i][j] + v;
+            }
+    }
+    epi.template run<G>(acc, w, op, lds);
 }
 
 // ------------------------------------------------------------------------- plain epilogue -----
@@ -471,70 +529,155 @@ struct StoreEpi {
 };
 
 // ------------------------------------------------------------------- 16-bit tiles, two ways ---
+// A block of the wavefront's tile (64 x 64, or all of a smaller one) as 16-bit values in the LDS, lines of
+// kLine bytes whose 16-byte chunks are XOR-permuted by the line's upper bits.
+template <class G>
+struct Block16 {
+    static constexpr int kRows = G::kWaveRows < 64 ? G::kWaveRows : 64, kCols = G::kWaveCols;
+    static_assert(kCols <= 64 && kRows == kCols && G::kWaveRows % kRows == 0, "square blocks as wide as the wave tile");
+    static constexpr int kLine = kCols * 2, kChunks = kLine / 16, kBytes = kRows * kLine;
+    static constexpr int kBlocks = G::kWaveRows / kRows, BI = kRows / 16;
+    static constexpr int kLinesPerPass = 64 / kChunks, kPasses = kRows / kLinesPerPass;
+    static_assert(G::NW * 2 * kBytes <= G::kRingBytes, "two blocks per wavefront");
+    static __device__ __forceinline__ int chunk(int line, int c) { return line * kLine + 16 * (c ^ ((line >> 1) & (kChunks - 1))); }
+    // four consecutive values at (line, col), col a multiple of 4
+    static __device__ __forceinline__ int quad(int line, int col) { return chunk(line, col >> 3) + 2 * (col & 4); }
+
+    // the wavefront's whole lines between the block and memory: pass p of a lane
+    static __device__ __forceinline__ int line_of(int lane, int p) { return kLinesPerPass * p + lane / kChunks; }
+    static __device__ __forceinline__ int chunk_of(int lane) { return lane % kChunks; }
+    static __device__ __forceinline__ void to_memory(const uint8_t *block, int lane, uint16_t *at, int64_t ld)
+    {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const int l = line_of(lane, p), c = chunk_of(lane);
+            *reinterpret_cast<u32x4 *>(at + l * ld + 8 * c) = *reinterpret_cast<const u32x4 *>(block + chunk(l, c));
+        }
+    }
+    static __device__ __forceinline__ void from_memory(u32x4 (&v)[kPasses], int lane, const uint16_t *at, int64_t ld)
+    {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) v[p] = *reinterpret_cast<const u32x4 *>(at + line_of(lane, p) * ld + 8 * chunk_of(lane));
+    }
+    static __device__ __forceinline__ void put(uint8_t *block, int lane, const u32x4 (&v)[kPasses])
+    {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) *reinterpret_cast<u32x4 *>(block + chunk(line_of(lane, p), chunk_of(lane))) = v[p];
+    }
+    // Four values of one row, packed in two words, into the block `turned` (transposed): a lane swaps two of
+    // its four columns against its neighbour's row, so that it holds two rows of two columns and
+    // writes words.
+    static __device__ __forceinline__ void put_turned(uint8_t *turned, int row, int col, uint32_t lo, uint32_t hi)
+    {
+        const bool odd = row & 1;
+        const uint32_t give = odd ? lo : hi;
+        const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
+        // even lanes: columns 0, 1 of rows r, r + 1; odd lanes: columns 2, 3 of rows r - 1, r
+        const uint32_t up = odd ? got : lo, dn = odd ? hi : got;   // the upper and the lower row's pair
+        const int c = col + (odd ? 2 : 0), r = row & ~1;
+        *reinterpret_cast<uint32_t *>(turned + chunk(c, r >> 3) + 2 * (r & 7)) = __builtin_amdgcn_perm(dn, up, 0x05040100u);
+        *reinterpret_cast<uint32_t *>(turned + chunk(c + 1, r >> 3) + 2 * (r & 7)) = __builtin_amdgcn_perm(dn, up, 0x07060302u);
+    }
+};
+
 // Writes the wavefront's part of the tile as 16-bit values, row-major at rows[m][ld_rows] and (cols !=
 // nullptr) transposed at cols[n][ld_cols], m and n counted from the matrix' origin; every element of
-// the tile has its place in both. pack makes two values one word; val(i, j) gives the four
-// values of acc[i][j]. 64 x 64 blocks pass through the LDS in both orientations, 8 KB each, so that
-// a store instruction writes whole 128-byte lines of either. For the transposed block a lane
-// swaps two of its four columns against its neighbour's row, so that it holds two rows of two
-// columns and writes words.
+// the tile has its place in both. pack makes two values one word; val(i, j) gives the four values of
+// acc[i][j]. Blocks pass through the LDS in both orientations, so that a store instruction writes
+// whole lines of either.
 template <class G, class Pack, class Val>
 __device__ __forceinline__ void store_tile16(const Where &w, uint8_t *lds, Pack pack, Val val, uint16_t *rows, int64_t ld_rows,
                                              uint16_t *cols, int64_t ld_cols)
 {
-    static_assert(G::FJ == 4 && G::FI % 4 == 0, "64 x 64 blocks");
-    static_assert(G::NW * 16384 <= G::kRingBytes, "two staged blocks per wavefront");
+    using B = Block16<G>;
     const int r = w.lane & 15, q = w.lane >> 4;
-    const bool odd = r & 1;
-    uint8_t *tile = lds + w.wave * 16384, *turned = tile + 8192;
+    uint8_t *tile = lds + w.wave * 2 * B::kBytes, *turned = tile + B::kBytes;
 #pragma unroll
-    for (int blk = 0; blk < G::FI / 4; ++blk) {
+    for (int blk = 0; blk < B::kBlocks; ++blk) {
 #pragma unroll
-        for (int ii = 0; ii < 4; ++ii)
+        for (int ii = 0; ii < B::BI; ++ii)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x4 v = val(4 * blk + ii, j);
+            for (int j = 0; j < G::FJ; ++j) {
+                const f32x4 v = val(B::BI * blk + ii, j);
                 const uint32_t lo = pack(v[0], v[1]), hi = pack(v[2], v[3]);
                 const int row = 16 * ii + r, col = 16 * j + 4 * q;
-                *reinterpret_cast<u32x2 *>(tile + row * 128 + 16 * ((col >> 3) ^ ((row >> 1) & 7)) + 8 * (q & 1)) =
-                    u32x2{lo, hi};
-                if (cols) {
-                    const uint32_t give = odd ? lo : hi;
-                    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
-                    // even lanes: columns 0, 1 of rows r, r + 1; odd lanes: columns 2, 3 of rows r - 1, r
-                    const uint32_t up = odd ? got : lo, dn = odd ? hi : got;   // the upper and the lower row's pair
-                    const uint32_t c0 = __builtin_amdgcn_perm(dn, up, 0x05040100u);
-                    const uint32_t c1 = __builtin_amdgcn_perm(dn, up, 0x07060302u);
-                    const int c = col + (odd ? 2 : 0), at = 2 * (row & ~1);
-                    const int swizzled = (at & 15) | (((at >> 4) ^ ((c >> 1) & 7)) << 4);   // c and c + 1 alike: c is even
-                    *reinterpret_cast<uint32_t *>(turned + c * 128 + swizzled) = c0;
-                    *reinterpret_cast<uint32_t *>(turned + (c + 1) * 128 + swizzled) = c1;
-                }
+                *reinterpret_cast<u32x2 *>(tile + B::quad(row, col)) = u32x2{lo, hi};
+                if (cols) B::put_turned(turned, row, col, lo, hi);
             }
-        const int64_t m = w.m0 + w.row0 + 64 * blk, n = w.n0 + w.col0;
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            const int line = 8 * p + (w.lane >> 3), chunk = w.lane & 7;
-            const u32x4 a = *reinterpret_cast<const u32x4 *>(tile + line * 128 + 16 * (chunk ^ ((line >> 1) & 7)));
-            *reinterpret_cast<u32x4 *>(rows + (m + line) * ld_rows + n + 8 * chunk) = a;
-            if (cols) {
-                const u32x4 b = *reinterpret_cast<const u32x4 *>(turned + line * 128 + 16 * (chunk ^ ((line >> 1) & 7)));
-                *reinterpret_cast<u32x4 *>(cols + (n + line) * ld_cols + m + 8 * chunk) = b;
-            }
-        }
+        const int64_t m = w.m0 + w.row0 + B::kRows * blk, n = w.n0 + w.col0;
+        B::to_memory(tile, w.lane, rows + m * ld_rows + n, ld_rows);
+        if (cols) B::to_memory(turned, w.lane, cols + n * ld_cols + m, ld_cols);
     }
 }
 
 // ---------------------------------------------------------------------------------- launch ----
+// What runs a product: the tile and how many workgroups share a tile's contraction.
+struct Plan {
+    int geo;      // 0 Big, 1 Small, 2 Tiny
+    int splits, per;
+    int64_t tiles;
+    size_t partial_bytes;
+};
+constexpr int kTileSide[3] = {256, 128, 64};
+
+inline int64_t count_tiles(int64_t M, int64_t N, bool sym, int side)
+{
+    const int64_t tm = (M + side - 1) / side, tn = (N + side - 1) / side;
+    return sym ? tm * (tm + 1) / 2 : tm * tn;
+}
+
+// The plan with the least time by a simple account (measured, in microseconds): a workgroup spends so
+// much on each stage, and so much before and behind them; workgroups beyond what the chip holds at a time
+// wait for another round; partial sums cost a launch and their way through memory.
+inline Plan plan_product(int64_t M, int64_t N, int64_t nk, bool sym, int64_t batch, bool may_split)
+{
+    constexpr double kStage[3] = {1.35, 0.80, 0.33}, kEnds[3] = {9.0, 6.0, 4.0};
+    constexpr int kSlots[3] = {kComputeUnits, 2 * kComputeUnits, 2 * kComputeUnits};
+    Plan best{};
+    double least = 0.0;
+    if (nk < 1) nk = 1;   // an empty contraction asks for no workspace
+    for (int g = 0; g < 3; ++g) {
+        const int64_t tiles = count_tiles(M, N, sym, kTileSide[g]) * batch;
+        for (int s = 1; s <= 16; s = s < 4 ? s + 1 : s + 2) {
+            if (s > 1 && (!may_split || nk / s < 4)) break;
+            const int64_t per = (nk + s - 1) / s, used = (nk + per - 1) / per;
+            const double rounds = (double)((tiles * used + kSlots[g] - 1) / kSlots[g]);
+            const double bytes = used > 1 ? (double)tiles * used * kTileSide[g] * kTileSide[g] * 4 : 0.0;
+            const double t = rounds * ((double)per * kStage[g] + kEnds[g]) + (used > 1 ? 5.0 + bytes * 2 / 4.0e6 : 0.0);
+            if (best.splits == 0 || t < least) {
+                least = t;
+                best = Plan{g, (int)used, (int)per, tiles, (size_t)bytes};
+            }
+        }
+    }
+    return best;
+}
+
 template <class E, class G, class Epi>
-hipError_t launch_product(Operands op, const Epi &epi, int batch, hipStream_t stream)
+hipError_t launch_planned(Operands op, const Epi &epi, int batch, const Plan &plan, void *partials, hipStream_t stream)
 {
     op.tiles_m = (op.M + G::kTileM - 1) / G::kTileM;
     op.tiles_n = (op.N + G::kTileN - 1) / G::kTileN;
     const int64_t tiles = Epi::kSym ? (int64_t)op.tiles_m * (op.tiles_m + 1) / 2 : (int64_t)op.tiles_m * op.tiles_n;
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
-    return launch(product_kernel<E, G, Epi>, dim3((unsigned)tiles, 1, (unsigned)batch), dim3(64 * G::NW), 0, stream, op,
-                  epi);
+    op.splits = plan.splits;
+    op.per = plan.per;
+    op.partials = static_cast<f32x4 *>(partials);
+    const hipError_t e = launch(product_kernel<E, G, Epi>, dim3((unsigned)tiles, (unsigned)plan.splits, (unsigned)batch),
+                                dim3(64 * G::NW), 0, stream, op, epi);
+    if (e != hipSuccess || plan.splits == 1) return e;
+    return launch(finish_kernel<G, Epi>, dim3((unsigned)tiles, 1, (unsigned)batch), dim3(64 * G::NW), 0, stream, op, epi);
+}
+
+// partials: room for plan.partial_bytes (NULL when the plan does not split)
+template <class E, class Epi>
+hipError_t launch_product(const Operands &op, const Epi &epi, int batch, const Plan &plan, void *partials, hipStream_t stream)
+{
+    switch (plan.geo) {
+    case 0: return launch_planned<E, Big>(op, epi, batch, plan, partials, stream);
+    case 1: return launch_planned<E, Small>(op, epi, batch, plan, partials, stream);
+    default: return launch_planned<E, Tiny>(op, epi, batch, plan, partials, stream);
+    }
 }
 
 }  // namespace slab

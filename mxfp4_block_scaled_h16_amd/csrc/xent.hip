@@ -9,6 +9,8 @@
 // orientations; dX = G W adds up over the pieces in FP32, dW = G^T X has its rows of the piece written
 // once. The second operands of these are FP16 copies of W's piece and of X, transposed, so that every
 // product contracts along rows.
+#include <algorithm>
+
 #include "mx_device.h"
 #include "slab_gemm.h"
 #include "train_internal.h"
@@ -206,35 +208,59 @@ struct GradEpi {
 };
 
 // ---------------------------------------------------------------------------- ranges ----------
-constexpr int kRangeBlocks = 256;   // partial maxima of each of the three
+constexpr int kRangeBlocks = 1024;   // at most so many partial maxima, of each of the three
+constexpr int kRangeChunk = 8192;    // values of a row that a workgroup takes at a time
 
 __device__ __forceinline__ float block_max(float v)
 {
     __shared__ float slots[4];
     for (int k = 32; k >= 1; k >>= 1) v = fmaxf(v, __shfl_xor(v, k));
+    __syncthreads();   // slots may still be read from the call before
     if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
     __syncthreads();
     return fmaxf(fmaxf(slots[0], slots[1]), fmaxf(slots[2], slots[3]));
 }
 
-// largest |value| of a bf16 matrix over this workgroup's rows; a NaN or infinity counts as infinity
-__device__ __forceinline__ float rows_max(const uint16_t *p, int64_t ld, int64_t rows, int64_t cols, int64_t block, int64_t blocks,
-                                          bool vec, const RowWeights &weights)
+// Largest |value| of a bf16 matrix over this workgroup's share of it; a NaN or infinity counts as infinity.
+// Bound by memory, 2 bytes a value. vec: 16-byte aligned rows of whole 16 bytes.
+__device__ __forceinline__ float share_max(const uint16_t *p, int64_t ld, int64_t rows, int64_t cols, bool vec,
+                                           const RowWeights &weights)
 {
+    const int tid = threadIdx.x;
     uint32_t top = 0;
-    if (vec) {   // 16-byte aligned rows of whole 16 bytes: a wavefront's lanes read consecutive ones
-        const int64_t per_row = cols / 8, total = rows * per_row;
-        for (int64_t i = block * 256 + threadIdx.x; i < total; i += blocks * 256) {
-            const int64_t row = i / per_row;
-            if (!weights.live(row)) continue;
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(p + row * ld + (i - row * per_row) * 8);
+    const auto see = [&](uint32_t w) { top = max(max(top, w & 0x7FFFu), (w >> 16) & 0x7FFFu); };
+    if (vec && !weights.target && ld == cols) {   // one row of everything
+        const int64_t n = rows * cols / 8, step = (int64_t)gridDim.x * 256;
+        int64_t i = (int64_t)blockIdx.x * 256 + tid;
+        for (; i + 3 * step < n; i += 4 * step) {
+            u32x4 v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(max(top, v[e] & 0x7FFFu), (v[e] >> 16) & 0x7FFFu);
+            for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const u32x4 *>(p + (i + u * step) * 8);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) see(v[u][e]);
+        }
+        for (; i < n; i += step) {
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(p + i * 8);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) see(v[e]);
         }
     } else {
-        for (int64_t i = block * 256 + threadIdx.x; i < rows * cols; i += blocks * 256) {
-            const int64_t row = i / cols;
-            if (weights.live(row)) top = max(top, (uint32_t)p[row * ld + i - row * cols] & 0x7FFFu);
+        const int64_t chunks = (cols + kRangeChunk - 1) / kRangeChunk;
+        for (int64_t b = blockIdx.x; b < rows * chunks; b += gridDim.x) {
+            const int64_t row = chunks == 1 ? b : b / chunks, c0 = chunks == 1 ? 0 : (b - row * chunks) * kRangeChunk;
+            if (!weights.live(row)) continue;
+            const int64_t end = c0 + kRangeChunk < cols ? c0 + kRangeChunk : cols;
+            const uint16_t *src = p + row * ld;
+            if (vec)
+                for (int64_t c = c0 + 8 * tid; c < end; c += 2048) {
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(src + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) see(v[e]);
+                }
+            else
+                for (int64_t c = c0 + tid; c < end; c += 256) see(src[c]);
         }
     }
     return __uint_as_float(min(top, 0x7F80u) << 16);
@@ -244,29 +270,29 @@ __device__ __forceinline__ float rows_max(const uint16_t *p, int64_t ld, int64_t
 __global__ __launch_bounds__(256) void range_kernel(const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw, int64_t T,
                                                     int64_t K, int64_t V, int vec, RowWeights weights, float *part)
 {
-    const int64_t b = blockIdx.x;
     float top = 0.0f;
-    for (int64_t t = b * 256 + threadIdx.x; t < T; t += (int64_t)gridDim.x * 256) {
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < T; t += (int64_t)gridDim.x * 256) {
         float dl, dp;
         weights.of(t, dl, dp);
         top = fmaxf(top, fabsf(dl) + fabsf(dp));
     }
-    top = block_max(top);
-    if (threadIdx.x == 0) part[b] = top;
-    __syncthreads();
-    top = block_max(rows_max(x, ldx, T, K, b, gridDim.x, vec, weights));
-    if (threadIdx.x == 0) part[kRangeBlocks + b] = top;
-    __syncthreads();
-    top = block_max(rows_max(w, ldw, V, K, b, gridDim.x, vec, RowWeights{}));
-    if (threadIdx.x == 0) part[2 * kRangeBlocks + b] = top;
+    const float g = block_max(top);
+    const float tx = block_max(share_max(x, ldx, T, K, vec, weights));
+    const float tw = block_max(share_max(w, ldw, V, K, vec, RowWeights{}));
+    if (threadIdx.x == 0) {
+        part[blockIdx.x] = g;
+        part[kRangeBlocks + blockIdx.x] = tx;
+        part[2 * kRangeBlocks + blockIdx.x] = tw;
+    }
 }
 
 __global__ __launch_bounds__(256) void join_ranges_kernel(const float *part, int blocks, Ranges *out)
 {
     float s[3];
     for (int k = 0; k < 3; ++k) {
-        s[k] = range_scale(block_max((int)threadIdx.x < blocks ? part[k * kRangeBlocks + threadIdx.x] : 0.0f));
-        __syncthreads();
+        float top = 0.0f;
+        for (int i = threadIdx.x; i < blocks; i += 256) top = fmaxf(top, part[k * kRangeBlocks + i]);
+        s[k] = range_scale(block_max(top));
     }
     if (threadIdx.x == 0) *out = Ranges{s[0], s[1], s[2], {1.0f / s[0], 1.0f / s[2]}, {1.0f / s[0], 1.0f / s[1]}};
 }
@@ -341,9 +367,6 @@ hipError_t turn(const void *in, int64_t ld_in, int64_t rows, int64_t cols, const
 }
 
 // ------------------------------------------------------------------------------ workspace -----
-// tiles of 256 x 256 where there are enough of them, else of 128 x 128
-bool big_tiles(int64_t M, int64_t N) { return ((M + 255) / 256) * ((N + 255) / 256) > kComputeUnits / 2; }
-
 // Pieces of the vocabulary: G takes at most 256 MB per orientation, so that a piece stays near the
 // last-level cache, and a piece has at least 2048 columns.
 int64_t piece_columns(int64_t T, int64_t V)
@@ -374,6 +397,7 @@ struct Layout {
     Ranges *ranges;
     uint16_t *xt, *wt, *g, *gt;
     float *dx;
+    void *partials;      // of products whose contraction is split
 };
 Layout carve(Carve &c, int64_t T, int64_t K, int64_t V, bool backward)
 {
@@ -384,7 +408,8 @@ Layout carve(Carve &c, int64_t T, int64_t K, int64_t V, bool backward)
         l.wp = static_cast<uint16_t *>(c.take(2 * V * kp));
     }
     if (!backward) {
-        l.part = static_cast<float2 *>(c.take(8 * T * ((V + 127) / 128)));
+        const int64_t side = kTileSide[plan_product(T, V, kp / 64, false, 1, false).geo];
+        l.part = static_cast<float2 *>(c.take(8 * T * ((V + side - 1) / side)));
         l.zt = static_cast<float *>(c.take(4 * T));
         return l;
     }
@@ -396,6 +421,16 @@ Layout carve(Carve &c, int64_t T, int64_t K, int64_t V, bool backward)
     l.g = static_cast<uint16_t *>(c.take(2 * tp * vc));
     l.gt = static_cast<uint16_t *>(c.take(2 * tp * vc));
     l.dx = static_cast<float *>(c.take(4 * T * round_up(K, 4)));
+    // the plans of every piece's products: full ones and the last, whose contraction ends with a tile of
+    // one of three sizes
+    size_t most = 0;
+    const int64_t rest = V % vc ? V % vc : vc;
+    for (const int64_t cols : {vc < V ? vc : V, rest})
+        for (const int64_t side : kTileSide) {
+            most = std::max(most, plan_product(T, K, round_up(cols, side) / 64, false, 1, true).partial_bytes);
+            most = std::max(most, plan_product(cols, K, round_up(T, side) / 64, false, 1, true).partial_bytes);
+        }
+    l.partials = c.take(most);
     return l;
 }
 
@@ -449,10 +484,9 @@ hipError_t launch_xent_forward(const XentProblem &p, void *ws, float *loss, floa
     if (hipError_t e = logits_operands(p, l, op, stream)) return e;
     op.N = (int)p.V;
     const StatsEpi epi{l.part, l.zt, p.target};
-    const bool big = big_tiles(p.T, p.V);
-    if (hipError_t e = big ? launch_product<BF16, Big>(op, epi, 1, stream) : launch_product<BF16, Small>(op, epi, 1, stream))
-        return e;
-    const int tiles = (int)((p.V + (big ? 255 : 127)) / (big ? 256 : 128));
+    const Plan plan = plan_product(p.T, p.V, op.nk, false, 1, false);
+    if (hipError_t e = launch_product<BF16>(op, epi, 1, plan, nullptr, stream)) return e;
+    const int tiles = (int)((p.V + kTileSide[plan.geo] - 1) / kTileSide[plan.geo]);
     return launch(xent_join_kernel, dim3((unsigned)((p.T + 31) / 32)), dim3(256), 0, stream, l.part, tiles, (int)p.T, p.V,
                   l.zt, p.target, p.ignore_index, loss, lse);
 }
@@ -468,7 +502,7 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
     const RowWeights weights{dloss, dlse, p.target, p.ignore_index, p.V};
     const bool vec = p.K % 8 == 0 && p.ldx % 8 == 0 && p.ldw % 8 == 0 && (uintptr_t)p.x % 16 == 0 && (uintptr_t)p.w % 16 == 0;
     const int64_t work = (p.T + p.V) * p.K;
-    const int blocks = (int)(work > 4096 * kRangeBlocks ? kRangeBlocks : work / 4096 + 1);
+    const int blocks = (int)(work > 8192 * kRangeBlocks ? kRangeBlocks : work / 8192 + 1);
     if (hipError_t e = launch(range_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, static_cast<const uint16_t *>(p.x), p.ldx,
                               static_cast<const uint16_t *>(p.w), p.ldw, p.T, p.K, p.V, vec ? 1 : 0, weights, l.range_part))
         return e;
@@ -483,11 +517,10 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
         op.b = lo.b + v0 * lo.ldb;
         op.N = (int)cols;
         const GradEpi epi{weights, lse, v0, l.ranges, l.g, l.gt, vc, tp};
-        const bool big = big_tiles(p.T, cols);
-        if (hipError_t e = big ? launch_product<BF16, Big>(op, epi, 1, stream) : launch_product<BF16, Small>(op, epi, 1, stream))
-            return e;
+        const Plan plan = plan_product(p.T, cols, op.nk, false, 1, false);
+        if (hipError_t e = launch_product<BF16>(op, epi, 1, plan, nullptr, stream)) return e;
         // G covers whole tiles; the products over it run to the end of the last one
-        const int64_t step = big ? 256 : 128;
+        const int64_t step = kTileSide[plan.geo];
         const int64_t cols_done = round_up(cols, step), rows_done = round_up(p.T, step);
         if (dx) {
             if (hipError_t e = turn(static_cast<const uint16_t *>(p.w) + v0 * p.ldw, p.ldw, cols, p.K, &l.ranges->w, l.wt, vc,
@@ -501,10 +534,8 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             q.M = (int)p.T;
             q.N = (int)p.K;
             q.nk = (int)(cols_done / 64);
-            auto run = [&](const auto &e) {
-                return big_tiles(p.T, p.K) ? launch_product<F16, Big>(q, e, 1, stream)
-                                           : launch_product<F16, Small>(q, e, 1, stream);
-            };
+            const Plan how = plan_product(p.T, p.K, q.nk, false, 1, true);
+            auto run = [&](const auto &e) { return launch_product<F16>(q, e, 1, how, l.partials, stream); };
             const float *add = first ? nullptr : l.dx;
             hipError_t e;
             if (!last)
@@ -524,10 +555,8 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             q.M = (int)cols;
             q.N = (int)p.K;
             q.nk = (int)(rows_done / 64);
-            auto run = [&](const auto &e) {
-                return big_tiles(cols, p.K) ? launch_product<F16, Big>(q, e, 1, stream)
-                                            : launch_product<F16, Small>(q, e, 1, stream);
-            };
+            const Plan how = plan_product(cols, p.K, q.nk, false, 1, true);
+            auto run = [&](const auto &e) { return launch_product<F16>(q, e, 1, how, l.partials, stream); };
             const hipError_t e =
                 dw_bf16 ? run(StoreEpi<true>{static_cast<uint16_t *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, l.ranges->inv_gx})
                         : run(StoreEpi<false>{static_cast<float *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, l.ranges->inv_gx});

@@ -77,6 +77,8 @@ def test_fp8_linear_refusals(L, name):
     need = L.mxfp4_fp8_linear_workspace_bytes({"fprop": 0, "dgrad": 1, "wgrad": 2}[name], 32, 64, 96)
     assert need > 0 and call(n=need - 1) == WORKSPACE
     assert call(N=0, M=0, a=None, b=None, out=None) == 0
+    for sizes in ((0, 64, 32), (64, 0, 32), (64, 32, 0), (0, 0, 0)):     # an empty product of every pass
+        assert all(L.mxfp4_fp8_linear_workspace_bytes(p, *sizes) < 1 << 20 for p in range(3))
     assert L.mxfp4_fp8_linear_workspace_bytes(7, 32, 64, 96) == 0 and L.mxfp4_fp8_linear_workspace_bytes(0, -1, 64, 96) == 0
 
 
