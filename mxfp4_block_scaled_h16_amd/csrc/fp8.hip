@@ -59,9 +59,19 @@ typedef f32x4 f32x4_any __attribute__((aligned(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 template <bool F32>
+__device__ __forceinline__ float load1(const Fp8Input &it, int64_t at)
+{
+    if constexpr (F32)
+        return static_cast<const float *>(it.x)[at];
+    else
+        return bf16_lo(static_cast<const uint16_t *>(it.x)[at]);
+}
+
+// RAGGED: a row may end within these eight
+template <bool F32, bool RAGGED>
 __device__ __forceinline__ void load8(const Fp8Input &it, int64_t row, int64_t col, float (&v)[8])
 {
-    if (row < it.rows && col + 8 <= it.cols) {
+    if (row < it.rows && (RAGGED ? col + 8 <= it.cols : col < it.cols)) {
         if constexpr (F32) {
             const float *p = static_cast<const float *>(it.x) + row * it.ldx + col;
             const f32x4 a = *reinterpret_cast<const f32x4_any *>(p), b = *reinterpret_cast<const f32x4_any *>(p + 4);
@@ -81,18 +91,18 @@ __device__ __forceinline__ void load8(const Fp8Input &it, int64_t row, int64_t c
         }
         return;
     }
+    // the end of a row, value by value
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         v[e] = 0.0f;
-        if (row < it.rows && col + e < it.cols) {
-            if constexpr (F32)
-                v[e] = static_cast<const float *>(it.x)[row * it.ldx + col + e];
-            else
-                v[e] = bf16_lo(static_cast<const uint16_t *>(it.x)[row * it.ldx + col + e]);
-        }
+        if constexpr (RAGGED)
+            if (row < it.rows && col + e < it.cols) v[e] = load1<F32>(it, row * it.ldx + col + e);
     }
 }
 
+// F32: the tensors' type. RAGGED: some row's length is no multiple of eight (its end is then read value by
+// value, in code that the others need not fetch).
+template <bool F32, bool RAGGED>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(Fp8Args args)
 {
     __shared__ uint32_t cmax[16][128 + 4];
@@ -107,13 +117,8 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(Fp8Args args)
     const int64_t row0 = tm * 128 + 8 * rg, col0 = tn * 128 + 8 * cg;
 
     float v[8][8];
-    if (it.f32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load8<true>(it, row0 + i, col0, v[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) load8<false>(it, row0 + i, col0, v[i]);
-    }
+    for (int i = 0; i < 8; ++i) load8<F32, RAGGED>(it, row0 + i, col0, v[i]);
     uint32_t rmax[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) rmax[i] = row16_max(amax_bits<8>(v[i]));
@@ -229,7 +234,14 @@ hipError_t launch_fp8_quantize(const Fp8Input *items, int count, hipStream_t str
     if (n == 0) return hipSuccess;
     if (total > INT32_MAX) return hipErrorInvalidValue;
     for (int i = n; i <= kFp8Group; ++i) args.first[i] = (int)total;
-    return launch(fp8_quantize_kernel, dim3((unsigned)total), dim3(256), 0, stream, args);
+    bool ragged = false;
+    for (int i = 0; i < n; ++i) ragged = ragged || args.item[i].cols % 8 != 0;
+    const dim3 grid((unsigned)total), block(256);
+    if (args.item[0].f32)
+        return ragged ? launch(fp8_quantize_kernel<true, true>, grid, block, 0, stream, args)
+                      : launch(fp8_quantize_kernel<true, false>, grid, block, 0, stream, args);
+    return ragged ? launch(fp8_quantize_kernel<false, true>, grid, block, 0, stream, args)
+                  : launch(fp8_quantize_kernel<false, false>, grid, block, 0, stream, args);
 }
 
 size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K)

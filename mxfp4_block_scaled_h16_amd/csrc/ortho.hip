@@ -30,13 +30,16 @@ constexpr float kLoScale = 2048.0f, kLoUnscale = 1.0f / 2048.0f;   // the remain
 
 __device__ __forceinline__ uint16_t f16_bits(float x) { return __builtin_bit_cast(uint16_t, (_Float16)x); }
 __device__ __forceinline__ float f16_float(uint16_t b) { return (float)__builtin_bit_cast(_Float16, b); }
-[[maybe_unused]] __device__ __forceinline__ f32x4 f16_quad(const uint16_t *p)
+// eight FP16 values
+__device__ __forceinline__ void f16_eight(const u32x4 &w, f32x4 (&v)[2])
 {
-    const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
-    // copied out first: a bit cast of a vector's element reads the vector's first one
-    const uint32_t first = w.x, second = w.y;
-    const f16x2 a = __builtin_bit_cast(f16x2, first), b = __builtin_bit_cast(f16x2, second);
-    return f32x4{(float)a[0], (float)a[1], (float)b[0], (float)b[1]};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t word = w[k];   // copied out first: a bit cast of a vector's element reads the vector's first one
+        const f16x2 two = __builtin_bit_cast(f16x2, word);
+        v[k / 2][2 * (k % 2)] = (float)two[0];
+        v[k / 2][2 * (k % 2) + 1] = (float)two[1];
+    }
 }
 
 // ------------------------------------------------------------------------- the epilogues ------
@@ -49,8 +52,11 @@ struct GramEpi {
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
     {
         uint16_t *o = out + w.batch * batch_out;
-        store_tile16<G>(w, lds, [](float a, float b) { return pack_f16(a, b); },
-                        [&](int i, int j) { return acc[i][j] * kUnscale; },
+        store_tile16<G>(acc, w, lds, [](float a, float b) { return pack_f16(a, b); }, [](int, int) { return 0; },
+                        [&](f32x4 (&v)[2], int, int, int) {
+                            v[0] *= kUnscale;
+                            v[1] *= kUnscale;
+                        },
                         o, ld, w.m0 == w.n0 ? nullptr : o, ld);
     }
 };
@@ -65,35 +71,37 @@ struct PolyEpi {
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
     {
-        using B = Block16<G>;
-        const int r = w.lane & 15, q = w.lane >> 4;
-        uint8_t *tile = lds + w.wave * 2 * B::kBytes, *turned = tile + B::kBytes;
-        const int64_t n = w.n0 + w.col0;
         const uint16_t *in = gram + w.batch * batch_out;
         uint16_t *o = out + w.batch * batch_out;
         const float cs = c * kUnscale;
-#pragma unroll
-        for (int blk = 0; blk < B::kBlocks; ++blk) {
-            const int64_t m = w.m0 + w.row0 + B::kRows * blk;
-            u32x4 v[B::kPasses];
-            B::from_memory(v, w.lane, in + m * ld + n, ld);
-            B::put(tile, w.lane, v);
-#pragma unroll
-            for (int ii = 0; ii < B::BI; ++ii)
-#pragma unroll
-                for (int j = 0; j < G::FJ; ++j) {
-                    const int row = 16 * ii + r, col = 16 * j + 4 * q;
-                    uint8_t *place = tile + B::quad(row, col);   // read and written by this lane alone
-                    const f32x4 p = b * f16_quad(reinterpret_cast<const uint16_t *>(place)) + cs * acc[B::BI * blk + ii][j];
-                    const uint32_t lo = pack_f16(p[0], p[1]), hi = pack_f16(p[2], p[3]);
-                    *reinterpret_cast<u32x2 *>(place) = u32x2{lo, hi};
-                    if (w.m0 != w.n0) B::put_turned(turned, row, col, lo, hi);
-                }
-            B::to_memory(tile, w.lane, o + m * ld + n, ld);
-            if (w.m0 != w.n0) B::to_memory(turned, w.lane, o + n * ld + m, ld);
-        }
+        store_tile16<G>(acc, w, lds, [](float x, float y) { return pack_f16(x, y); },
+                        [&](int m, int n) { return *reinterpret_cast<const u32x4 *>(in + (int64_t)m * ld + n); },
+                        [&](f32x4 (&v)[2], const u32x4 &gram8, int, int) {
+                            f32x4 g[2];
+                            f16_eight(gram8, g);
+                            v[0] = b * g[0] + cs * v[0];
+                            v[1] = b * g[1] + cs * v[1];
+                        },
+                        o, ld, w.m0 == w.n0 ? nullptr : o, ld);
     }
 };
+
+// eight values of X as they are kept
+struct TwoPart {
+    u32x4 hi, lo;
+    __device__ __forceinline__ void read(f32x4 (&x)[2]) const
+    {
+        f32x4 rest[2];
+        f16_eight(hi, x);
+        f16_eight(lo, rest);
+        x[0] += rest[0] * kLoUnscale;
+        x[1] += rest[1] * kLoUnscale;
+    }
+};
+__device__ __forceinline__ TwoPart two_part(const uint16_t *hi, const uint16_t *lo, int64_t at)
+{
+    return TwoPart{*reinterpret_cast<const u32x4 *>(hi + at), *reinterpret_cast<const u32x4 *>(lo + at)};
+}
 
 // a X + (b A + c A A) X in X's own orientation: value (both orientations) and remainder
 struct UpdateEpi {
@@ -106,44 +114,25 @@ struct UpdateEpi {
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds) const
     {
-        using B = Block16<G>;
-        const int r = w.lane & 15, q = w.lane >> 4;
-        uint8_t *tile = lds + w.wave * 2 * B::kBytes, *turned = tile + B::kBytes;
-        const int64_t base = w.batch * batch_x, n = w.n0 + w.col0;
+        const int64_t base = w.batch * batch_x;
+        store_tile16<G>(acc, w, lds, [](float x, float y) { return pack_f16(x, y); },
+                        [&](int m, int n) { return two_part(hi, lo, base + (int64_t)m * ld + n); },
+                        [&](f32x4 (&v)[2], const TwoPart &two, int m, int n) {
+                            f32x4 x[2];
+                            two.read(x);
+                            u32x4 rests;
 #pragma unroll
-        for (int blk = 0; blk < B::kBlocks; ++blk) {
-            const int64_t m = w.m0 + w.row0 + B::kRows * blk, at = base + m * ld + n;
-            u32x4 h[B::kPasses], l[B::kPasses];
-            B::from_memory(h, w.lane, hi + at, ld);
-            B::from_memory(l, w.lane, lo + at, ld);
-            B::put(tile, w.lane, h);
-            B::put(turned, w.lane, l);   // not turned yet: the remainders, row by row
+                            for (int k = 0; k < 2; ++k) {
+                                v[k] = a * x[k] + kUnscale * v[k];
+                                float rest[4];
 #pragma unroll
-            for (int ii = 0; ii < B::BI; ++ii)
-#pragma unroll
-                for (int j = 0; j < G::FJ; ++j) {
-                    const int place = B::quad(16 * ii + r, 16 * j + 4 * q);   // read and written by this lane alone
-                    const f32x4 x = f16_quad(reinterpret_cast<const uint16_t *>(tile + place)) +
-                                    f16_quad(reinterpret_cast<const uint16_t *>(turned + place)) * kLoUnscale;
-                    const f32x4 v = a * x + kUnscale * acc[B::BI * blk + ii][j];
-                    f32x4 rest;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) rest[t] = (v[t] - f16_float(f16_bits(v[t]))) * kLoScale;
-                    *reinterpret_cast<u32x2 *>(tile + place) = u32x2{pack_f16(v[0], v[1]), pack_f16(v[2], v[3])};
-                    *reinterpret_cast<u32x2 *>(turned + place) = u32x2{pack_f16(rest[0], rest[1]), pack_f16(rest[2], rest[3])};
-                }
-            B::to_memory(tile, w.lane, hi_out + at, ld);
-            B::to_memory(turned, w.lane, lo + at, ld);
-#pragma unroll
-            for (int ii = 0; ii < B::BI; ++ii)
-#pragma unroll
-                for (int j = 0; j < G::FJ; ++j) {
-                    const int row = 16 * ii + r, col = 16 * j + 4 * q;
-                    const u32x2 v = *reinterpret_cast<const u32x2 *>(tile + B::quad(row, col));
-                    B::put_turned(turned, row, col, v.x, v.y);
-                }
-            B::to_memory(turned, w.lane, turned_out + base + n * ld_turned + m, ld_turned);
-        }
+                                for (int t = 0; t < 4; ++t) rest[t] = (v[k][t] - f16_float(f16_bits(v[k][t]))) * kLoScale;
+                                rests[2 * k] = pack_f16(rest[0], rest[1]);
+                                rests[2 * k + 1] = pack_f16(rest[2], rest[3]);
+                            }
+                            *reinterpret_cast<u32x4 *>(lo + base + (int64_t)m * ld + n) = rests;
+                        },
+                        hi_out + base, ld, turned_out + base, ld_turned);
     }
 };
 
@@ -158,30 +147,14 @@ struct LastEpi {
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
     {
-        using B = Block16<G>;
-        const int r = w.lane & 15, q = w.lane >> 4;
-        uint8_t *tile = lds + w.wave * 2 * B::kBytes, *rests = tile + B::kBytes;
-#pragma unroll
-        for (int blk = 0; blk < B::kBlocks; ++blk) {
-            const int64_t at = w.batch * batch_x + (w.m0 + w.row0 + B::kRows * blk) * ld + w.n0 + w.col0;
-            u32x4 v[B::kPasses];
-            B::from_memory(v, w.lane, hi + at, ld);
-            B::put(tile, w.lane, v);
-            B::from_memory(v, w.lane, lo + at, ld);
-            B::put(rests, w.lane, v);
-#pragma unroll
-            for (int ii = 0; ii < B::BI; ++ii)
-#pragma unroll
-                for (int j = 0; j < G::FJ; ++j) {
-                    const int place = B::quad(16 * ii + r, 16 * j + 4 * q);
-                    const f32x4 x = f16_quad(reinterpret_cast<const uint16_t *>(tile + place)) +
-                                    f16_quad(reinterpret_cast<const uint16_t *>(rests + place)) * kLoUnscale;
-                    acc[B::BI * blk + ii][j] = a * x + kUnscale * acc[B::BI * blk + ii][j];
-                }
-        }
-        // the staged rows below reuse the LDS, part of it another wavefront's blocks until now
-        __syncthreads();
-        store.template run<G>(acc, w, op, lds);
+        const int64_t base = w.batch * batch_x;
+        store.template run_with<G>(acc, w, op, lds, [&](int m, int n) { return two_part(hi, lo, base + (int64_t)m * ld + n); },
+                                   [&](f32x4 (&v)[2], const TwoPart &two) {
+                                       f32x4 x[2];
+                                       two.read(x);
+                                       v[0] = a * x[0] + kUnscale * v[0];
+                                       v[1] = a * x[1] + kUnscale * v[1];
+                                   });
     }
 };
 

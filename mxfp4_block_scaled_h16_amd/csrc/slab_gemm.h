@@ -25,6 +25,7 @@
 #pragma once
 
 #include <climits>
+#include <utility>
 
 #include "internal.h"
 
@@ -110,14 +111,17 @@ struct Geo {
     static constexpr int kDmaPerStage = kDmaA + kDmaB;
     static_assert(kDmaA * kRowsPerDma * NW == TM && kDmaB * kRowsPerDma * NW == TN, "whole loads per wavefront");
     static_assert((TM + TN) / 64 <= NW, "at most one scale load per wavefront and group");
-    // LDS for staging the output: 32 rows of the wavefront's columns, rows 16 bytes apart
-    static constexpr int kEpiRow = kWaveCols * 4 + 16, kEpiWave = 32 * kEpiRow;
+    // a wavefront's part of the LDS in the epilogue: 32 rows of its tile in FP32, and transposed in 16 bits; behind
+    // all of them 16 bytes for each row of the tile
+    static constexpr int kBlockRows = 32;
+    static constexpr int kEpiWave = kBlockRows * kWaveCols * (4 + 2), kEpiBytes = NW * kEpiWave;
+    static constexpr int kRowInfo = kEpiBytes;
     template <class E>
     static constexpr int lds_bytes()
     {
-        return kRingBytes + (E::kScaled ? 2 * kScaleSlot : 0);
+        const int main = kRingBytes + (E::kScaled ? 2 * kScaleSlot : 0), epi = kEpiBytes + TM * 16;
+        return main > epi ? main : epi;
     }
-    static_assert(NW * kEpiWave <= kRingBytes, "the staged output reuses the ring");
     static constexpr int kMinBlocks = kRingBytes + 2 * kScaleSlot <= 80 * 1024 ? 2 : 1;   // workgroups per CU
 };
 using Big = Geo<8, 256, 256, 2>;       // wave tiles 128 x 64, 128 accumulator registers
@@ -151,7 +155,8 @@ struct Where {
 // Tile v of the grid. Consecutive workgroups go to the eight XCDs in turn; each XCD gets a contiguous
 // range of tiles, walked column by column in groups of row panels covering 1024 rows, so that the
 // workgroups running on one XCD share operand panels in its L2. SYM: only the tiles that touch
-// the lower triangle of a square of tiles, row by row.
+// the lower triangle of a square of tiles, in bands of four rows of tiles, each in squares of 4 x 4 and
+// what is left at the diagonal.
 template <class G, bool SYM>
 __device__ __forceinline__ void locate(int v, int tiles_m, int tiles_n, int &m0, int &n0)
 {
@@ -159,11 +164,22 @@ __device__ __forceinline__ void locate(int v, int tiles_m, int tiles_n, int &m0,
     const int per = total / 8, rem = total % 8, x = v % 8;
     const int t = x * per + min(x, rem) + v / 8;
     if constexpr (SYM) {
-        int i = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-        if ((i + 1) * (i + 2) / 2 <= t) ++i;     // the root may be a rounding off
-        if (i * (i + 1) / 2 > t) --i;
-        m0 = i * G::kTileM;
-        n0 = (t - i * (i + 1) / 2) * G::kTileN;
+        // band I holds 16 I + 10 tiles, the bands before it 8 I I + 2 I (a short last band fewer)
+        int band = (int)sqrtf((float)t * 0.125f);   // a start that the loops put right
+        while (8 * band * band + 2 * band > t) --band;
+        while (8 * (band + 1) * (band + 1) + 2 * (band + 1) <= t && 4 * (band + 1) < tiles_m) ++band;
+        const int in = t - (8 * band * band + 2 * band), high = min(4, tiles_m - 4 * band), square = 4 * high;
+        int i, j;
+        if (in < band * square) {
+            i = in % square % high;
+            j = in / square * 4 + in % square / high;
+        } else {
+            int rest = in - band * square;
+            for (i = 0; rest > i; ++i) rest -= i + 1;
+            j = 4 * band + rest;
+        }
+        m0 = (4 * band + i) * G::kTileM;
+        n0 = j * G::kTileN;
     } else {
         constexpr int kGroupRows = 1024 / G::kTileM;
         const int group = kGroupRows * tiles_n;
@@ -408,7 +424,7 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
 template <class G, class Epi>
 __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void finish_kernel(Operands op, Epi epi)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kRingBytes];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kEpiBytes + G::kTileM * 16];
     Where w;
     locate<G, Epi::kSym>(blockIdx.x, op.tiles_m, op.tiles_n, w.m0, w.n0);
     w.batch = blockIdx.z;
@@ -443,6 +459,53 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b)
 }
 __device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
 
+// A block of the wavefront's tile (32 rows) in FP32 in the LDS, 16-byte chunks
+// XOR-permuted by the line: 16 lanes that write one chunk of 16 lines, or read every other chunk of two,
+// meet 16 distinct bank groups.
+template <class G>
+struct Block32 {
+    static constexpr int kRows = G::kBlockRows, kCols = G::kWaveCols;
+    static constexpr int kLine = kCols * 4, kChunks = kLine / 16, kBytes = kRows * kLine;
+    static constexpr int kBlocks = G::kWaveRows / kRows, BI = kRows / 16;
+    // afterwards a lane takes eight columns of a line
+    static constexpr int kLanes = kCols / 8, kLinesPerPass = 64 / kLanes, kPasses = kRows / kLinesPerPass;
+    static_assert(kChunks == 16 || kChunks == 8, "the permutation below");
+    static __device__ __forceinline__ int chunk(int line, int c)
+    {
+        return line * kLine + 16 * (c ^ (kChunks == 16 ? line & 15 : (line >> 1) & 7));
+    }
+    static __device__ __forceinline__ void get(const uint8_t *block, int line, int c8, f32x4 (&v)[2])
+    {
+        v[0] = *reinterpret_cast<const f32x4 *>(block + chunk(line, 2 * c8));
+        v[1] = *reinterpret_cast<const f32x4 *>(block + chunk(line, 2 * c8 + 1));
+    }
+    // Block blk of the accumulators into the wavefront's part of the LDS. Registers have fixed names, so each
+    // block has code of its own; the empty statements behind them differ, so that the compiler does not
+    // make one piece of code with a variable index out of them (the accumulators would go to memory).
+    static __device__ __forceinline__ void put(uint8_t *block, int lane, const f32x4 (&acc)[G::FI][G::FJ], int blk)
+    {
+        put_blocks(block + (lane & 15) * kLine, lane, acc, blk, std::make_integer_sequence<int, kBlocks>());
+    }
+
+private:
+    template <int... K>
+    static __device__ __forceinline__ void put_blocks(uint8_t *line0, int lane, const f32x4 (&acc)[G::FI][G::FJ], int blk,
+                                                      std::integer_sequence<int, K...>)
+    {
+        ((K == blk ? put_one<K>(line0, lane, acc, std::make_integer_sequence<int, BI * G::FJ>()) : void()), ...);
+    }
+    template <int K, int... E>
+    static __device__ __forceinline__ void put_one(uint8_t *line0, int lane, const f32x4 (&acc)[G::FI][G::FJ],
+                                                   std::integer_sequence<int, E...>)
+    {
+        const int r = lane & 15, q = lane >> 4;
+        ((*reinterpret_cast<f32x4 *>(line0 + chunk(16 * (E / G::FJ) + r, 4 * (E % G::FJ) + q) - r * kLine) =
+              acc[BI * K + E / G::FJ][E % G::FJ]),
+         ...);
+        asm volatile("; block %0" ::"i"(K));
+    }
+};
+
 // c = alpha * A B^T + beta * c (+ add) in FP32 or bf16 (rounded once, after the sums); c is read only when
 // beta != 0, add (FP32 [M][ld_add], 16-byte aligned rows, readable up to a multiple of 4 columns) only
 // when it is not NULL. factors: NULL, or two powers of two in device memory that alpha is multiplied by.
@@ -459,42 +522,74 @@ struct StoreEpi {
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
     {
-        run_with<G>(w, op, lds, [&](int i, int j) { return acc[i][j]; });
+        run_with<G>(acc, w, op, lds, [](int, int) { return 0; }, [](f32x4 (&)[2], int) {});
     }
 
-    // val(i, j): what takes the place of acc[i][j]
-    template <class G, class Val>
-    __device__ __forceinline__ void run_with(const Where &w, const Operands &op, uint8_t *lds, Val val) const
+    // fetch(m, n): what make(v, fetched) wants to turn the product's eight values v at (m, n) into those that take
+    // their place; m and n lie in the tile
+    template <class G, class Fetch, class Make>
+    __device__ __forceinline__ void run_with(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds,
+                                             Fetch fetch, Make make) const
     {
-        const int r = w.lane & 15, q = w.lane >> 4;
-        uint8_t *epi = lds + w.wave * G::kEpiWave;
-        constexpr int kLanesPerRow = G::kWaveCols / 4, kRowsPerStore = 64 / kLanesPerRow;
-        constexpr int kElem = BF16_OUT ? 2 : 4;
-        const bool vec = ldc % 4 == 0 && (uintptr_t)c % (4 * kElem) == 0 && (batch_c % 4 == 0 || w.batch == 0);
-        const int cc = 4 * (w.lane % kLanesPerRow);
+        using B = Block32<G>;
+        uint8_t *block = lds + w.wave * G::kEpiWave;
         // one after the other: their product may leave FP32's range where the result does not
         const float f0 = factors ? alpha * factors[0] : alpha, f1 = factors ? factors[1] : 1.0f;
-        const int n = w.n0 + w.col0 + cc;
+        constexpr int kElem = BF16_OUT ? 2 : 4;
+        const bool vec = ldc % 8 == 0 && (uintptr_t)c % 16 == 0 && (batch_c % 8 == 0 || w.batch == 0);
+        // the whole tile in 16-byte stores of nothing but the product
+        const bool plain = vec && beta == 0.0f && !add && w.m0 + G::kTileM <= op.M && w.n0 + G::kTileN <= op.N;
+        const int line = w.lane / B::kLanes, c8 = w.lane % B::kLanes, n = w.n0 + w.col0 + 8 * c8;
+#pragma unroll 1
+        for (int blk = 0; blk < B::kBlocks; ++blk) {
+            // a block of the wavefront's rows through its part of the LDS (no barrier), so that a store
+            // instruction writes whole lines; one code for all blocks: it is fetched for one use
+            const int m = w.m0 + w.row0 + B::kRows * blk + line;
+            if (plain) {
+                decltype(fetch(0, 0)) got[B::kPasses];
 #pragma unroll
-        for (int i = 0; i < G::FI; i += 2) {
-            // 32 rows of the wavefront's columns through the LDS (its own part of it: no barrier),
-            // so that a store instruction writes whole rows
+                for (int p = 0; p < B::kPasses; ++p) got[p] = fetch(m + B::kLinesPerPass * p, n);
+                B::put(block, w.lane, acc, blk);
+                char *at = static_cast<char *>(c) + (w.batch * batch_c + (int64_t)m * ldc + n) * kElem;
 #pragma unroll
-            for (int ii = 0; ii < 2; ++ii)
+                for (int p = 0; p < B::kPasses; ++p) {
+                    f32x4 v[2];
+                    B::get(block, B::kLinesPerPass * p + line, c8, v);
+                    make(v, got[p]);
+                    v[0] = v[0] * f0 * f1;
+                    v[1] = v[1] * f0 * f1;
+                    if constexpr (BF16_OUT) {
+                        *reinterpret_cast<u32x4 *>(at) = u32x4{pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3]),
+                                                               pack_bf16(v[1][0], v[1][1]), pack_bf16(v[1][2], v[1][3])};
+                    } else {
+                        *reinterpret_cast<f32x4 *>(at) = v[0];
+                        *reinterpret_cast<f32x4 *>(at + 16) = v[1];
+                    }
+                    at += B::kLinesPerPass * ldc * kElem;
+                }
+            } else {
+                B::put(block, w.lane, acc, blk);
+#pragma unroll 1
+                for (int p = 0; p < B::kPasses; ++p) {
+                    const int mm = m + B::kLinesPerPass * p;
+                    if (mm >= op.M || n >= op.N) break;
+                    f32x4 v[2];
+                    B::get(block, B::kLinesPerPass * p + line, c8, v);
+                    make(v, fetch(mm, n));
 #pragma unroll
-                for (int j = 0; j < G::FJ; ++j)
-                    *reinterpret_cast<f32x4 *>(epi + (16 * ii + r) * G::kEpiRow + (16 * j + 4 * q) * 4) = val(i + ii, j);
-#pragma unroll
-            for (int p = 0; p < 32 / kRowsPerStore; ++p) {
-                const int rr = kRowsPerStore * p + w.lane / kLanesPerRow;
-                f32x4 v = *reinterpret_cast<const f32x4 *>(epi + rr * G::kEpiRow + cc * 4) * f0 * f1;
-                const int m = w.m0 + w.row0 + 16 * i + rr;
-                if (m < op.M && n < op.N && add) v += *reinterpret_cast<const f32x4 *>(add + (int64_t)m * ld_add + n);
-                if (m < op.M && n < op.N) put(w.batch * batch_c + (int64_t)m * ldc + n, v, vec && n + 4 <= op.N, op.N - n);
+                    for (int h = 0; h < 2; ++h) {
+                        const int nn = n + 4 * h;
+                        if (nn >= op.N) break;
+                        f32x4 x = v[h] * f0 * f1;
+                        if (add) x += *reinterpret_cast<const f32x4 *>(add + (int64_t)mm * ld_add + nn);
+                        put(w.batch * batch_c + (int64_t)mm * ldc + nn, x, vec && nn + 4 <= op.N, op.N - nn);
+                    }
+                }
             }
         }
     }
 
+    // four values at element `at`: at once (vec), or the first `count` of them one by one
     __device__ __forceinline__ void put(int64_t at, f32x4 v, bool vec, int count) const
     {
         if constexpr (BF16_OUT) {
@@ -529,84 +624,74 @@ struct StoreEpi {
 };
 
 // ------------------------------------------------------------------- 16-bit tiles, two ways ---
-// A block of the wavefront's tile (64 x 64, or all of a smaller one) as 16-bit values in the LDS, lines of
-// kLine bytes whose 16-byte chunks are XOR-permuted by the line's upper bits.
-template <class G>
-struct Block16 {
-    static constexpr int kRows = G::kWaveRows < 64 ? G::kWaveRows : 64, kCols = G::kWaveCols;
-    static_assert(kCols <= 64 && kRows == kCols && G::kWaveRows % kRows == 0, "square blocks as wide as the wave tile");
-    static constexpr int kLine = kCols * 2, kChunks = kLine / 16, kBytes = kRows * kLine;
-    static constexpr int kBlocks = G::kWaveRows / kRows, BI = kRows / 16;
-    static constexpr int kLinesPerPass = 64 / kChunks, kPasses = kRows / kLinesPerPass;
-    static_assert(G::NW * 2 * kBytes <= G::kRingBytes, "two blocks per wavefront");
-    static __device__ __forceinline__ int chunk(int line, int c) { return line * kLine + 16 * (c ^ ((line >> 1) & (kChunks - 1))); }
-    // four consecutive values at (line, col), col a multiple of 4
-    static __device__ __forceinline__ int quad(int line, int col) { return chunk(line, col >> 3) + 2 * (col & 4); }
-
-    // the wavefront's whole lines between the block and memory: pass p of a lane
-    static __device__ __forceinline__ int line_of(int lane, int p) { return kLinesPerPass * p + lane / kChunks; }
-    static __device__ __forceinline__ int chunk_of(int lane) { return lane % kChunks; }
-    static __device__ __forceinline__ void to_memory(const uint8_t *block, int lane, uint16_t *at, int64_t ld)
-    {
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p) {
-            const int l = line_of(lane, p), c = chunk_of(lane);
-            *reinterpret_cast<u32x4 *>(at + l * ld + 8 * c) = *reinterpret_cast<const u32x4 *>(block + chunk(l, c));
-        }
-    }
-    static __device__ __forceinline__ void from_memory(u32x4 (&v)[kPasses], int lane, const uint16_t *at, int64_t ld)
-    {
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p) v[p] = *reinterpret_cast<const u32x4 *>(at + line_of(lane, p) * ld + 8 * chunk_of(lane));
-    }
-    static __device__ __forceinline__ void put(uint8_t *block, int lane, const u32x4 (&v)[kPasses])
-    {
-#pragma unroll
-        for (int p = 0; p < kPasses; ++p) *reinterpret_cast<u32x4 *>(block + chunk(line_of(lane, p), chunk_of(lane))) = v[p];
-    }
-    // Four values of one row, packed in two words, into the block `turned` (transposed): a lane swaps two of
-    // its four columns against its neighbour's row, so that it holds two rows of two columns and
-    // writes words.
-    static __device__ __forceinline__ void put_turned(uint8_t *turned, int row, int col, uint32_t lo, uint32_t hi)
-    {
-        const bool odd = row & 1;
-        const uint32_t give = odd ? lo : hi;
-        const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);
-        // even lanes: columns 0, 1 of rows r, r + 1; odd lanes: columns 2, 3 of rows r - 1, r
-        const uint32_t up = odd ? got : lo, dn = odd ? hi : got;   // the upper and the lower row's pair
-        const int c = col + (odd ? 2 : 0), r = row & ~1;
-        *reinterpret_cast<uint32_t *>(turned + chunk(c, r >> 3) + 2 * (r & 7)) = __builtin_amdgcn_perm(dn, up, 0x05040100u);
-        *reinterpret_cast<uint32_t *>(turned + chunk(c + 1, r >> 3) + 2 * (r & 7)) = __builtin_amdgcn_perm(dn, up, 0x07060302u);
-    }
-};
-
 // Writes the wavefront's part of the tile as 16-bit values, row-major at rows[m][ld_rows] and (cols !=
 // nullptr) transposed at cols[n][ld_cols], m and n counted from the matrix' origin; every element of
-// the tile has its place in both. pack makes two values one word; val(i, j) gives the four values of
-// acc[i][j]. Blocks pass through the LDS in both orientations, so that a store instruction writes
-// whole lines of either.
-template <class G, class Pack, class Val>
-__device__ __forceinline__ void store_tile16(const Where &w, uint8_t *lds, Pack pack, Val val, uint16_t *rows, int64_t ld_rows,
-                                             uint16_t *cols, int64_t ld_cols)
+// the tile has its place in both. fetch(m, n) reads what make(v, fetched, m, n) wants to turn the
+// product's eight values v, columns n .. n + 7 of row m, into those to write; make may write
+// row-major memory of its own there: the lanes of a row cover a line of 128 bytes. pack makes two
+// values one word.
+//
+// A block of the accumulators goes through the LDS in FP32; one code serves all blocks, as it is fetched for
+// one use. For the transposed a lane swaps four of its eight columns against the next row's, so
+// that it holds two rows of four columns and writes words; its lines are 64 bytes.
+template <class G, class Pack, class Fetch, class Make>
+__device__ __forceinline__ void store_tile16(f32x4 (&acc)[G::FI][G::FJ], const Where &w, uint8_t *lds, Pack pack, Fetch fetch,
+                                             Make make, uint16_t *rows, int64_t ld_rows, uint16_t *cols, int64_t ld_cols)
 {
-    using B = Block16<G>;
-    const int r = w.lane & 15, q = w.lane >> 4;
-    uint8_t *tile = lds + w.wave * 2 * B::kBytes, *turned = tile + B::kBytes;
-#pragma unroll
+    using B = Block32<G>;
+    constexpr int kLine = B::kRows * 2, kPieces = kLine / 16;   // the transposed block: kCols lines
+    uint8_t *block = lds + w.wave * G::kEpiWave, *turned = block + B::kBytes;
+    const int line = w.lane / B::kLanes, c8 = w.lane % B::kLanes, n = w.n0 + w.col0 + 8 * c8;
+    const bool odd = line & 1;
+    // 16-byte pieces of the transposed lines, XOR-permuted by the column
+    const auto piece = [](int col, int p) { return col * kLine + 16 * (p ^ ((col >> 1) & (kPieces - 1))); };
+    const auto next_row = [](uint32_t v) {
+        if constexpr (B::kLanes == 8)
+            return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, true);   // row_ror:8
+        else
+            return (uint32_t)__shfl_xor((int)v, B::kLanes);
+    };
+#pragma unroll 1
     for (int blk = 0; blk < B::kBlocks; ++blk) {
+        const int m = w.m0 + w.row0 + B::kRows * blk;
+        decltype(fetch(0, 0)) got[B::kPasses];
 #pragma unroll
-        for (int ii = 0; ii < B::BI; ++ii)
+        for (int p = 0; p < B::kPasses; ++p) got[p] = fetch(m + B::kLinesPerPass * p + line, n);
+        B::put(block, w.lane, acc, blk);
+        uint16_t *at = rows + (int64_t)(m + line) * ld_rows + n;
 #pragma unroll
-            for (int j = 0; j < G::FJ; ++j) {
-                const f32x4 v = val(B::BI * blk + ii, j);
-                const uint32_t lo = pack(v[0], v[1]), hi = pack(v[2], v[3]);
-                const int row = 16 * ii + r, col = 16 * j + 4 * q;
-                *reinterpret_cast<u32x2 *>(tile + B::quad(row, col)) = u32x2{lo, hi};
-                if (cols) B::put_turned(turned, row, col, lo, hi);
+        for (int p = 0; p < B::kPasses; ++p) {
+            const int l = B::kLinesPerPass * p + line;
+            f32x4 v[2];
+            B::get(block, l, c8, v);
+            make(v, got[p], m + l, n);
+            const uint32_t word[4] = {pack(v[0][0], v[0][1]), pack(v[0][2], v[0][3]), pack(v[1][0], v[1][1]),
+                                      pack(v[1][2], v[1][3])};
+            *reinterpret_cast<u32x4 *>(at) = u32x4{word[0], word[1], word[2], word[3]};
+            at += B::kLinesPerPass * ld_rows;
+            if (cols) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // even lines keep columns 0 .. 3 and get those of the line below; odd ones keep 4 .. 7
+                    const uint32_t got_word = next_row(odd ? word[h] : word[2 + h]);
+                    const uint32_t up = odd ? got_word : word[h], dn = odd ? word[2 + h] : got_word;
+                    const int c = 8 * c8 + (odd ? 4 : 0) + 2 * h, r = l & ~1;
+                    *reinterpret_cast<uint32_t *>(turned + piece(c, r >> 3) + 2 * (r & 7)) =
+                        __builtin_amdgcn_perm(dn, up, 0x05040100u);
+                    *reinterpret_cast<uint32_t *>(turned + piece(c + 1, r >> 3) + 2 * (r & 7)) =
+                        __builtin_amdgcn_perm(dn, up, 0x07060302u);
+                }
             }
-        const int64_t m = w.m0 + w.row0 + B::kRows * blk, n = w.n0 + w.col0;
-        B::to_memory(tile, w.lane, rows + m * ld_rows + n, ld_rows);
-        if (cols) B::to_memory(turned, w.lane, cols + n * ld_cols + m, ld_cols);
+        }
+        if (cols) {
+            constexpr int kColsPerPass = 64 / kPieces;
+            const int col = w.lane / kPieces, pc = w.lane % kPieces;
+            uint16_t *to = cols + (int64_t)(w.n0 + w.col0 + col) * ld_cols + m + 8 * pc;
+#pragma unroll
+            for (int p = 0; p < B::kCols / kColsPerPass; ++p)
+                *reinterpret_cast<u32x4 *>(to + (int64_t)kColsPerPass * p * ld_cols) =
+                    *reinterpret_cast<const u32x4 *>(turned + piece(kColsPerPass * p + col, pc));
+        }
     }
 }
 
@@ -626,24 +711,42 @@ inline int64_t count_tiles(int64_t M, int64_t N, bool sym, int side)
     return sym ? tm * (tm + 1) / 2 : tm * tn;
 }
 
-// The plan with the least time by a simple account (measured, in microseconds): a workgroup spends so
-// much on each stage, and so much before and behind them; workgroups beyond what the chip holds at a time
-// wait for another round; partial sums cost a launch and their way through memory.
+// A round of n workgroups of one tile size, `per` stages each, in microseconds: so much for a stage and so
+// much around the stages, with how many workgroups share a CU. Measured in bf16 on the whole chip and on
+// parts of it (256 x 256: 16, 128 and 256 workgroups take 1.02, 1.07 and 1.45 a stage, the last by the
+// power cap; 128 x 128: 16, 256 and 512 take 0.44, 0.50 and 0.95; 64 x 64: 0.18, 0.20 and 0.36).
+inline double round_time(int geo, int64_t n, int64_t per)
+{
+    const double share = (double)n / kComputeUnits;
+    switch (geo) {
+    case 0: return (double)per * (1.02 + 0.86 * (share > 0.5 ? share - 0.5 : 0.0)) + 8.0 + 3.0 * share;
+    case 1: return (double)per * 0.48 * (share > 1.0 ? share : 1.0) + 4.5 + 2.0 * share;
+    default: return (double)per * (share > 1.0 ? 0.20 + 0.16 * (share - 1.0) : 0.20) + 4.0 + 0.8 * share;
+    }
+}
+
+// The plan with the least time by that account: rounds of as many workgroups as the chip holds; for a split
+// contraction the partial sums' kernel too, whose workgroups read one split after the other (measured 3, 0.9
+// and 0.3 us each by tile size). 1024 x 1024 x 8192: 137 us in 256 x 256 tiles, 54 split eight ways, 35 in
+// 128 x 128 tiles split four ways, 30 in 64 x 64 unsplit; 1537 x 1024 x 50304: 811, 195 split nine ways, 216
+// in 128 x 128 split four ways.
 inline Plan plan_product(int64_t M, int64_t N, int64_t nk, bool sym, int64_t batch, bool may_split)
 {
-    constexpr double kStage[3] = {1.35, 0.80, 0.33}, kEnds[3] = {9.0, 6.0, 4.0};
     constexpr int kSlots[3] = {kComputeUnits, 2 * kComputeUnits, 2 * kComputeUnits};
+    constexpr double kJoin[3] = {3.0, 0.9, 0.3};
     Plan best{};
     double least = 0.0;
     if (nk < 1) nk = 1;   // an empty contraction asks for no workspace
     for (int g = 0; g < 3; ++g) {
         const int64_t tiles = count_tiles(M, N, sym, kTileSide[g]) * batch;
-        for (int s = 1; s <= 16; s = s < 4 ? s + 1 : s + 2) {
+        for (int s = 1; s <= 16; ++s) {
             if (s > 1 && (!may_split || nk / s < 4)) break;
-            const int64_t per = (nk + s - 1) / s, used = (nk + per - 1) / per;
-            const double rounds = (double)((tiles * used + kSlots[g] - 1) / kSlots[g]);
-            const double bytes = used > 1 ? (double)tiles * used * kTileSide[g] * kTileSide[g] * 4 : 0.0;
-            const double t = rounds * ((double)per * kStage[g] + kEnds[g]) + (used > 1 ? 5.0 + bytes * 2 / 4.0e6 : 0.0);
+            const int64_t per = (nk + s - 1) / s, used = (nk + per - 1) / per, n = tiles * used;
+            double t = (double)(n / kSlots[g]) * round_time(g, kSlots[g], per);
+            if (n % kSlots[g]) t += round_time(g, n % kSlots[g], per);
+            const double bytes = used > 1 ? (double)n * kTileSide[g] * kTileSide[g] * 4 : 0.0;
+            if (used > 1)
+                t += 3.0 + (double)((tiles + kSlots[g] - 1) / kSlots[g]) * (double)used * kJoin[g] + bytes / 4.0e6;
             if (best.splits == 0 || t < least) {
                 least = t;
                 best = Plan{g, (int)used, (int)per, tiles, (size_t)bytes};

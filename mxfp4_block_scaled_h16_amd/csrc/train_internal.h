@@ -28,7 +28,7 @@ struct Fp8Input {
     Fp8Out axis1, axis0;
 };
 constexpr int kFp8Group = 2;
-// up to kFp8Group tensors in one launch
+// up to kFp8Group tensors of one type in one launch
 hipError_t launch_fp8_quantize(const Fp8Input *items, int count, hipStream_t stream);
 
 // c = alpha A B^T + beta c, FP32 or bf16. K is the row length the scales cover; rows hold

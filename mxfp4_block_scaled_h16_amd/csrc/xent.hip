@@ -175,35 +175,37 @@ struct GradEpi {
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
     {
-        const int r = w.lane & 15, q = w.lane >> 4;
-        const int nbase = w.n0 + w.col0 + 4 * q;
-        const int nleft = op.N - nbase;
+        // of each row of the tile: scaled dl and dp, lse in base 2, and the target's column in the piece (-1: no
+        // column of it, or a row without a gradient of its loss)
+        f32x4 *info = reinterpret_cast<f32x4 *>(lds + G::kRowInfo);
         const float scale = ranges->g;
-#pragma unroll
-        for (int i = 0; i < G::FI; ++i) {
-            const int m = w.m0 + w.row0 + 16 * i + r;
-            const bool live = m < op.M;
-            const int mm = live ? m : op.M - 1;
-            float dl, dp;
-            weights.of(mm, dl, dp);
-            dl = live ? dl * scale : 0.0f;
-            dp = live ? dp * scale : 0.0f;
-            const float ref = lse[mm] * kLog2e;
-            const int64_t tc = weights.target[mm] - v0 - nbase;
-            const int want = dl != 0.0f && tc >= 0 && tc < 64 ? (int)tc : -1;
-#pragma unroll
-            for (int j = 0; j < G::FJ; ++j)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const int c = 16 * j + t;
-                    float v = fast_exp2(fmaf(acc[i][j][t], kLog2e, -ref)) * dp;
-                    // dp == 0: nothing of the exponentials counts, whatever they are
-                    v = c < nleft && dp != 0.0f ? v : 0.0f;
-                    acc[i][j][t] = c == want ? v - dl : v;
-                }
+        for (int row = threadIdx.x; row < G::kTileM; row += 64 * G::NW) {
+            const int m = w.m0 + row;
+            f32x4 v = {0.0f, 0.0f, 0.0f, __int_as_float(-1)};
+            if (m < op.M) {
+                float dl, dp;
+                weights.of(m, dl, dp);
+                const int64_t at = weights.target[m] - v0;
+                v = f32x4{dl * scale, dp * scale, lse[m] * kLog2e,
+                          __int_as_float(dl != 0.0f && at >= 0 && at < op.N ? (int)at : -1)};
+            }
+            info[row] = v;
         }
-        store_tile16<G>(w, lds, [](float a, float b) { return pack_f16(a, b); }, [&](int i, int j) { return acc[i][j]; }, g, ldg,
-                        gt, ldt);
+        __syncthreads();
+        store_tile16<G>(acc, w, lds, [](float a, float b) { return pack_f16(a, b); },
+                        [&](int m, int) { return info[m - w.m0]; },
+                        [&](f32x4 (&z)[2], const f32x4 &row, int, int n) {
+                            const float dl = row[0], dp = row[1], ref = row[2];
+                            const int want = __float_as_int(row[3]) - n, left = op.N - n;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float v = fast_exp2(fmaf(z[e / 4][e % 4], kLog2e, -ref)) * dp;
+                                // dp == 0: nothing of the exponentials counts, whatever they are
+                                v = e < left && dp != 0.0f ? v : 0.0f;
+                                z[e / 4][e % 4] = e == want ? v - dl : v;
+                            }
+                        },
+                        g, ldg, gt, ldt);
     }
 };
 
