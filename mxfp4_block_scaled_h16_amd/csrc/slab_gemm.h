@@ -712,15 +712,16 @@ inline int64_t count_tiles(int64_t M, int64_t N, bool sym, int side)
 }
 
 // A round of n workgroups of one tile size, `per` stages each, in microseconds: so much for a stage and so
-// much around the stages, with how many workgroups share a CU. Measured in bf16 on the whole chip and on
-// parts of it (256 x 256: 16, 128 and 256 workgroups take 1.02, 1.07 and 1.45 a stage, the last by the
-// power cap; 128 x 128: 16, 256 and 512 take 0.44, 0.50 and 0.95; 64 x 64: 0.18, 0.20 and 0.36).
+// much around the stages, with how many workgroups share a CU. Measured in bf16: 16 workgroups of 256 x 256
+// take 1.02 a stage, 256 of them 1.45 by the power cap, and 136 of them 1.44 in a run of such products,
+// which the cap holds down for longer than one of them lasts; 128 x 128: 16 take 0.44, 256 0.50, 512 0.95 to
+// 1.05, 416 over a contraction of 50304 1.34; 64 x 64: 0.18, 0.20 and 0.36.
 inline double round_time(int geo, int64_t n, int64_t per)
 {
     const double share = (double)n / kComputeUnits;
     switch (geo) {
-    case 0: return (double)per * (1.02 + 0.86 * (share > 0.5 ? share - 0.5 : 0.0)) + 8.0 + 3.0 * share;
-    case 1: return (double)per * 0.48 * (share > 1.0 ? share : 1.0) + 4.5 + 2.0 * share;
+    case 0: return (double)per * (1.02 + 0.43 * (share < 0.5 ? 2.0 * share : 1.0)) + 8.0 + 3.0 * share;
+    case 1: return (double)per * (share > 1.0 ? 0.50 + 0.70 * (share - 1.0) : 0.50) + 4.5 + 2.0 * share;
     default: return (double)per * (share > 1.0 ? 0.20 + 0.16 * (share - 1.0) : 0.20) + 4.0 + 0.8 * share;
     }
 }
@@ -740,7 +741,8 @@ inline Plan plan_product(int64_t M, int64_t N, int64_t nk, bool sym, int64_t bat
     for (int g = 0; g < 3; ++g) {
         const int64_t tiles = count_tiles(M, N, sym, kTileSide[g]) * batch;
         for (int s = 1; s <= 16; ++s) {
-            if (s > 1 && (!may_split || nk / s < 4)) break;
+            // nothing to gain once the tiles fill the chip four times, or stages run out
+            if (s > 1 && (!may_split || nk / s < 4 || tiles > 4 * kSlots[g])) break;
             const int64_t per = (nk + s - 1) / s, used = (nk + per - 1) / per, n = tiles * used;
             double t = (double)(n / kSlots[g]) * round_time(g, kSlots[g], per);
             if (n % kSlots[g]) t += round_time(g, n % kSlots[g], per);

@@ -288,29 +288,56 @@ __global__ __launch_bounds__(256) void range_kernel(const uint16_t *x, int64_t l
     }
 }
 
-__global__ __launch_bounds__(256) void join_ranges_kernel(const float *part, int blocks, Ranges *out)
+// The scales, from the partial maxima: by every workgroup of the first kernel that needs them, the first of which
+// leaves them for those that follow.
+__device__ __forceinline__ Ranges join_ranges(const float *part, int blocks)
 {
     float s[3];
+#pragma unroll 1
     for (int k = 0; k < 3; ++k) {
         float top = 0.0f;
         for (int i = threadIdx.x; i < blocks; i += 256) top = fmaxf(top, part[k * kRangeBlocks + i]);
         s[k] = range_scale(block_max(top));
     }
-    if (threadIdx.x == 0) *out = Ranges{s[0], s[1], s[2], {1.0f / s[0], 1.0f / s[2]}, {1.0f / s[0], 1.0f / s[1]}};
+    return Ranges{s[0], s[1], s[2], {1.0f / s[0], 1.0f / s[2]}, {1.0f / s[0], 1.0f / s[1]}};
 }
 
 // ------------------------------------------------------------------------------- copies -------
-// out[c][r] = in[r][c] * *scale, bf16 to FP16; r < rows (zero for rows up to rows_padded, a multiple of
-// 64, and for rows that add nothing), c < cols. 128 x 128 tiles: a thread transposes 8 x 8 values in
+// A matrix to be transposed and scaled: out[c][r] = in[r][c] * scale, bf16 to FP16; r < rows (zero for rows up to
+// rows_padded, a multiple of 64, and for rows that add nothing), c < cols. in == NULL: none.
+struct Turn {
+    const uint16_t *in;
+    int64_t ld_in, rows, cols;
+    uint16_t *out;
+    int64_t ld_out, rows_padded;
+    int vec, across;   // 16-byte aligned rows; tiles across the columns
+    int tiles;
+};
+// One or two of them, X's and that of a piece of W. 128 x 128 tiles: a thread transposes 8 x 8 values in
 // registers, then 256-byte lines are put together in the LDS. Bound by memory: 2 bytes in, 2 out.
-__global__ __launch_bounds__(256) void turn_kernel(const uint16_t *__restrict__ in, int64_t ld_in, int64_t rows, int64_t cols,
-                                                   int vec, const float *__restrict__ scale, uint16_t *__restrict__ out,
-                                                   int64_t ld_out, int64_t rows_padded, RowWeights weights)
+// blocks > 0: the ranges are joined here.
+__global__ __launch_bounds__(256) void turn_kernel(Turn tx, Turn tw, RowWeights weights, const float *part, int blocks,
+                                                   Ranges *ranges)
 {
     __shared__ __attribute__((aligned(16))) uint16_t tile[128 * 128];   // [column][row], 16-byte pieces permuted
-    const int64_t r0 = (int64_t)blockIdx.x * 128, c0 = (int64_t)blockIdx.y * 128;
+    Ranges now;
+    if (blocks > 0) {
+        now = join_ranges(part, blocks);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *ranges = now;
+    } else {
+        now = *ranges;
+    }
+    const bool is_w = (int)blockIdx.x >= tx.tiles;
+    const Turn &t = is_w ? tw : tx;
+    const int index = (int)blockIdx.x - (is_w ? tx.tiles : 0);
+    const int64_t rows = t.rows, cols = t.cols, ld_in = t.ld_in, ld_out = t.ld_out, rows_padded = t.rows_padded;
+    const uint16_t *in = t.in;
+    uint16_t *out = t.out;
+    const int vec = t.vec;
+    if (is_w) weights.target = nullptr;   // every row of W counts
+    const int64_t r0 = (int64_t)(index / t.across) * 128, c0 = (int64_t)(index % t.across) * 128;
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
-    const float s = *scale;
+    const float s = is_w ? now.w : now.x;
     u32x4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -360,12 +387,20 @@ __global__ __launch_bounds__(256) void pad16_kernel(const uint16_t *__restrict__
     }
 }
 
-hipError_t turn(const void *in, int64_t ld_in, int64_t rows, int64_t cols, const float *scale, uint16_t *out, int64_t ld_out,
-                int64_t rows_padded, const RowWeights &weights, hipStream_t stream)
+Turn turn_of(const void *in, int64_t ld_in, int64_t rows, int64_t cols, uint16_t *out, int64_t ld_out, int64_t rows_padded)
 {
-    const int vec = (uintptr_t)in % 16 == 0 && ld_in % 8 == 0;
-    return launch(turn_kernel, dim3((unsigned)((rows_padded + 127) / 128), (unsigned)((cols + 127) / 128)), dim3(256), 0, stream,
-                  static_cast<const uint16_t *>(in), ld_in, rows, cols, vec, scale, out, ld_out, rows_padded, weights);
+    Turn t{};
+    t.in = static_cast<const uint16_t *>(in);
+    t.ld_in = ld_in;
+    t.rows = rows;
+    t.cols = cols;
+    t.out = out;
+    t.ld_out = ld_out;
+    t.rows_padded = rows_padded;
+    t.vec = (uintptr_t)in % 16 == 0 && ld_in % 8 == 0;
+    t.across = (int)((cols + 127) / 128);
+    t.tiles = (int)((rows_padded + 127) / 128) * t.across;
+    return t;
 }
 
 // ------------------------------------------------------------------------------ workspace -----
@@ -378,6 +413,23 @@ int64_t piece_columns(int64_t T, int64_t V)
     if (most < 2048) most = 2048;
     const int64_t pieces = (V + most - 1) / most;
     return round_up((V + pieces - 1) / pieces, 256);
+}
+
+// The products of a piece: G covers whole tiles, and the products over it run to the end of the last one.
+struct PiecePlans {
+    Plan g, dx, dw;
+    int64_t cols_done, rows_done;
+};
+PiecePlans plans_of(int64_t T, int64_t K, int64_t cols)
+{
+    PiecePlans p;
+    p.g = plan_product(T, cols, round_up(K, 64) / 64, false, 1, false);
+    const int64_t side = kTileSide[p.g.geo];
+    p.cols_done = round_up(cols, side);
+    p.rows_done = round_up(T, side);
+    p.dx = plan_product(T, K, p.cols_done / 64, false, 1, true);
+    p.dw = plan_product(cols, K, p.rows_done / 64, false, 1, true);
+    return p;
 }
 
 struct Carve {
@@ -423,15 +475,13 @@ Layout carve(Carve &c, int64_t T, int64_t K, int64_t V, bool backward)
     l.g = static_cast<uint16_t *>(c.take(2 * tp * vc));
     l.gt = static_cast<uint16_t *>(c.take(2 * tp * vc));
     l.dx = static_cast<float *>(c.take(4 * T * round_up(K, 4)));
-    // the plans of every piece's products: full ones and the last, whose contraction ends with a tile of
-    // one of three sizes
     size_t most = 0;
     const int64_t rest = V % vc ? V % vc : vc;
-    for (const int64_t cols : {vc < V ? vc : V, rest})
-        for (const int64_t side : kTileSide) {
-            most = std::max(most, plan_product(T, K, round_up(cols, side) / 64, false, 1, true).partial_bytes);
-            most = std::max(most, plan_product(cols, K, round_up(T, side) / 64, false, 1, true).partial_bytes);
-        }
+    for (const int64_t cols : {vc < V ? vc : V, rest}) {
+        const PiecePlans plans = plans_of(T, K, cols);
+        most = std::max(most, std::max(plans.dx.partial_bytes, plans.dw.partial_bytes));
+        if (rest == cols) break;
+    }
     l.partials = c.take(most);
     return l;
 }
@@ -508,9 +558,6 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
     if (hipError_t e = launch(range_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, static_cast<const uint16_t *>(p.x), p.ldx,
                               static_cast<const uint16_t *>(p.w), p.ldw, p.T, p.K, p.V, vec ? 1 : 0, weights, l.range_part))
         return e;
-    if (hipError_t e = launch(join_ranges_kernel, dim3(1), dim3(256), 0, stream, l.range_part, blocks, l.ranges)) return e;
-    if (dw)
-        if (hipError_t e = turn(p.x, p.ldx, p.T, p.K, &l.ranges->x, l.xt, tp, tp, weights, stream)) return e;
     const int64_t ld_acc = round_up(p.K, 4);
     for (int64_t v0 = 0; v0 < p.V; v0 += vc) {
         const int64_t cols = p.V - v0 < vc ? p.V - v0 : vc;
@@ -519,15 +566,17 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
         op.b = lo.b + v0 * lo.ldb;
         op.N = (int)cols;
         const GradEpi epi{weights, lse, v0, l.ranges, l.g, l.gt, vc, tp};
-        const Plan plan = plan_product(p.T, cols, op.nk, false, 1, false);
-        if (hipError_t e = launch_product<BF16>(op, epi, 1, plan, nullptr, stream)) return e;
-        // G covers whole tiles; the products over it run to the end of the last one
-        const int64_t step = kTileSide[plan.geo];
-        const int64_t cols_done = round_up(cols, step), rows_done = round_up(p.T, step);
-        if (dx) {
-            if (hipError_t e = turn(static_cast<const uint16_t *>(p.w) + v0 * p.ldw, p.ldw, cols, p.K, &l.ranges->w, l.wt, vc,
-                                    cols_done, RowWeights{}, stream))
+        const PiecePlans plans = plans_of(p.T, p.K, cols);
+        const int64_t cols_done = plans.cols_done, rows_done = plans.rows_done;
+        Turn tx{}, tw{};
+        if (dw && first) tx = turn_of(p.x, p.ldx, p.T, p.K, l.xt, tp, tp);
+        if (dx) tw = turn_of(static_cast<const uint16_t *>(p.w) + v0 * p.ldw, p.ldw, cols, p.K, l.wt, vc, cols_done);
+        if (tx.tiles + tw.tiles > 0)
+            if (hipError_t e = launch(turn_kernel, dim3((unsigned)(tx.tiles + tw.tiles)), dim3(256), 0, stream, tx, tw, weights,
+                                      l.range_part, first ? blocks : 0, l.ranges))
                 return e;
+        if (hipError_t e = launch_product<BF16>(op, epi, 1, plans.g, nullptr, stream)) return e;
+        if (dx) {
             Operands q{};
             q.a = reinterpret_cast<const uint8_t *>(l.g);
             q.lda = 2 * vc;
@@ -536,8 +585,7 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             q.M = (int)p.T;
             q.N = (int)p.K;
             q.nk = (int)(cols_done / 64);
-            const Plan how = plan_product(p.T, p.K, q.nk, false, 1, true);
-            auto run = [&](const auto &e) { return launch_product<F16>(q, e, 1, how, l.partials, stream); };
+            auto run = [&](const auto &e) { return launch_product<F16>(q, e, 1, plans.dx, l.partials, stream); };
             const float *add = first ? nullptr : l.dx;
             hipError_t e;
             if (!last)
@@ -557,8 +605,7 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             q.M = (int)cols;
             q.N = (int)p.K;
             q.nk = (int)(rows_done / 64);
-            const Plan how = plan_product(cols, p.K, q.nk, false, 1, true);
-            auto run = [&](const auto &e) { return launch_product<F16>(q, e, 1, how, l.partials, stream); };
+            auto run = [&](const auto &e) { return launch_product<F16>(q, e, 1, plans.dw, l.partials, stream); };
             const hipError_t e =
                 dw_bf16 ? run(StoreEpi<true>{static_cast<uint16_t *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, l.ranges->inv_gx})
                         : run(StoreEpi<false>{static_cast<float *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, l.ranges->inv_gx});

@@ -9,6 +9,7 @@ allocated on that stream.
 """
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch  # imported first: the library binds to the HIP runtime torch has loaded
@@ -104,12 +105,25 @@ def _on(device, stream):
     return _other(device, stream)
 
 
+# the current stream's handle without a Stream object around it (a call costs a few microseconds of host
+# time in all, which is what small products take on the GPU)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _current():
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
+@functools.lru_cache(maxsize=1024)
+def _need(name, *sizes):
+    """Workspace bytes of one operator at these sizes."""
+    return int(getattr(train_lib(), "mxfp4_%s_workspace_bytes" % name)(*sizes))
+
+
 def _room(workspace, need, device):
-    """(pointer, bytes) of the workspace, allocated if there is none, and the tensor that holds it."""
+    """The workspace, allocated if there is none."""
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
     elif workspace.device != device:
@@ -191,7 +205,7 @@ def fp8_quantize(x, axis=1, block="row", q=None, scales=None, stream=None):
 
 
 def fp8_gemm_workspace_bytes(M, N, K) -> int:
-    return int(train_lib().mxfp4_fp8_gemm_workspace_bytes(int(M), int(N), int(K)))
+    return _need("fp8_gemm", int(M), int(N), int(K))
 
 
 def fp8_gemm(aq, as_, bq, bs, alpha=1.0, beta=0.0, out=None, out_dtype=None, k=None, workspace="auto", stream=None):
@@ -232,7 +246,7 @@ def fp8_gemm(aq, as_, bq, bs, alpha=1.0, beta=0.0, out=None, out_dtype=None, k=N
 
 
 def fp8_linear_workspace_bytes(pass_, M, K, N) -> int:
-    return int(train_lib().mxfp4_fp8_linear_workspace_bytes(int(pass_), int(M), int(K), int(N)))
+    return _need("fp8_linear", int(pass_), int(M), int(K), int(N))
 
 
 def _fp8_linear(name, pass_, a, b, M, K, N, shape, out, out_dtype, workspace, stream):
@@ -245,7 +259,7 @@ def _fp8_linear(name, pass_, a, b, M, K, N, shape, out, out_dtype, workspace, st
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
         L = train_lib()
-        ws = _room(workspace, L.mxfp4_fp8_linear_workspace_bytes(pass_, M, K, N), device)
+        ws = _room(workspace, _need("fp8_linear", pass_, M, K, N), device)
         _check(getattr(L, name)(a.data_ptr(), b.data_ptr(), M, K, N, ws.data_ptr(), _bytes(ws), out.data_ptr(),
                                 _OUT[out.dtype], _current()), name)
     return out
@@ -285,9 +299,7 @@ def fp8_linear_wgrad(dy, x, out=None, out_dtype=None, workspace=None, stream=Non
 
 # ------------------------------------------------------------------------------- head loss ---
 def linear_xent_workspace_bytes(T, K, V, backward=False) -> int:
-    L = train_lib()
-    f = L.mxfp4_linear_xent_backward_workspace_bytes if backward else L.mxfp4_linear_xent_forward_workspace_bytes
-    return int(f(int(T), int(K), int(V)))
+    return _need("linear_xent_backward" if backward else "linear_xent_forward", int(T), int(K), int(V))
 
 
 def _xent_operands(x, w, target):
@@ -318,7 +330,7 @@ def linear_xent_forward(x, w, target, ignore_index=-100, workspace=None, stream=
         L = train_lib()
         loss = torch.empty(T, dtype=torch.float32, device=device)
         lse = torch.empty(T, dtype=torch.float32, device=device)
-        ws = _room(workspace, L.mxfp4_linear_xent_forward_workspace_bytes(T, K, V), device)
+        ws = _room(workspace, _need("linear_xent_forward", T, K, V), device)
         _check(L.mxfp4_linear_xent_forward(x.data_ptr(), ldx, w.data_ptr(), ldw, target.data_ptr(), T, K, V, int(ignore_index),
                                            ws.data_ptr(), _bytes(ws), loss.data_ptr(), lse.data_ptr(), _current()),
                "mxfp4_linear_xent_forward")
@@ -343,7 +355,7 @@ def linear_xent_backward(dloss, x, w, target, lse, dlse=None, ignore_index=-100,
         for t, name in ((dx, "dx"), (dw, "dw")):
             if t is not None and not t.is_contiguous():
                 raise ValueError("%s must be contiguous" % name)
-        ws = _room(workspace, L.mxfp4_linear_xent_backward_workspace_bytes(T, K, V), device)
+        ws = _room(workspace, _need("linear_xent_backward", T, K, V), device)
         at = lambda t: (None, 0) if t is None else (t.data_ptr(), _OUT[t.dtype])  # noqa: E731
         _check(L.mxfp4_linear_xent_backward(rows[0], rows[1], x.data_ptr(), ldx, w.data_ptr(), ldw, target.data_ptr(), rows[2],
                                             T, K, V, int(ignore_index), ws.data_ptr(), _bytes(ws), *at(dx), *at(dw),
@@ -353,7 +365,7 @@ def linear_xent_backward(dloss, x, w, target, lse, dlse=None, ignore_index=-100,
 
 # --------------------------------------------------------------------------- Newton-Schulz ---
 def orthogonalize_workspace_bytes(batch, m, n) -> int:
-    return int(train_lib().mxfp4_orthogonalize_workspace_bytes(int(batch), int(m), int(n)))
+    return _need("orthogonalize", int(batch), int(m), int(n))
 
 
 def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, alpha=1.0, beta=0.0, out=None,
@@ -381,7 +393,7 @@ def orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
             row = t.stride(1) if m > 1 else max(n, 1)
             strides.append((row, t.stride(0) if B > 1 else m * row))
         L = train_lib()
-        ws = _room(workspace, L.mxfp4_orthogonalize_workspace_bytes(B, m, n), device)
+        ws = _room(workspace, _need("orthogonalize", B, m, n), device)
         _check(L.mxfp4_orthogonalize(g.data_ptr(), _IN[g.dtype], B, m, n, *strides[0], int(steps), float(a), float(b), float(c),
                                      float(eps), float(alpha), float(beta), out.data_ptr(), _OUT[out.dtype], *strides[1],
                                      ws.data_ptr(), _bytes(ws), _current()), "mxfp4_orthogonalize")
