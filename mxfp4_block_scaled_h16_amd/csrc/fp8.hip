@@ -246,7 +246,7 @@ hipError_t launch_fp8_quantize(const Fp8Input *items, int count, hipStream_t str
 
 size_t fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
-    return slab::plan_product(M, N, round_up(K, 128) / 128, false, 1, true).partial_bytes;
+    return slab::plan_product(M, N, round_up(K, 128) / 128, false, 1).partial_bytes;
 }
 
 hipError_t launch_fp8_gemm(const uint8_t *aq, int64_t lda, const uint8_t *as, int64_t ldas, const uint8_t *bq,
@@ -267,9 +267,9 @@ hipError_t launch_fp8_gemm(const uint8_t *aq, int64_t lda, const uint8_t *as, in
     op.M = (int)M;
     op.N = (int)N;
     op.nk = (int)(round_up(K, 128) / 128);
-    Plan plan = plan_product(M, N, op.nk, false, 1, true);
-    if (plan.partial_bytes > ws_bytes || !workspace) plan = plan_product(M, N, op.nk, false, 1, false);
-    auto run = [&](const auto &epi) { return launch_product<E4M3>(op, epi, 1, plan, workspace, stream); };
+    Plan plan = plan_product(M, N, op.nk, false, 1);
+    if (plan.partial_bytes > ws_bytes || !workspace) plan = unsplit(plan, op.nk);
+    auto run = [&](const auto &epi) { return launch_product<E4M3>(op, epi, plan, workspace, stream); };
     return bf16 ? run(StoreEpi<true>{c, ldc, 0, alpha, beta}) : run(StoreEpi<false>{c, ldc, 0, alpha, beta});
 }
 

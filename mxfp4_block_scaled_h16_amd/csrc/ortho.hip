@@ -326,10 +326,10 @@ Sizes sizes_of(int64_t batch, int64_t m, int64_t n)
         z.np = round_up(n, pad);
         z.sp = m <= n ? z.mp : z.np;
         z.lp = m <= n ? z.np : z.mp;
-        z.gram = plan_product(z.sp, z.sp, z.lp / 64, true, batch, true);
-        z.poly = plan_product(z.sp, z.sp, z.sp / 64, true, batch, true);
-        z.update = plan_product(z.mp, z.np, z.sp / 64, false, batch, true);
-        z.last = plan_product(m, n, z.sp / 64, false, batch, true);
+        z.gram = plan_product(z.sp, z.sp, z.lp / 64, true, batch);
+        z.poly = plan_product(z.sp, z.sp, z.sp / 64, true, batch);
+        z.update = plan_product(z.mp, z.np, z.sp / 64, false, batch);
+        z.last = plan_product(m, n, z.sp / 64, false, batch);
     };
     plans(256);
     const bool big = z.gram.geo == 0 || z.poly.geo == 0 || z.update.geo == 0 || z.last.geo == 0;
@@ -371,9 +371,9 @@ Space carve(uint8_t *base, int64_t batch, const Sizes &z)
 }
 
 template <class Epi>
-hipError_t product(const Plan &plan, const Operands &op, const Epi &epi, int64_t batch, const Space &s, hipStream_t stream)
+hipError_t product(const Plan &plan, const Operands &op, const Epi &epi, const Space &s, hipStream_t stream)
 {
-    return launch_product<F16>(op, epi, (int)batch, plan, s.partials, stream);
+    return launch_product<F16>(op, epi, plan, s.partials, stream);
 }
 
 }  // namespace
@@ -417,12 +417,12 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
         op.M = op.N = (int)z.sp;
         op.nk = (int)((wide ? z.np : z.mp) / 64);
         op.batch_a = op.batch_b = 2 * bx;
-        if ((e = product(z.gram, op, GramEpi{s.gram, z.sp, ba}, p.batch, s, stream))) return e;
+        if ((e = product(z.gram, op, GramEpi{s.gram, z.sp, ba}, s, stream))) return e;
         op.a = op.b = reinterpret_cast<const uint8_t *>(s.gram);
         op.lda = op.ldb = 2 * z.sp;
         op.nk = (int)(z.sp / 64);
         op.batch_a = op.batch_b = 2 * ba;
-        if ((e = product(z.poly, op, PolyEpi{s.gram, s.poly, z.sp, ba, p.b, p.c}, p.batch, s, stream))) return e;
+        if ((e = product(z.poly, op, PolyEpi{s.gram, s.poly, z.sp, ba, p.b, p.c}, s, stream))) return e;
         // the update in X's orientation: poly X for wide, X poly for tall (poly is symmetric)
         op.a = reinterpret_cast<const uint8_t *>(wide ? s.poly : x);
         op.lda = 2 * (wide ? z.sp : z.np);
@@ -435,17 +435,15 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
         op.N = (int)z.np;
         if (k + 1 < p.steps) {
             const UpdateEpi epi{x, s.lo, s.hi[(k + 1) & 1], s.turned[(k + 1) & 1], z.np, z.mp, bx, p.a};
-            if ((e = product(z.update, op, epi, p.batch, s, stream))) return e;
+            if ((e = product(z.update, op, epi, s, stream))) return e;
         } else {
             op.M = (int)p.m;
             op.N = (int)p.n;
             const float alpha = p.alpha * kUnscale;
             e = p.out_bf16 ? product(z.last, op, LastEpi<true>{x, s.lo, z.np, bx, p.a,
-                                                              StoreEpi<true>{p.out, p.ldo, p.batch_o, alpha, p.beta}},
-                                     p.batch, s, stream)
+                                                              StoreEpi<true>{p.out, p.ldo, p.batch_o, alpha, p.beta}}, s, stream)
                            : product(z.last, op, LastEpi<false>{x, s.lo, z.np, bx, p.a,
-                                                               StoreEpi<false>{p.out, p.ldo, p.batch_o, alpha, p.beta}},
-                                     p.batch, s, stream);
+                                                               StoreEpi<false>{p.out, p.ldo, p.batch_o, alpha, p.beta}}, s, stream);
             if (e) return e;
         }
     }

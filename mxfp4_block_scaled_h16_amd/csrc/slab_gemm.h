@@ -138,11 +138,12 @@ struct Operands {
     int64_t ldas, ldbs;
     int M, N, nk;
     int tiles_m, tiles_n;
-    int64_t batch_a, batch_b;  // bytes from one product of a batch (blockIdx.z) to the next
-    // A contraction worked by several workgroups (blockIdx.y), stages [y per, y per + per) each: with splits > 1
-    // they leave their sums in partials, in the order of their registers, and finish_kernel adds them up.
-    int splits = 1, per = 0;
-    f32x4 *partials = nullptr;
+    int64_t batch_a, batch_b;  // bytes from one product of a batch to the next
+    // The first `whole` tiles of all products have a workgroup each. The others, which would leave much of the chip
+    // idle, are worked by `splits` workgroups each, stages [y per, y per + per) by the y-th: these leave their
+    // sums in partials, in the order of their registers, and finish_kernel adds them up.
+    int whole, splits, per;
+    f32x4 *partials;
 };
 
 struct Where {
@@ -152,17 +153,21 @@ struct Where {
     int batch;
 };
 
-// Tile v of the grid. Consecutive workgroups go to the eight XCDs in turn; each XCD gets a contiguous
-// range of tiles, walked column by column in groups of row panels covering 1024 rows, so that the
-// workgroups running on one XCD share operand panels in its L2. SYM: only the tiles that touch
+// Where workgroup v of n neighbours works in their order: consecutive workgroups go to the eight XCDs in
+// turn; each XCD gets a contiguous range.
+__device__ __forceinline__ int spread(int v, int n)
+{
+    const int per = n / 8, rem = n % 8, x = v % 8;
+    return x * per + min(x, rem) + v / 8;
+}
+
+// Tile t of a product. Tiles are walked column by column in groups of row panels covering 1024 rows, so that
+// the workgroups running on one XCD share operand panels in its L2. SYM: only the tiles that touch
 // the lower triangle of a square of tiles, in bands of four rows of tiles, each in squares of 4 x 4 and
 // what is left at the diagonal.
 template <class G, bool SYM>
-__device__ __forceinline__ void locate(int v, int tiles_m, int tiles_n, int &m0, int &n0)
+__device__ __forceinline__ void locate(int t, int tiles_m, int tiles_n, int &m0, int &n0)
 {
-    const int total = SYM ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n;
-    const int per = total / 8, rem = total % 8, x = v % 8;
-    const int t = x * per + min(x, rem) + v / 8;
     if constexpr (SYM) {
         // band I holds 16 I + 10 tiles, the bands before it 8 I I + 2 I (a short last band fewer)
         int band = (int)sqrtf((float)t * 0.125f);   // a start that the loops put right
@@ -190,11 +195,24 @@ __device__ __forceinline__ void locate(int v, int tiles_m, int tiles_n, int &m0,
     }
 }
 
-// where this workgroup's tile keeps its sums over split y
+// where split y of the i-th split tile keeps its sums
 template <class G>
-__device__ __forceinline__ int64_t partial_at(const Operands &op, int y)
+__device__ __forceinline__ f32x4 *partial_at(const Operands &op, int i, int y)
 {
-    return (((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * op.splits + y) * (G::kTileM * G::kTileN / 4);
+    return op.partials + ((int64_t)i * op.splits + y) * (G::kTileM * G::kTileN / 4);
+}
+
+// tile t of all products: its batch and origin
+template <class G, class Epi>
+__device__ __forceinline__ void place(Where &w, const Operands &op, int t)
+{
+    const int tiles = Epi::kSym ? op.tiles_m * (op.tiles_m + 1) / 2 : op.tiles_m * op.tiles_n;
+    w.batch = t / tiles;
+    locate<G, Epi::kSym>(t - w.batch * tiles, op.tiles_m, op.tiles_n, w.m0, w.n0);
+    w.lane = threadIdx.x & 63;
+    w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    w.row0 = w.wave % G::kWavesM * G::kWaveRows;
+    w.col0 = w.wave / G::kWavesM * G::kWaveCols;
 }
 
 // -------------------------------------------------------------------------------- the kernel --
@@ -215,14 +233,20 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
     constexpr int FI = G::FI, FJ = G::FJ;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[G::template lds_bytes<E>()];
 
+    // this workgroup's tile and stages
     Where w;
-    locate<G, Epi::kSym>(blockIdx.x, op.tiles_m, op.tiles_n, w.m0, w.n0);
-    w.batch = blockIdx.z;
-    w.lane = threadIdx.x & 63;
-    w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = w.wave % G::kWavesM, wn = w.wave / G::kWavesM;
-    w.row0 = wm * G::kWaveRows;
-    w.col0 = wn * G::kWaveCols;
+    int first = 0, end = op.nk, split_tile = -1, split = 0;
+    if ((int)blockIdx.x < op.whole) {
+        place<G, Epi>(w, op, spread(blockIdx.x, op.whole));
+    } else {
+        const int rest = (int)gridDim.x - op.whole, tail = rest / op.splits;
+        const int i = spread((int)blockIdx.x - op.whole, rest);
+        split = i / tail;
+        split_tile = i - split * tail;
+        place<G, Epi>(w, op, op.whole + split_tile);
+        first = split * op.per;
+        end = min(op.nk, first + op.per);
+    }
     const int lane = w.lane, r = lane & 15, q = lane >> 4;
 
     // load u of this wavefront fills rows [8 (kDma wave + u), + 8) of the stage: lane L the 16 bytes at
@@ -243,8 +267,6 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
         const int row = b_row0 + kRowsPerDma * u + lane / 8;
         boff[u] = (uint32_t)min(row, op.N - 1 - w.n0) * (uint32_t)op.ldb + 16u * ((lane % 8) ^ chunk_perm(row));
     }
-    const int first = op.splits > 1 ? blockIdx.y * op.per : 0;
-    const int end = op.splits > 1 ? min(op.nk, first + op.per) : op.nk;
     constexpr int NB = G::kBuffers;
     auto dma = [&](int stage) {
         // past the last stage the last one again, into a free buffer
@@ -407,8 +429,8 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
     wait_vmcnt<0>();
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     barrier();
-    if (op.splits > 1) {
-        f32x4 *out = op.partials + partial_at<G>(op, blockIdx.y) + threadIdx.x;
+    if (split_tile >= 0) {
+        f32x4 *out = partial_at<G>(op, split_tile, split) + threadIdx.x;
 #pragma unroll
         for (int i = 0; i < FI; ++i)
 #pragma unroll
@@ -426,15 +448,10 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void finish_kernel(Opera
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kEpiBytes + G::kTileM * 16];
     Where w;
-    locate<G, Epi::kSym>(blockIdx.x, op.tiles_m, op.tiles_n, w.m0, w.n0);
-    w.batch = blockIdx.z;
-    w.lane = threadIdx.x & 63;
-    w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    w.row0 = w.wave % G::kWavesM * G::kWaveRows;
-    w.col0 = w.wave / G::kWavesM * G::kWaveCols;
+    place<G, Epi>(w, op, op.whole + blockIdx.x);
     f32x4 acc[G::FI][G::FJ];
     for (int y = 0; y < op.splits; ++y) {
-        const f32x4 *in = op.partials + partial_at<G>(op, y) + threadIdx.x;
+        const f32x4 *in = partial_at<G>(op, blockIdx.x, y) + threadIdx.x;
 #pragma unroll
         for (int i = 0; i < G::FI; ++i)
 #pragma unroll
@@ -696,11 +713,11 @@ __device__ __forceinline__ void store_tile16(f32x4 (&acc)[G::FI][G::FJ], const W
 }
 
 // ---------------------------------------------------------------------------------- launch ----
-// What runs a product: the tile and how many workgroups share a tile's contraction.
+// What runs a product: the tile, how many tiles have a workgroup each, and how many workgroups share each of
+// the others.
 struct Plan {
     int geo;      // 0 Big, 1 Small, 2 Tiny
-    int splits, per;
-    int64_t tiles;
+    int whole, tail, splits, per;
     size_t partial_bytes;
 };
 constexpr int kTileSide[3] = {256, 128, 64};
@@ -726,62 +743,74 @@ inline double round_time(int geo, int64_t n, int64_t per)
     }
 }
 
-// The plan with the least time by that account: rounds of as many workgroups as the chip holds; for a split
-// contraction the partial sums' kernel too, whose workgroups read one split after the other (measured 3, 0.9
-// and 0.3 us each by tile size). 1024 x 1024 x 8192: 137 us in 256 x 256 tiles, 54 split eight ways, 35 in
-// 128 x 128 tiles split four ways, 30 in 64 x 64 unsplit; 1537 x 1024 x 50304: 811, 195 split nine ways, 216
-// in 128 x 128 split four ways.
-inline Plan plan_product(int64_t M, int64_t N, int64_t nk, bool sym, int64_t batch, bool may_split)
+// The plan with the least time by that account: full rounds of as many workgroups as the chip holds, and the
+// tiles left over, each worked by several workgroups if that is quicker; then their sums' kernel too, whose
+// workgroups read one split after the other (measured 3, 0.9 and 0.3 us each by tile size). 1024 x 1024 x
+// 8192: 137 us in 256 x 256 tiles, 54 split eight ways, 35 in 128 x 128 tiles split four ways, 30 in 64 x 64
+// unsplit; 1537 x 1024 x 50304: 811, 195 split nine ways, 216 in 128 x 128 split four ways.
+inline Plan plan_product(int64_t M, int64_t N, int64_t nk, bool sym, int64_t batch)
 {
     constexpr int kSlots[3] = {kComputeUnits, 2 * kComputeUnits, 2 * kComputeUnits};
     constexpr double kJoin[3] = {3.0, 0.9, 0.3};
-    Plan best{};
+    Plan best{0, -1, 0, 1, 1, 0};
     double least = 0.0;
     if (nk < 1) nk = 1;   // an empty contraction asks for no workspace
+    // more tiles than a grid is counted in here: no plan (such operands fit no memory)
+    if ((double)M * (double)N * (double)batch > 1e15) return Plan{0, -1, 0, 1, (int)nk, 0};
     for (int g = 0; g < 3; ++g) {
         const int64_t tiles = count_tiles(M, N, sym, kTileSide[g]) * batch;
-        for (int s = 1; s <= 16; ++s) {
-            // nothing to gain once the tiles fill the chip four times, or stages run out
-            if (s > 1 && (!may_split || nk / s < 4 || tiles > 4 * kSlots[g])) break;
-            const int64_t per = (nk + s - 1) / s, used = (nk + per - 1) / per, n = tiles * used;
-            double t = (double)(n / kSlots[g]) * round_time(g, kSlots[g], per);
-            if (n % kSlots[g]) t += round_time(g, n % kSlots[g], per);
-            const double bytes = used > 1 ? (double)n * kTileSide[g] * kTileSide[g] * 4 : 0.0;
-            if (used > 1)
-                t += 3.0 + (double)((tiles + kSlots[g] - 1) / kSlots[g]) * (double)used * kJoin[g] + bytes / 4.0e6;
-            if (best.splits == 0 || t < least) {
+        if (tiles > 1 << 26) continue;
+        const int64_t full = tiles / kSlots[g] * kSlots[g], left = tiles - full;
+        const double rounds = (double)(tiles / kSlots[g]) * round_time(g, kSlots[g], nk);
+        double t = rounds + (left ? round_time(g, left, nk) : 0.0);
+        if (least == 0.0 || t < least) {
+            least = t;
+            best = Plan{g, (int)tiles, 0, 1, (int)nk, 0};
+        }
+        for (int64_t s = 2; s <= 16 && left > 0 && nk / s >= 4; ++s) {
+            const int64_t per = (nk + s - 1) / s, used = (nk + per - 1) / per, n = left * used;
+            if (used != s) continue;
+            const double bytes = (double)n * kTileSide[g] * kTileSide[g] * 4;
+            t = rounds + (double)(n / kSlots[g]) * round_time(g, kSlots[g], per) +
+                (n % kSlots[g] ? round_time(g, n % kSlots[g], per) : 0.0) + 3.0 + (double)used * kJoin[g] + bytes / 4.0e6;
+            if (t < least) {
                 least = t;
-                best = Plan{g, (int)used, (int)per, tiles, (size_t)bytes};
+                best = Plan{g, (int)full, (int)left, (int)used, (int)per, (size_t)bytes};
             }
         }
     }
     return best;
 }
+// The same tile without the workspace.
+inline Plan unsplit(Plan p, int64_t nk)
+{
+    return Plan{p.geo, p.whole + p.tail, 0, 1, (int)nk, 0};
+}
 
 template <class E, class G, class Epi>
-hipError_t launch_planned(Operands op, const Epi &epi, int batch, const Plan &plan, void *partials, hipStream_t stream)
+hipError_t launch_planned(Operands op, const Epi &epi, const Plan &plan, void *partials, hipStream_t stream)
 {
     op.tiles_m = (op.M + G::kTileM - 1) / G::kTileM;
     op.tiles_n = (op.N + G::kTileN - 1) / G::kTileN;
-    const int64_t tiles = Epi::kSym ? (int64_t)op.tiles_m * (op.tiles_m + 1) / 2 : (int64_t)op.tiles_m * op.tiles_n;
-    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    if (plan.whole < 0) return hipErrorInvalidValue;
+    op.whole = plan.whole;
     op.splits = plan.splits;
     op.per = plan.per;
     op.partials = static_cast<f32x4 *>(partials);
-    const hipError_t e = launch(product_kernel<E, G, Epi>, dim3((unsigned)tiles, (unsigned)plan.splits, (unsigned)batch),
-                                dim3(64 * G::NW), 0, stream, op, epi);
-    if (e != hipSuccess || plan.splits == 1) return e;
-    return launch(finish_kernel<G, Epi>, dim3((unsigned)tiles, 1, (unsigned)batch), dim3(64 * G::NW), 0, stream, op, epi);
+    const unsigned grid = (unsigned)plan.whole + (unsigned)plan.tail * (unsigned)plan.splits;
+    const hipError_t e = launch(product_kernel<E, G, Epi>, dim3(grid), dim3(64 * G::NW), 0, stream, op, epi);
+    if (e != hipSuccess || plan.tail == 0) return e;
+    return launch(finish_kernel<G, Epi>, dim3((unsigned)plan.tail), dim3(64 * G::NW), 0, stream, op, epi);
 }
 
 // partials: room for plan.partial_bytes (NULL when the plan does not split)
 template <class E, class Epi>
-hipError_t launch_product(const Operands &op, const Epi &epi, int batch, const Plan &plan, void *partials, hipStream_t stream)
+hipError_t launch_product(const Operands &op, const Epi &epi, const Plan &plan, void *partials, hipStream_t stream)
 {
     switch (plan.geo) {
-    case 0: return launch_planned<E, Big>(op, epi, batch, plan, partials, stream);
-    case 1: return launch_planned<E, Small>(op, epi, batch, plan, partials, stream);
-    default: return launch_planned<E, Tiny>(op, epi, batch, plan, partials, stream);
+    case 0: return launch_planned<E, Big>(op, epi, plan, partials, stream);
+    case 1: return launch_planned<E, Small>(op, epi, plan, partials, stream);
+    default: return launch_planned<E, Tiny>(op, epi, plan, partials, stream);
     }
 }
 

@@ -423,12 +423,12 @@ struct PiecePlans {
 PiecePlans plans_of(int64_t T, int64_t K, int64_t cols)
 {
     PiecePlans p;
-    p.g = plan_product(T, cols, round_up(K, 64) / 64, false, 1, false);
+    p.g = plan_product(T, cols, round_up(K, 64) / 64, false, 1);
     const int64_t side = kTileSide[p.g.geo];
     p.cols_done = round_up(cols, side);
     p.rows_done = round_up(T, side);
-    p.dx = plan_product(T, K, p.cols_done / 64, false, 1, true);
-    p.dw = plan_product(cols, K, p.rows_done / 64, false, 1, true);
+    p.dx = plan_product(T, K, p.cols_done / 64, false, 1);
+    p.dw = plan_product(cols, K, p.rows_done / 64, false, 1);
     return p;
 }
 
@@ -462,9 +462,11 @@ Layout carve(Carve &c, int64_t T, int64_t K, int64_t V, bool backward)
         l.wp = static_cast<uint16_t *>(c.take(2 * V * kp));
     }
     if (!backward) {
-        const int64_t side = kTileSide[plan_product(T, V, kp / 64, false, 1, false).geo];
+        const Plan plan = plan_product(T, V, kp / 64, false, 1);
+        const int64_t side = kTileSide[plan.geo];
         l.part = static_cast<float2 *>(c.take(8 * T * ((V + side - 1) / side)));
         l.zt = static_cast<float *>(c.take(4 * T));
+        l.partials = c.take(plan.partial_bytes);
         return l;
     }
     const int64_t tp = round_up(T, 256), vc = piece_columns(T, V);
@@ -479,7 +481,7 @@ Layout carve(Carve &c, int64_t T, int64_t K, int64_t V, bool backward)
     const int64_t rest = V % vc ? V % vc : vc;
     for (const int64_t cols : {vc < V ? vc : V, rest}) {
         const PiecePlans plans = plans_of(T, K, cols);
-        most = std::max(most, std::max(plans.dx.partial_bytes, plans.dw.partial_bytes));
+        most = std::max(most, std::max(plans.g.partial_bytes, std::max(plans.dx.partial_bytes, plans.dw.partial_bytes)));
         if (rest == cols) break;
     }
     l.partials = c.take(most);
@@ -536,8 +538,8 @@ hipError_t launch_xent_forward(const XentProblem &p, void *ws, float *loss, floa
     if (hipError_t e = logits_operands(p, l, op, stream)) return e;
     op.N = (int)p.V;
     const StatsEpi epi{l.part, l.zt, p.target};
-    const Plan plan = plan_product(p.T, p.V, op.nk, false, 1, false);
-    if (hipError_t e = launch_product<BF16>(op, epi, 1, plan, nullptr, stream)) return e;
+    const Plan plan = plan_product(p.T, p.V, op.nk, false, 1);
+    if (hipError_t e = launch_product<BF16>(op, epi, plan, l.partials, stream)) return e;
     const int tiles = (int)((p.V + kTileSide[plan.geo] - 1) / kTileSide[plan.geo]);
     return launch(xent_join_kernel, dim3((unsigned)((p.T + 31) / 32)), dim3(256), 0, stream, l.part, tiles, (int)p.T, p.V,
                   l.zt, p.target, p.ignore_index, loss, lse);
@@ -575,7 +577,7 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             if (hipError_t e = launch(turn_kernel, dim3((unsigned)(tx.tiles + tw.tiles)), dim3(256), 0, stream, tx, tw, weights,
                                       l.range_part, first ? blocks : 0, l.ranges))
                 return e;
-        if (hipError_t e = launch_product<BF16>(op, epi, 1, plans.g, nullptr, stream)) return e;
+        if (hipError_t e = launch_product<BF16>(op, epi, plans.g, l.partials, stream)) return e;
         if (dx) {
             Operands q{};
             q.a = reinterpret_cast<const uint8_t *>(l.g);
@@ -585,7 +587,7 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             q.M = (int)p.T;
             q.N = (int)p.K;
             q.nk = (int)(cols_done / 64);
-            auto run = [&](const auto &e) { return launch_product<F16>(q, e, 1, plans.dx, l.partials, stream); };
+            auto run = [&](const auto &e) { return launch_product<F16>(q, e, plans.dx, l.partials, stream); };
             const float *add = first ? nullptr : l.dx;
             hipError_t e;
             if (!last)
@@ -605,7 +607,7 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             q.M = (int)cols;
             q.N = (int)p.K;
             q.nk = (int)(rows_done / 64);
-            auto run = [&](const auto &e) { return launch_product<F16>(q, e, 1, plans.dw, l.partials, stream); };
+            auto run = [&](const auto &e) { return launch_product<F16>(q, e, plans.dw, l.partials, stream); };
             const hipError_t e =
                 dw_bf16 ? run(StoreEpi<true>{static_cast<uint16_t *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, l.ranges->inv_gx})
                         : run(StoreEpi<false>{static_cast<float *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, l.ranges->inv_gx});
