@@ -113,7 +113,7 @@ struct Geo {
     static_assert((TM + TN) / 64 <= NW, "at most one scale load per wavefront and group");
     // a wavefront's part of the LDS in the epilogue: 32 rows of its tile in FP32, and transposed in 16 bits; behind
     // all of them 16 bytes for each row of the tile
-    static constexpr int kBlockRows = 32;
+    static constexpr int kBlockRows = 32, kEpiBlocks = kWaveRows / kBlockRows;
     static constexpr int kEpiWave = kBlockRows * kWaveCols * (4 + 2), kEpiBytes = NW * kEpiWave;
     static constexpr int kRowInfo = kEpiBytes;
     template <class E>
@@ -151,6 +151,7 @@ struct Where {
     int wave, lane;
     int row0, col0;  // the wavefront's origin in the tile
     int batch;
+    int block0, block1;   // the blocks of 32 rows of every wavefront that the epilogue is for
 };
 
 // Where workgroup v of n neighbours works in their order: consecutive workgroups go to the eight XCDs in
@@ -207,12 +208,14 @@ template <class G, class Epi>
 __device__ __forceinline__ void place(Where &w, const Operands &op, int t)
 {
     const int tiles = Epi::kSym ? op.tiles_m * (op.tiles_m + 1) / 2 : op.tiles_m * op.tiles_n;
-    w.batch = t / tiles;
+    w.batch = t < tiles ? 0 : t / tiles;
     locate<G, Epi::kSym>(t - w.batch * tiles, op.tiles_m, op.tiles_n, w.m0, w.n0);
     w.lane = threadIdx.x & 63;
     w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     w.row0 = w.wave % G::kWavesM * G::kWaveRows;
     w.col0 = w.wave / G::kWavesM * G::kWaveCols;
+    w.block0 = 0;
+    w.block1 = G::kEpiBlocks;
 }
 
 // -------------------------------------------------------------------------------- the kernel --
@@ -442,24 +445,34 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
 }
 
 // The sums of a split contraction, in their order (so that the result does not depend on which workgroup
-// came first), and the epilogue.
+// came first), and the epilogue. A tile's blocks of 32 rows have a workgroup each: what bounds this kernel is
+// how fast a CU reads (a 256 x 256 tile of nine splits by one workgroup: 39 us).
 template <class G, class Epi>
 __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void finish_kernel(Operands op, Epi epi)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kEpiBytes + G::kTileM * 16];
+    const int tile = blockIdx.x / G::kEpiBlocks, blk = blockIdx.x % G::kEpiBlocks;
     Where w;
-    place<G, Epi>(w, op, op.whole + blockIdx.x);
-    f32x4 acc[G::FI][G::FJ];
+    place<G, Epi>(w, op, op.whole + tile);
+    w.block0 = blk;
+    w.block1 = blk + 1;
+    f32x4 sum[2][G::FJ];
     for (int y = 0; y < op.splits; ++y) {
-        const f32x4 *in = partial_at<G>(op, blockIdx.x, y) + threadIdx.x;
+        const f32x4 *in = partial_at<G>(op, tile, y) + threadIdx.x + 2 * blk * G::FJ * 64 * G::NW;
 #pragma unroll
-        for (int i = 0; i < G::FI; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < G::FJ; ++j) {
                 const f32x4 v = in[(i * G::FJ + j) * 64 * G::NW];
-                acc[i][j] = y == 0 ? v : acc[i][j] + v;
+                sum[i][j] = y == 0 ? v : sum[i][j] + v;
             }
     }
+    // only this block's registers of acc are looked at
+    f32x4 acc[G::FI][G::FJ];
+#pragma unroll
+    for (int i = 0; i < G::FI; ++i)
+#pragma unroll
+        for (int j = 0; j < G::FJ; ++j) acc[i][j] = sum[i % 2][j];
     epi.template run<G>(acc, w, op, lds);
 }
 
@@ -558,7 +571,7 @@ struct StoreEpi {
         const bool plain = vec && beta == 0.0f && !add && w.m0 + G::kTileM <= op.M && w.n0 + G::kTileN <= op.N;
         const int line = w.lane / B::kLanes, c8 = w.lane % B::kLanes, n = w.n0 + w.col0 + 8 * c8;
 #pragma unroll 1
-        for (int blk = 0; blk < B::kBlocks; ++blk) {
+        for (int blk = w.block0; blk < w.block1; ++blk) {
             // a block of the wavefront's rows through its part of the LDS (no barrier), so that a store
             // instruction writes whole lines; one code for all blocks: it is fetched for one use
             const int m = w.m0 + w.row0 + B::kRows * blk + line;
@@ -669,7 +682,7 @@ __device__ __forceinline__ void store_tile16(f32x4 (&acc)[G::FI][G::FJ], const W
             return (uint32_t)__shfl_xor((int)v, B::kLanes);
     };
 #pragma unroll 1
-    for (int blk = 0; blk < B::kBlocks; ++blk) {
+    for (int blk = w.block0; blk < w.block1; ++blk) {
         const int m = w.m0 + w.row0 + B::kRows * blk;
         decltype(fetch(0, 0)) got[B::kPasses];
 #pragma unroll
@@ -745,13 +758,13 @@ inline double round_time(int geo, int64_t n, int64_t per)
 
 // The plan with the least time by that account: full rounds of as many workgroups as the chip holds, and the
 // tiles left over, each worked by several workgroups if that is quicker; then their sums' kernel too, whose
-// workgroups read one split after the other (measured 3, 0.9 and 0.3 us each by tile size). 1024 x 1024 x
+// workgroups read one split after the other (0.9, 0.5 and 0.3 us each by tile size). 1024 x 1024 x
 // 8192: 137 us in 256 x 256 tiles, 54 split eight ways, 35 in 128 x 128 tiles split four ways, 30 in 64 x 64
 // unsplit; 1537 x 1024 x 50304: 811, 195 split nine ways, 216 in 128 x 128 split four ways.
 inline Plan plan_product(int64_t M, int64_t N, int64_t nk, bool sym, int64_t batch)
 {
     constexpr int kSlots[3] = {kComputeUnits, 2 * kComputeUnits, 2 * kComputeUnits};
-    constexpr double kJoin[3] = {3.0, 0.9, 0.3};
+    constexpr double kJoin[3] = {0.9, 0.5, 0.3};
     Plan best{0, -1, 0, 1, 1, 0};
     double least = 0.0;
     if (nk < 1) nk = 1;   // an empty contraction asks for no workspace
@@ -800,7 +813,7 @@ hipError_t launch_planned(Operands op, const Epi &epi, const Plan &plan, void *p
     const unsigned grid = (unsigned)plan.whole + (unsigned)plan.tail * (unsigned)plan.splits;
     const hipError_t e = launch(product_kernel<E, G, Epi>, dim3(grid), dim3(64 * G::NW), 0, stream, op, epi);
     if (e != hipSuccess || plan.tail == 0) return e;
-    return launch(finish_kernel<G, Epi>, dim3((unsigned)plan.tail), dim3(64 * G::NW), 0, stream, op, epi);
+    return launch(finish_kernel<G, Epi>, dim3((unsigned)(plan.tail * G::kEpiBlocks)), dim3(64 * G::NW), 0, stream, op, epi);
 }
 
 // partials: room for plan.partial_bytes (NULL when the plan does not split)

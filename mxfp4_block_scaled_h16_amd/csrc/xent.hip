@@ -44,6 +44,7 @@ struct StatsEpi {
         const int nleft = op.N - (w.n0 + w.col0 + 4 * q);   // valid: 16 j + t < nleft
 #pragma unroll
         for (int i = 0; i < G::FI; ++i) {
+            if (i / 2 < w.block0 || i / 2 >= w.block1) continue;
             const int row = w.row0 + 16 * i + r;
             const int m = min(w.m0 + row, op.M - 1);
             // the target's place among this lane's columns; far outside when it is not an index
@@ -81,6 +82,8 @@ struct StatsEpi {
         }
         __syncthreads();
         for (int row = threadIdx.x; row < G::kTileM; row += 64 * G::NW) {
+            const int blk = row % G::kWaveRows / G::kBlockRows;
+            if (blk < w.block0 || blk >= w.block1) continue;
             float2 s = slots[row];
 #pragma unroll
             for (int k = 1; k < G::kWavesN; ++k) {
