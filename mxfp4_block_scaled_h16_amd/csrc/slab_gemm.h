@@ -68,12 +68,14 @@ struct F16 {
 // values of a stage; which 32 does not matter, as A and B take the same ones and all share a scale.
 struct E4M3 {
     static constexpr bool kScaled = true;
+    // the scales are bytes BB of sb and BA of sa
+    template <int BB, int BA>
     static __device__ __forceinline__ void mfma(f32x4 &acc, const u32x4 &b0, const u32x4 &b1, const u32x4 &a0,
                                                 const u32x4 &a1, uint32_t sb, uint32_t sa)
     {
         const v8i vb = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
         const v8i va = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, acc, 0, 0, 0, (int)sb, 0, (int)sa);
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, acc, 0, 0, BB, (int)sb, BA, (int)sa);
     }
 };
 
@@ -90,6 +92,18 @@ __device__ __forceinline__ void barrier()
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
+}
+
+// f(0), f(1), ... f(N - 1), the numbers as types
+template <class F, int... K>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, K...>)
+{
+    (f(std::integral_constant<int, K>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F f)
+{
+    each_of(f, std::make_integer_sequence<int, N>());
 }
 
 __device__ __forceinline__ int chunk_perm(int row) { return (row >> 1) & 7; }
@@ -110,7 +124,7 @@ struct Geo {
     static constexpr int kDmaA = TM / kRowsPerDma / NW, kDmaB = TN / kRowsPerDma / NW;
     static constexpr int kDmaPerStage = kDmaA + kDmaB;
     static_assert(kDmaA * kRowsPerDma * NW == TM && kDmaB * kRowsPerDma * NW == TN, "whole loads per wavefront");
-    static_assert((TM + TN) / 64 <= NW, "at most one scale load per wavefront and group");
+    static_assert(TM + TN <= 64 * NW, "a thread for each row's scales");
     // a wavefront's part of the LDS in the epilogue: 32 rows of its tile in FP32, and transposed in 16 bits; behind
     // all of them 16 bytes for each row of the tile
     static constexpr int kBlockRows = 32, kEpiBlocks = kWaveRows / kBlockRows;
@@ -284,23 +298,25 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
             __builtin_amdgcn_raw_ptr_buffer_load_lds(brsrc, (lds_void_t *)(dst + G::kABytes + b_row0 * kRowBytes + u * 1024),
                                                      16, boff[u], at, 0, 0);
     };
-    // E4M3: the scales of 16 stages (16 bytes of every row) per load, wavefront w those of the tile's rows
-    // [64 w, + 64) (A's first, then B's; wavefronts past the last of them none)
-    const uint8_t *sbase = nullptr;
-    uint32_t soff = 0;
-    if constexpr (E::kScaled) {
-        const bool is_b = 64 * w.wave >= G::kTileM;
-        const int row = 64 * w.wave + lane - (is_b ? G::kTileM : 0);
-        sbase = is_b ? op.bs + (int64_t)w.n0 * op.ldbs : op.as + (int64_t)w.m0 * op.ldas;
-        soff = is_b ? (uint32_t)min(row, op.N - 1 - w.n0) * (uint32_t)op.ldbs
-                    : (uint32_t)min(row, op.M - 1 - w.m0) * (uint32_t)op.ldas;
-    }
+    // E4M3: a thread per row of the tile (A's first, then B's) takes the scales of 16 stages, 16 bytes, and lays
+    // them into one of two slots of the LDS: [stage][64 rows][row % 16][row / 16], so that a lane has the
+    // scales of its row in four 16-row tiles in one word.
+    const uint8_t *srow = nullptr;
+    int sput = 0;
     const int last_group = (end - 1) / 16;
-    auto dma_scales = [&](int g) {
-        if ((G::kTileM + G::kTileN) / 64 < G::NW && w.wave >= (G::kTileM + G::kTileN) / 64) return;
-        __builtin_amdgcn_global_load_lds((gbl_void_t *)(sbase + (int64_t)min(g, last_group) * 16 + soff),
-                                         (lds_void_t *)(lds + G::kRingBytes + (g & 1) * G::kScaleSlot + w.wave * 1024),
-                                         16, 0, 0);
+    if constexpr (E::kScaled) {
+        const bool is_b = (int)threadIdx.x >= G::kTileM;
+        const int row = min((int)threadIdx.x, G::kTileM + G::kTileN - 1) - (is_b ? G::kTileM : 0);
+        srow = is_b ? op.bs + (int64_t)(w.n0 + min(row, op.N - 1 - w.n0)) * op.ldbs
+                    : op.as + (int64_t)(w.m0 + min(row, op.M - 1 - w.m0)) * op.ldas;
+        sput = G::kRingBytes + (is_b ? G::kTileM : 0) + row / 64 * 64 + row % 16 * 4 + row % 64 / 16;
+    }
+    auto load_scales = [&](int g) { return *reinterpret_cast<const u32x4 *>(srow + (int64_t)min(g, last_group) * 16); };
+    auto put_scales = [&](int g, const u32x4 &v) {
+        if (G::kTileM + G::kTileN < 64 * G::NW && (int)threadIdx.x >= G::kTileM + G::kTileN) return;
+        uint8_t *dst = lds + (g & 1) * G::kScaleSlot + sput;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) dst[k * (G::kTileM + G::kTileN)] = (uint8_t)(v[k / 4] >> (8 * (k % 4)));
     };
 
     const int perm = chunk_perm(r);
@@ -316,10 +332,11 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
 #pragma unroll
         for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{};
 
-    // a wavefront may load no scales: its waits then cover a load more than they have to
     if constexpr (E::kScaled) {
-        dma_scales(first >> 4);
-        dma_scales((first >> 4) + 1);
+        const u32x4 v0 = load_scales(first >> 4), v1 = load_scales((first >> 4) + 1);
+        put_scales(first >> 4, v0);
+        put_scales((first >> 4) + 1, v1);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): for the barrier below
     }
 #pragma unroll
     for (int k = 0; k < NB; ++k) dma(first + k);
@@ -378,53 +395,69 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
             __builtin_amdgcn_sched_barrier(0);
         }
     } else {
-        constexpr int H = FI / 2;
+        constexpr int H = FI / 2, WA = (FI + 3) / 4, WB = (FJ + 3) / 4;
         u32x4 fa[FI][2], fb[FJ][2];
-        uint32_t sa[FI], sb[FJ];
-        const int sa_at = G::kRingBytes + 16 * (w.row0 + r), sb_at = G::kRingBytes + 16 * (G::kTileM + w.col0 + r);
-        auto scales = [&](int stage) { return lds + ((stage >> 4) & 1) * G::kScaleSlot + (stage & 15); };
+        uint32_t sa[WA], sb[WB], ta[WA], tb[WB];
+        const int sa_at = G::kRingBytes + w.row0 / 64 * 64 + 4 * r, sb_at = G::kRingBytes + G::kTileM + w.col0 / 64 * 64 + 4 * r;
+        // wave tiles of 32 rows start in the middle of a word
+        const int a_shift = FI < 4 ? w.row0 % 64 / 2 : 0, b_shift = FJ < 4 ? w.col0 % 64 / 2 : 0;
+        auto take_scales = [&](int stage, uint32_t (&xa)[WA], uint32_t (&xb)[WB]) {
+            const uint8_t *src = lds + ((stage >> 4) & 1) * G::kScaleSlot + (stage & 15) * (G::kTileM + G::kTileN);
+#pragma unroll
+            for (int k = 0; k < WA; ++k) xa[k] = *reinterpret_cast<const uint32_t *>(src + sa_at + 64 * k) >> a_shift;
+#pragma unroll
+            for (int k = 0; k < WB; ++k) xb[k] = *reinterpret_cast<const uint32_t *>(src + sb_at + 64 * k) >> b_shift;
+        };
         auto take_a = [&](int stage, int i) {
             fa[i][0] = read_a(buffer(stage) + chunk0, i);
             fa[i][1] = read_a(buffer(stage) + chunk1, i);
-            sa[i] = scales(stage)[sa_at + 256 * i];
         };
         auto take_b = [&](int stage, int j) {
             fb[j][0] = read_b(buffer(stage) + chunk0, j);
             fb[j][1] = read_b(buffer(stage) + chunk1, j);
-            sb[j] = scales(stage)[sb_at + 256 * j];
         };
-        auto mfma = [&](int i, int j) { E::mfma(acc[i][j], fb[j][0], fb[j][1], fa[i][0], fa[i][1], sb[j], sa[i]); };
+        auto mfma = [&](auto I, auto J) {
+            constexpr int i = decltype(I)::value, j = decltype(J)::value;
+            E::template mfma<j % 4, i % 4>(acc[i][j], fb[j][0], fb[j][1], fa[i][0], fa[i][1], sb[j / 4], sa[i / 4]);
+        };
 #pragma unroll
         for (int j = 0; j < FJ; ++j) take_b(first, j);
 #pragma unroll
         for (int i = 0; i < H; ++i) take_a(first, i);
+        take_scales(first, sa, sb);
+        u32x4 next_scales = {};
         for (int s = first; s < end; ++s) {
             // the upper rows; the lower rows' fragments are read behind each group of MFMAs
-#pragma unroll
-            for (int i = 0; i < H; ++i) {
-                take_a(s, H + i);
-#pragma unroll
-                for (int j = 0; j < FJ; ++j) mfma(i, j);
+            each<H>([&](auto I) {
+                take_a(s, H + decltype(I)::value);
+                each<FJ>([&](auto J) { mfma(I, J); });
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
                 __builtin_amdgcn_sched_group_barrier(0x008, FJ - 1, 0);
-            }
+            });
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
             wait_vmcnt<(NB - 2) * G::kDmaPerStage>();
             barrier();
-            if ((s & 15) == 0) dma_scales((s >> 4) + 1);
+            // the next 16 stages' scales: asked for early in these 16, laid down in the middle of them (those of a
+            // split that starts between the two are there already)
+            if ((s & 15) == 2) next_scales = load_scales((s >> 4) + 1);
+            if ((s & 15) == 8 && s - 6 >= first) put_scales((s >> 4) + 1, next_scales);
             dma(s + NB);
+            take_scales(s + 1, ta, tb);
             // the lower rows column by column; column j's fragments and those of upper row j follow it
-#pragma unroll
-            for (int j = 0; j < FJ; ++j) {
-#pragma unroll
-                for (int i = 0; i < H; ++i) mfma(H + i, j);
+            each<FJ>([&](auto J) {
+                constexpr int j = decltype(J)::value;
+                each<H>([&](auto I) { mfma(std::integral_constant<int, H + decltype(I)::value>(), J); });
                 __builtin_amdgcn_sched_barrier(0);
                 take_b(s + 1, j);
                 if (j < H) take_a(s + 1, j);
-            }
+            });
             __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < WA; ++k) sa[k] = ta[k];
+#pragma unroll
+            for (int k = 0; k < WB; ++k) sb[k] = tb[k];
         }
         static_assert(H <= FJ, "an upper row for each column");
     }
