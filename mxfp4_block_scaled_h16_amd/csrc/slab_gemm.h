@@ -125,16 +125,15 @@ struct Geo {
     static constexpr int kDmaPerStage = kDmaA + kDmaB;
     static_assert(kDmaA * kRowsPerDma * NW == TM && kDmaB * kRowsPerDma * NW == TN, "whole loads per wavefront");
     static_assert(TM + TN <= 64 * NW, "a thread for each row's scales");
-    // a wavefront's part of the LDS in the epilogue: 32 rows of its tile in FP32, and transposed in 16 bits; behind
-    // all of them 16 bytes for each row of the tile
+    // a wavefront's part of the LDS in the epilogue, 32 rows of its tile in FP32: one stage buffer in all
     static constexpr int kBlockRows = 32, kEpiBlocks = kWaveRows / kBlockRows;
-    static constexpr int kEpiWave = kBlockRows * kWaveCols * (4 + 2), kEpiBytes = NW * kEpiWave;
-    static constexpr int kRowInfo = kEpiBytes;
+    static constexpr int kEpiWave = kBlockRows * kWaveCols * 4;
+    static_assert(NW * kEpiWave <= kStageBytes, "the epilogue works in a stage buffer");
+    // behind the stage buffers: scales, or 16 bytes for each row of the tile for the epilogue's use
     template <class E>
     static constexpr int lds_bytes()
     {
-        const int main = kRingBytes + (E::kScaled ? 2 * kScaleSlot : 0), epi = kEpiBytes + TM * 16;
-        return main > epi ? main : epi;
+        return kRingBytes + (E::kScaled ? 2 * kScaleSlot : TM * 16);
     }
     static constexpr int kMinBlocks = kRingBytes + 2 * kScaleSlot <= 80 * 1024 ? 2 : 1;   // workgroups per CU
 };
@@ -234,8 +233,9 @@ __device__ __forceinline__ void place(Where &w, const Operands &op, int t)
 
 // -------------------------------------------------------------------------------- the kernel --
 // Epi: a trivially copyable functor with kSym and
-//   template <class G> __device__ void run(f32x4 (&acc)[FI][FJ], const Where &, const Operands &, uint8_t *lds)
-// called by every wavefront once the stage buffers are free.
+//   template <class G> __device__ void run(f32x4 (&acc)[FI][FJ], const Where &, const Operands &, uint8_t *lds, uint8_t *info)
+// called by every wavefront with a stage buffer that nothing else uses (lds) and, for 16-bit operands, 16 bytes
+// of LDS for each row of the tile (info).
 //
 // A stage is worked in two halves of its MFMAs. During the first, the fragments of the second are
 // read from the LDS; then nothing of the stage is left to read, and one barrier says both that its
@@ -247,17 +247,18 @@ template <class E, class G, class Epi>
 __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Operands op, Epi epi)
 {
 #if defined(__HIP_DEVICE_COMPILE__)   // the buffer-resource builtins do not exist in the host's pass
-    constexpr int FI = G::FI, FJ = G::FJ;
+    constexpr int FI = G::FI, FJ = G::FJ, NB = G::kBuffers;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[G::template lds_bytes<E>()];
 
     // this workgroup's tile and stages
     Where w;
     int first = 0, end = op.nk, split_tile = -1, split = 0;
-    if ((int)blockIdx.x < op.whole) {
-        place<G, Epi>(w, op, spread(blockIdx.x, op.whole));
+    const int tile = blockIdx.x;
+    if (tile < op.whole) {
+        place<G, Epi>(w, op, spread(tile, op.whole));
     } else {
         const int rest = (int)gridDim.x - op.whole, tail = rest / op.splits;
-        const int i = spread((int)blockIdx.x - op.whole, rest);
+        const int i = spread(tile - op.whole, rest);
         split = i / tail;
         split_tile = i - split * tail;
         place<G, Epi>(w, op, op.whole + split_tile);
@@ -268,27 +269,39 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
 
     // load u of this wavefront fills rows [8 (kDma wave + u), + 8) of the stage: lane L the 16 bytes at
     // row L / 8, physical chunk L % 8, from the row's chunk (L % 8) ^ perm(row)
-    const uint8_t *abase = op.a + w.batch * op.batch_a + (int64_t)w.m0 * op.lda;
-    const uint8_t *bbase = op.b + w.batch * op.batch_b + (int64_t)w.n0 * op.ldb;
-    const auto arsrc = __builtin_amdgcn_make_buffer_rsrc((void *)abase, 0, 0xFFFFFFFFu, 0x00027000);
-    const auto brsrc = __builtin_amdgcn_make_buffer_rsrc((void *)bbase, 0, 0xFFFFFFFFu, 0x00027000);
     const int a_row0 = kRowsPerDma * G::kDmaA * w.wave, b_row0 = kRowsPerDma * G::kDmaB * w.wave;
+    const uint8_t *abase, *bbase;
     uint32_t aoff[G::kDmaA], boff[G::kDmaB];
+    // E4M3: a thread per row of the tile (A's first, then B's) takes the scales of 16 stages, 16 bytes, and lays
+    // them into one of two slots of the LDS: [stage][64 rows][row % 16][row / 16], so that a lane has the
+    // scales of its row in four 16-row tiles in one word.
+    const uint8_t *srow = nullptr;
+    auto aim = [&](const Where &t) {   // the loads' addresses for tile t
+        abase = op.a + t.batch * op.batch_a + (int64_t)t.m0 * op.lda;
+        bbase = op.b + t.batch * op.batch_b + (int64_t)t.n0 * op.ldb;
 #pragma unroll
-    for (int u = 0; u < G::kDmaA; ++u) {
-        const int row = a_row0 + kRowsPerDma * u + lane / 8;
-        aoff[u] = (uint32_t)min(row, op.M - 1 - w.m0) * (uint32_t)op.lda + 16u * ((lane % 8) ^ chunk_perm(row));
-    }
+        for (int u = 0; u < G::kDmaA; ++u) {
+            const int row = a_row0 + kRowsPerDma * u + lane / 8;
+            aoff[u] = (uint32_t)min(row, op.M - 1 - t.m0) * (uint32_t)op.lda + 16u * ((lane % 8) ^ chunk_perm(row));
+        }
 #pragma unroll
-    for (int u = 0; u < G::kDmaB; ++u) {
-        const int row = b_row0 + kRowsPerDma * u + lane / 8;
-        boff[u] = (uint32_t)min(row, op.N - 1 - w.n0) * (uint32_t)op.ldb + 16u * ((lane % 8) ^ chunk_perm(row));
-    }
-    constexpr int NB = G::kBuffers;
-    auto dma = [&](int stage) {
-        // past the last stage the last one again, into a free buffer
-        const int at = min(stage, end - 1) * kRowBytes;
-        uint8_t *dst = lds + (stage & (NB - 1)) * G::kStageBytes;
+        for (int u = 0; u < G::kDmaB; ++u) {
+            const int row = b_row0 + kRowsPerDma * u + lane / 8;
+            boff[u] = (uint32_t)min(row, op.N - 1 - t.n0) * (uint32_t)op.ldb + 16u * ((lane % 8) ^ chunk_perm(row));
+        }
+    };
+    auto aim_scales = [&](const Where &t) {
+        const bool is_b = (int)threadIdx.x >= G::kTileM;
+        const int row = min((int)threadIdx.x, G::kTileM + G::kTileN - 1) - (is_b ? G::kTileM : 0);
+        srow = is_b ? op.bs + (int64_t)(t.n0 + min(row, op.N - 1 - t.n0)) * op.ldbs
+                    : op.as + (int64_t)(t.m0 + min(row, op.M - 1 - t.m0)) * op.ldas;
+    };
+    aim(w);
+    auto buffer = [&](int stage) { return lds + (stage & (NB - 1)) * G::kStageBytes; };
+    auto dma = [&](int stage, uint8_t *dst) {
+        const auto arsrc = __builtin_amdgcn_make_buffer_rsrc((void *)abase, 0, 0xFFFFFFFFu, 0x00027000);
+        const auto brsrc = __builtin_amdgcn_make_buffer_rsrc((void *)bbase, 0, 0xFFFFFFFFu, 0x00027000);
+        const int at = stage * kRowBytes;
 #pragma unroll
         for (int u = 0; u < G::kDmaA; ++u)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(arsrc, (lds_void_t *)(dst + a_row0 * kRowBytes + u * 1024), 16, aoff[u],
@@ -298,23 +311,17 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
             __builtin_amdgcn_raw_ptr_buffer_load_lds(brsrc, (lds_void_t *)(dst + G::kABytes + b_row0 * kRowBytes + u * 1024),
                                                      16, boff[u], at, 0, 0);
     };
-    // E4M3: a thread per row of the tile (A's first, then B's) takes the scales of 16 stages, 16 bytes, and lays
-    // them into one of two slots of the LDS: [stage][64 rows][row % 16][row / 16], so that a lane has the
-    // scales of its row in four 16-row tiles in one word.
-    const uint8_t *srow = nullptr;
-    int sput = 0;
+    // the loads behind the barrier of stage s; past the last stage the last one again, into a free buffer, so that
+    // every wait counts alike
+    auto load_ahead = [&](int s) { dma(min(s + NB, end - 1), buffer(s + NB)); };
     const int last_group = (end - 1) / 16;
-    if constexpr (E::kScaled) {
-        const bool is_b = (int)threadIdx.x >= G::kTileM;
-        const int row = min((int)threadIdx.x, G::kTileM + G::kTileN - 1) - (is_b ? G::kTileM : 0);
-        srow = is_b ? op.bs + (int64_t)(w.n0 + min(row, op.N - 1 - w.n0)) * op.ldbs
-                    : op.as + (int64_t)(w.m0 + min(row, op.M - 1 - w.m0)) * op.ldas;
-        sput = G::kRingBytes + (is_b ? G::kTileM : 0) + row / 64 * 64 + row % 16 * 4 + row % 64 / 16;
-    }
     auto load_scales = [&](int g) { return *reinterpret_cast<const u32x4 *>(srow + (int64_t)min(g, last_group) * 16); };
     auto put_scales = [&](int g, const u32x4 &v) {
         if (G::kTileM + G::kTileN < 64 * G::NW && (int)threadIdx.x >= G::kTileM + G::kTileN) return;
-        uint8_t *dst = lds + (g & 1) * G::kScaleSlot + sput;
+        const bool is_b = (int)threadIdx.x >= G::kTileM;
+        const int row = (int)threadIdx.x - (is_b ? G::kTileM : 0);
+        uint8_t *dst = lds + G::kRingBytes + (g & 1) * G::kScaleSlot + (is_b ? G::kTileM : 0) + row / 64 * 64 +
+                       row % 16 * 4 + row % 64 / 16;
 #pragma unroll
         for (int k = 0; k < 16; ++k) dst[k * (G::kTileM + G::kTileN)] = (uint8_t)(v[k / 4] >> (8 * (k % 4)));
     };
@@ -322,7 +329,6 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
     const int perm = chunk_perm(r);
     const int a_frag = (w.row0 + r) * kRowBytes, b_frag = G::kABytes + (w.col0 + r) * kRowBytes;
     const int chunk0 = 16 * (q ^ perm), chunk1 = 16 * ((4 + q) ^ perm);
-    auto buffer = [&](int stage) { return lds + (stage & (NB - 1)) * G::kStageBytes; };
     auto read_a = [&](const uint8_t *src, int i) { return *reinterpret_cast<const u32x4 *>(src + a_frag + 16 * i * kRowBytes); };
     auto read_b = [&](const uint8_t *src, int j) { return *reinterpret_cast<const u32x4 *>(src + b_frag + 16 * j * kRowBytes); };
 
@@ -333,31 +339,66 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
         for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{};
 
     if constexpr (E::kScaled) {
+        aim_scales(w);
         const u32x4 v0 = load_scales(first >> 4), v1 = load_scales((first >> 4) + 1);
         put_scales(first >> 4, v0);
         put_scales((first >> 4) + 1, v1);
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): for the barrier below
     }
 #pragma unroll
-    for (int k = 0; k < NB; ++k) dma(first + k);
+    for (int k = 0; k < NB; ++k) dma(min(first + k, end - 1), buffer(first + k));
     wait_vmcnt<(NB - 1) * G::kDmaPerStage>();
     barrier();
 
+    // 16-bit: the fragments of a half stage, twice. 8-bit: of a stage, and its scales.
+    u32x4 fa0[FI], fb0[FJ], fa1[FI], fb1[FJ];
+    auto read = [&](const uint8_t *src, u32x4 (&fa)[FI], u32x4 (&fb)[FJ]) {
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) fb[j] = read_b(src, j);
+#pragma unroll
+        for (int i = 0; i < FI; ++i) fa[i] = read_a(src, i);
+    };
+    constexpr int H = FI / 2, WA = (FI + 3) / 4, WB = (FJ + 3) / 4;
+    static_assert(H <= FJ, "an upper row for each column");
+    uint32_t sa[WA], sb[WB], ta[WA], tb[WB];
+    u32x4 next_scales = {};
+    auto take_scales = [&](int stage, int slot, uint32_t (&xa)[WA], uint32_t (&xb)[WB]) {
+        // wave tiles of 32 rows start in the middle of a word
+        const int a_shift = FI < 4 ? w.row0 % 64 / 2 : 0, b_shift = FJ < 4 ? w.col0 % 64 / 2 : 0;
+        const uint8_t *src =
+            lds + G::kRingBytes + (slot & 1) * G::kScaleSlot + (stage & 15) * (G::kTileM + G::kTileN) + 4 * r;
+#pragma unroll
+        for (int k = 0; k < WA; ++k)
+            xa[k] = *reinterpret_cast<const uint32_t *>(src + w.row0 / 64 * 64 + 64 * k) >> a_shift;
+#pragma unroll
+        for (int k = 0; k < WB; ++k)
+            xb[k] = *reinterpret_cast<const uint32_t *>(src + G::kTileM + w.col0 / 64 * 64 + 64 * k) >> b_shift;
+    };
+    auto take_a = [&](const uint8_t *src, int i) {
+        fa0[i] = read_a(src + chunk0, i);
+        fa1[i] = read_a(src + chunk1, i);
+    };
+    auto take_b = [&](const uint8_t *src, int j) {
+        fb0[j] = read_b(src + chunk0, j);
+        fb1[j] = read_b(src + chunk1, j);
+    };
+    // the tile's first fragments
     if constexpr (!E::kScaled) {
-        u32x4 fa0[FI], fb0[FJ], fa1[FI], fb1[FJ];
-        auto read = [&](const uint8_t *src, u32x4 (&fa)[FI], u32x4 (&fb)[FJ]) {
+        read(buffer(first) + chunk0, fa0, fb0);
+    } else {
 #pragma unroll
-            for (int j = 0; j < FJ; ++j) fb[j] = read_b(src, j);
+        for (int j = 0; j < FJ; ++j) take_b(buffer(first), j);
 #pragma unroll
-            for (int i = 0; i < FI; ++i) fa[i] = read_a(src, i);
-        };
+        for (int i = 0; i < H; ++i) take_a(buffer(first), i);
+        take_scales(first, first >> 4, sa, sb);
+    }
+    if constexpr (!E::kScaled) {
         auto mfmas = [&](const u32x4 (&fa)[FI], const u32x4 (&fb)[FJ]) {
 #pragma unroll
             for (int i = 0; i < FI; ++i)
 #pragma unroll
                 for (int j = 0; j < FJ; ++j) E::mfma(acc[i][j], fb[j], fa[i]);
         };
-        read(buffer(first) + chunk0, fa0, fb0);
         constexpr int kMfma = FI * FJ, kReads = FI + FJ, kLoads = G::kDmaPerStage;
         constexpr int kPer = kMfma / kReads;   // MFMAs per read in the first half
         for (int s = first; s < end; ++s) {
@@ -375,10 +416,10 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
             __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the stage has been read
             wait_vmcnt<(NB - 2) * G::kDmaPerStage>();   // stage s + 1 has landed
             barrier();
-            dma(s + NB);
+            // the loads at once: they have the longest way to go
+            load_ahead(s);
             read(buffer(s + 1) + chunk0, fa0, fb0);
             mfmas(fa1, fb1);
-            // the loads at once: they have the longest way to go
             if constexpr (kLoads + kReads <= kMfma) {
 #pragma unroll
                 for (int k = 0; k < kLoads; ++k) {
@@ -395,41 +436,15 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
             __builtin_amdgcn_sched_barrier(0);
         }
     } else {
-        constexpr int H = FI / 2, WA = (FI + 3) / 4, WB = (FJ + 3) / 4;
-        u32x4 fa[FI][2], fb[FJ][2];
-        uint32_t sa[WA], sb[WB], ta[WA], tb[WB];
-        const int sa_at = G::kRingBytes + w.row0 / 64 * 64 + 4 * r, sb_at = G::kRingBytes + G::kTileM + w.col0 / 64 * 64 + 4 * r;
-        // wave tiles of 32 rows start in the middle of a word
-        const int a_shift = FI < 4 ? w.row0 % 64 / 2 : 0, b_shift = FJ < 4 ? w.col0 % 64 / 2 : 0;
-        auto take_scales = [&](int stage, uint32_t (&xa)[WA], uint32_t (&xb)[WB]) {
-            const uint8_t *src = lds + ((stage >> 4) & 1) * G::kScaleSlot + (stage & 15) * (G::kTileM + G::kTileN);
-#pragma unroll
-            for (int k = 0; k < WA; ++k) xa[k] = *reinterpret_cast<const uint32_t *>(src + sa_at + 64 * k) >> a_shift;
-#pragma unroll
-            for (int k = 0; k < WB; ++k) xb[k] = *reinterpret_cast<const uint32_t *>(src + sb_at + 64 * k) >> b_shift;
-        };
-        auto take_a = [&](int stage, int i) {
-            fa[i][0] = read_a(buffer(stage) + chunk0, i);
-            fa[i][1] = read_a(buffer(stage) + chunk1, i);
-        };
-        auto take_b = [&](int stage, int j) {
-            fb[j][0] = read_b(buffer(stage) + chunk0, j);
-            fb[j][1] = read_b(buffer(stage) + chunk1, j);
-        };
         auto mfma = [&](auto I, auto J) {
             constexpr int i = decltype(I)::value, j = decltype(J)::value;
-            E::template mfma<j % 4, i % 4>(acc[i][j], fb[j][0], fb[j][1], fa[i][0], fa[i][1], sb[j / 4], sa[i / 4]);
+            E::template mfma<j % 4, i % 4>(acc[i][j], fb0[j], fb1[j], fa0[i], fa1[i], sb[j / 4], sa[i / 4]);
         };
-#pragma unroll
-        for (int j = 0; j < FJ; ++j) take_b(first, j);
-#pragma unroll
-        for (int i = 0; i < H; ++i) take_a(first, i);
-        take_scales(first, sa, sb);
-        u32x4 next_scales = {};
         for (int s = first; s < end; ++s) {
             // the upper rows; the lower rows' fragments are read behind each group of MFMAs
+            const uint8_t *now = buffer(s), *then = buffer(s + 1);
             each<H>([&](auto I) {
-                take_a(s, H + decltype(I)::value);
+                take_a(now, H + decltype(I)::value);
                 each<FJ>([&](auto J) { mfma(I, J); });
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
@@ -439,19 +454,19 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
             __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
             wait_vmcnt<(NB - 2) * G::kDmaPerStage>();
             barrier();
-            // the next 16 stages' scales: asked for early in these 16, laid down in the middle of them (those of a
-            // split that starts between the two are there already)
-            if ((s & 15) == 2) next_scales = load_scales((s >> 4) + 1);
-            if ((s & 15) == 8 && s - 6 >= first) put_scales((s >> 4) + 1, next_scales);
-            dma(s + NB);
-            take_scales(s + 1, ta, tb);
+            // the next 16 stages' scales: asked for early in these 16, laid down in the middle of them (those of
+            // a split that starts between the two are there already)
+            if ((s & 15) == 2 && (s >> 4) < last_group) next_scales = load_scales((s >> 4) + 1);
+            if ((s & 15) == 8 && (s >> 4) < last_group && s - 6 >= first) put_scales((s >> 4) + 1, next_scales);
+            load_ahead(s);
+            take_scales(s + 1, (s + 1) >> 4, ta, tb);
             // the lower rows column by column; column j's fragments and those of upper row j follow it
             each<FJ>([&](auto J) {
                 constexpr int j = decltype(J)::value;
                 each<H>([&](auto I) { mfma(std::integral_constant<int, H + decltype(I)::value>(), J); });
                 __builtin_amdgcn_sched_barrier(0);
-                take_b(s + 1, j);
-                if (j < H) take_a(s + 1, j);
+                take_b(then, j);
+                if (j < H) take_a(then, j);
             });
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -459,9 +474,8 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
 #pragma unroll
             for (int k = 0; k < WB; ++k) sb[k] = tb[k];
         }
-        static_assert(H <= FJ, "an upper row for each column");
     }
-    // the stage buffers are free for the epilogue: every load has landed and every wavefront is past its reads
+    // the last stage's buffer is the epilogue's: every load has landed and every wavefront is past its reads
     wait_vmcnt<0>();
     __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
     barrier();
@@ -473,7 +487,7 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
             for (int j = 0; j < FJ; ++j) out[(i * FJ + j) * 64 * G::NW] = acc[i][j];
         return;
     }
-    epi.template run<G>(acc, w, op, lds);
+    epi.template run<G>(acc, w, op, buffer(end - 1), lds + G::kRingBytes);
 #endif
 }
 
@@ -483,7 +497,7 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void product_kernel(Oper
 template <class G, class Epi>
 __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void finish_kernel(Operands op, Epi epi)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kEpiBytes + G::kTileM * 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kStageBytes + G::kTileM * 16];
     const int tile = blockIdx.x / G::kEpiBlocks, blk = blockIdx.x % G::kEpiBlocks;
     Where w;
     place<G, Epi>(w, op, op.whole + tile);
@@ -506,7 +520,7 @@ __global__ __launch_bounds__(64 * G::NW, G::kMinBlocks) void finish_kernel(Opera
     for (int i = 0; i < G::FI; ++i)
 #pragma unroll
         for (int j = 0; j < G::FJ; ++j) acc[i][j] = sum[i % 2][j];
-    epi.template run<G>(acc, w, op, lds);
+    epi.template run<G>(acc, w, op, lds, lds + G::kStageBytes);
 }
 
 // ------------------------------------------------------------------------- plain epilogue -----
@@ -583,7 +597,8 @@ struct StoreEpi {
     const float *factors = nullptr;
 
     template <class G>
-    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds,
+                                        uint8_t *) const
     {
         run_with<G>(acc, w, op, lds, [](int, int) { return 0; }, [](f32x4 (&)[2], int) {});
     }
@@ -695,15 +710,15 @@ struct StoreEpi {
 // values one word.
 //
 // A block of the accumulators goes through the LDS in FP32; one code serves all blocks, as it is fetched for
-// one use. For the transposed a lane swaps four of its eight columns against the next row's, so
-// that it holds two rows of four columns and writes words; its lines are 64 bytes.
+// one use. For the transposed a lane swaps four of its eight columns against the next row's, so that it holds
+// two rows of four columns, and writes them as words where the block was; its lines are 64 bytes.
 template <class G, class Pack, class Fetch, class Make>
 __device__ __forceinline__ void store_tile16(f32x4 (&acc)[G::FI][G::FJ], const Where &w, uint8_t *lds, Pack pack, Fetch fetch,
                                              Make make, uint16_t *rows, int64_t ld_rows, uint16_t *cols, int64_t ld_cols)
 {
     using B = Block32<G>;
     constexpr int kLine = B::kRows * 2, kPieces = kLine / 16;   // the transposed block: kCols lines
-    uint8_t *block = lds + w.wave * G::kEpiWave, *turned = block + B::kBytes;
+    uint8_t *block = lds + w.wave * G::kEpiWave;
     const int line = w.lane / B::kLanes, c8 = w.lane % B::kLanes, n = w.n0 + w.col0 + 8 * c8;
     const bool odd = line & 1;
     // 16-byte pieces of the transposed lines, XOR-permuted by the column
@@ -722,6 +737,7 @@ __device__ __forceinline__ void store_tile16(f32x4 (&acc)[G::FI][G::FJ], const W
         for (int p = 0; p < B::kPasses; ++p) got[p] = fetch(m + B::kLinesPerPass * p + line, n);
         B::put(block, w.lane, acc, blk);
         uint16_t *at = rows + (int64_t)(m + line) * ld_rows + n;
+        uint32_t pairs[B::kPasses][4];
 #pragma unroll
         for (int p = 0; p < B::kPasses; ++p) {
             const int l = B::kLinesPerPass * p + line;
@@ -738,22 +754,26 @@ __device__ __forceinline__ void store_tile16(f32x4 (&acc)[G::FI][G::FJ], const W
                     // even lines keep columns 0 .. 3 and get those of the line below; odd ones keep 4 .. 7
                     const uint32_t got_word = next_row(odd ? word[h] : word[2 + h]);
                     const uint32_t up = odd ? got_word : word[h], dn = odd ? word[2 + h] : got_word;
-                    const int c = 8 * c8 + (odd ? 4 : 0) + 2 * h, r = l & ~1;
-                    *reinterpret_cast<uint32_t *>(turned + piece(c, r >> 3) + 2 * (r & 7)) =
-                        __builtin_amdgcn_perm(dn, up, 0x05040100u);
-                    *reinterpret_cast<uint32_t *>(turned + piece(c + 1, r >> 3) + 2 * (r & 7)) =
-                        __builtin_amdgcn_perm(dn, up, 0x07060302u);
+                    pairs[p][2 * h] = __builtin_amdgcn_perm(dn, up, 0x05040100u);
+                    pairs[p][2 * h + 1] = __builtin_amdgcn_perm(dn, up, 0x07060302u);
                 }
             }
         }
         if (cols) {
+#pragma unroll
+            for (int p = 0; p < B::kPasses; ++p)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int c = 8 * c8 + (odd ? 4 : 0) + h, l = (B::kLinesPerPass * p + line) & ~1;
+                    *reinterpret_cast<uint32_t *>(block + piece(c, l >> 3) + 2 * (l & 7)) = pairs[p][h];
+                }
             constexpr int kColsPerPass = 64 / kPieces;
             const int col = w.lane / kPieces, pc = w.lane % kPieces;
             uint16_t *to = cols + (int64_t)(w.n0 + w.col0 + col) * ld_cols + m + 8 * pc;
 #pragma unroll
             for (int p = 0; p < B::kCols / kColsPerPass; ++p)
                 *reinterpret_cast<u32x4 *>(to + (int64_t)kColsPerPass * p * ld_cols) =
-                    *reinterpret_cast<const u32x4 *>(turned + piece(kColsPerPass * p + col, pc));
+                    *reinterpret_cast<const u32x4 *>(block + piece(kColsPerPass * p + col, pc));
         }
     }
 }

@@ -36,7 +36,7 @@ struct StatsEpi {
     const int64_t *target;
 
     template <class G>
-    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds, [[maybe_unused]] uint8_t *info_at) const
     {
         const int r = w.lane & 15, q = w.lane >> 4;
         float2 *slots = reinterpret_cast<float2 *>(lds);   // [wave column][row of the tile]
@@ -176,11 +176,11 @@ struct GradEpi {
     int64_t ldg, ldt;
 
     template <class G>
-    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds, [[maybe_unused]] uint8_t *info_at) const
     {
         // of each row of the tile: scaled dl and dp, lse in base 2, and the target's column in the piece (-1: no
         // column of it, or a row without a gradient of its loss)
-        f32x4 *info = reinterpret_cast<f32x4 *>(lds + G::kRowInfo);
+        f32x4 *info = reinterpret_cast<f32x4 *>(info_at);
         const float scale = ranges->g;
         for (int row = threadIdx.x; row < G::kTileM; row += 64 * G::NW) {
             const int m = w.m0 + row;
