@@ -6,11 +6,19 @@
 // products run on the FP16 matrix cores with FP32 accumulation. FP16 holds 2^10 X, 2^10 A and
 // 2^10 (b A + c A A): every entry of X stays below 1.3 and of the others below 3 in magnitude
 // (singular values of X lie in [0, 1.3] at every step for the usual coefficients), so nothing
-// overflows, and entries down to 2^-24 keep all 11 bits. X itself is carried from step to step in two FP16
+// overflows (other coefficients are checked on the host to stay within FP16, t is held to 16), and entries down to 2^-24 keep all 11 bits. X itself is carried from step to step in two FP16
 // numbers, value and remainder (22 bits): the term a X, which carries the small singular values,
 // loses nothing, and what the 11-bit operands add stays below the rounding of a bf16 result
-// (relative error 0.0004 to 0.0016 against bf16's 0.0017; with X in FP16 alone a matrix of a few
-// strong directions was off by 0.011, with bf16 operands by 0.09).
+// (with X in FP16 alone a matrix of a few strong directions was off by 0.011, with bf16 operands by 0.09).
+//
+// Near singular values of 1 the two terms of the update nearly cancel, and the roundings of b A + c A A and
+// of the X that it is multiplied by count |b + c| times (2.7). A step may as well be (a - t) X +
+// (b A + c A A + t) X: with t = -(b + c) they count next to nothing there, but t times for the directions that
+// are still small, and what those pick up grows with them in the steps that follow. So the last step takes
+// t = -(b + c), the two before it a half and a quarter of it, and the others none. Relative error in five steps
+// (16 x 16 to 486 x 900, heavy tails): 0.0007 to 0.0016, without t 0.0014 to 0.0029; a few strong directions
+// over noise 1/1000 of them: 0.0016, without t 0.0004, with t = -(b + c) in every step 0.03. A bf16 result's own
+// rounding is 0.0017.
 //
 // Per step three launches: A (symmetric: the lower triangle of tiles, written twice), b A + c A A
 // (symmetric too), and the update, which writes X in both orientations for the next step's
@@ -61,13 +69,13 @@ struct GramEpi {
     }
 };
 
-// b A + c A A: 2^20 A A in acc, 2^10 A read
+// b A + c A A + t: 2^20 A A in acc, 2^10 A read
 struct PolyEpi {
     static constexpr bool kSym = true;
     const uint16_t *gram;
     uint16_t *out;
     int64_t ld, batch_out;
-    float b, c;
+    float b, c, t;
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds, uint8_t *) const
     {
@@ -76,11 +84,16 @@ struct PolyEpi {
         const float cs = c * kUnscale;
         store_tile16<G>(acc, w, lds, [](float x, float y) { return pack_f16(x, y); },
                         [&](int m, int n) { return *reinterpret_cast<const u32x4 *>(in + (int64_t)m * ld + n); },
-                        [&](f32x4 (&v)[2], const u32x4 &gram8, int, int) {
+                        [&](f32x4 (&v)[2], const u32x4 &gram8, int m, int n) {
                             f32x4 g[2];
                             f16_eight(gram8, g);
-                            v[0] = b * g[0] + cs * v[0];
-                            v[1] = b * g[1] + cs * v[1];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                v[k] = b * g[k] + cs * v[k];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (m == n + 4 * k + e) v[k][e] += 1024.0f * t;
+                            }
                         },
                         o, ld, w.m0 == w.n0 ? nullptr : o, ld);
     }
@@ -103,7 +116,7 @@ __device__ __forceinline__ TwoPart two_part(const uint16_t *hi, const uint16_t *
     return TwoPart{*reinterpret_cast<const u32x4 *>(hi + at), *reinterpret_cast<const u32x4 *>(lo + at)};
 }
 
-// a X + (b A + c A A) X in X's own orientation: value (both orientations) and remainder
+// (a - t) X + (b A + c A A + t) X in X's own orientation: value (both orientations) and remainder
 struct UpdateEpi {
     static constexpr bool kSym = false;
     const uint16_t *hi;      // X [mp][np]
@@ -410,6 +423,8 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
     const bool wide = p.m <= p.n;
     for (int k = 0; k < p.steps; ++k) {
         const uint16_t *x = s.hi[k & 1], *t = s.turned[k & 1];
+        const int after = p.steps - 1 - k;
+        const float shift = after < 3 ? std::min(16.0f, std::max(-16.0f, -(p.b + p.c))) / (float)(1 << after) : 0.0f;
         Operands op{};
         // A: rows of X (wide) or of its transpose
         op.a = op.b = reinterpret_cast<const uint8_t *>(wide ? x : t);
@@ -422,7 +437,7 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
         op.lda = op.ldb = 2 * z.sp;
         op.nk = (int)(z.sp / 64);
         op.batch_a = op.batch_b = 2 * ba;
-        if ((e = product(z.poly, op, PolyEpi{s.gram, s.poly, z.sp, ba, p.b, p.c}, s, stream))) return e;
+        if ((e = product(z.poly, op, PolyEpi{s.gram, s.poly, z.sp, ba, p.b, p.c, shift}, s, stream))) return e;
         // the update in X's orientation: poly X for wide, X poly for tall (poly is symmetric)
         op.a = reinterpret_cast<const uint8_t *>(wide ? s.poly : x);
         op.lda = 2 * (wide ? z.sp : z.np);
@@ -434,15 +449,15 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
         op.M = (int)z.mp;
         op.N = (int)z.np;
         if (k + 1 < p.steps) {
-            const UpdateEpi epi{x, s.lo, s.hi[(k + 1) & 1], s.turned[(k + 1) & 1], z.np, z.mp, bx, p.a};
+            const UpdateEpi epi{x, s.lo, s.hi[(k + 1) & 1], s.turned[(k + 1) & 1], z.np, z.mp, bx, p.a - shift};
             if ((e = product(z.update, op, epi, s, stream))) return e;
         } else {
             op.M = (int)p.m;
             op.N = (int)p.n;
             const float alpha = p.alpha * kUnscale;
-            e = p.out_bf16 ? product(z.last, op, LastEpi<true>{x, s.lo, z.np, bx, p.a,
+            e = p.out_bf16 ? product(z.last, op, LastEpi<true>{x, s.lo, z.np, bx, p.a - shift,
                                                               StoreEpi<true>{p.out, p.ldo, p.batch_o, alpha, p.beta}}, s, stream)
-                           : product(z.last, op, LastEpi<false>{x, s.lo, z.np, bx, p.a,
+                           : product(z.last, op, LastEpi<false>{x, s.lo, z.np, bx, p.a - shift,
                                                                StoreEpi<false>{p.out, p.ldo, p.batch_o, alpha, p.beta}}, s, stream);
             if (e) return e;
         }
