@@ -1,0 +1,75 @@
+"""The training operators at shapes that take each way of working a product: tiles of three sizes, whole, split over the
+contraction, and both in one launch."""
+import pytest
+import torch
+
+from tests.gpu_util import announce, require_gpu
+from tests.test_gpu_orthogonalize import BF16, COEFFS, OWN
+from tests.test_gpu_xent import _check, _problem
+
+pytestmark = pytest.mark.gpu
+# rows, columns, contraction in stages of 128 bytes
+SHAPES = [(16, 16, 1), (16, 16, 32), (1300, 1537, 1), (512, 4200, 40), (1537, 5000, 72), (1537, 5000, 1), (700, 4096, 152),
+          (4096, 4200, 16)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _mx():
+    import mxfp4_block_scaled_h16_amd as mx
+    return mx
+
+
+@pytest.mark.parametrize("M,N,stages", SHAPES)
+def test_fp8_products_of_small_integers(M, N, stages):
+    """Codes of 0, +-1, +-2 and scales of 1, 2 or 1/2: products are at most 16, and sums multiples of 1/4 below 2^19
+    that FP32 holds exactly in any order; the 13 bits that a group of eight keeps do as well."""
+    K = 128 * stages
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    codes = torch.tensor([0x00, 0x38, 0xB8, 0x40, 0xC0], dtype=torch.uint8, device="cuda")
+    values = torch.tensor([0.0, 1.0, -1.0, 2.0, -2.0], dtype=torch.float64, device="cuda")
+
+    def operand(outer):
+        at = torch.randint(0, 5, (outer, K), generator=g, device="cuda")
+        e = torch.randint(-1, 2, (outer, stages), generator=g, device="cuda")
+        scales = torch.zeros(outer, (stages + 15) // 16 * 16, dtype=torch.uint8, device="cuda")
+        scales[:, :stages] = (127 + e).to(torch.uint8)
+        factor = torch.where(e == 0, 1.0, torch.where(e > 0, 2.0, 0.5)).double()
+        return codes[at], scales, values[at] * factor.repeat_interleave(128, dim=1)
+
+    aq, as_, A = operand(M)
+    bq, bs, B = operand(N)
+    announce("fp8 gemm", M, N, K)
+    want = A @ B.t().contiguous()
+    assert torch.equal(_mx().fp8_gemm(aq, as_, bq, bs).double(), want)
+    # on what is there, rounded once
+    out = torch.ones(M, N, dtype=torch.bfloat16, device="cuda")
+    _mx().fp8_gemm(aq, as_, bq, bs, alpha=0.5, beta=3.0, out=out)
+    assert torch.equal(out, (0.5 * want + 3.0).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("T,V,stages", SHAPES)
+def test_head(T, V, stages):
+    announce("xent", T, 64 * stages, V)
+    _check(*_problem(T, 64 * stages, V))
+
+
+@pytest.mark.parametrize("batch,m,n", [(3, 16, 2048), (1, 2000, 3584), (1, 4608, 4096), (1, 4200, 6656), (1, 8192, 8192),
+                                       (5, 700, 1100)])
+def test_orthogonalize(batch, m, n):
+    g = torch.randn(batch, m, n, generator=torch.Generator(device="cuda").manual_seed(m + n), device="cuda").to(torch.bfloat16)
+    announce("orthogonalize", batch, m, n)
+    got = _mx().orthogonalize(g)
+    a, b, c = COEFFS
+    for k in range(batch):
+        x = g[k].double()
+        x = x / (x.norm() + 1e-7)
+        x = x.t().contiguous() if m > n else x
+        for _ in range(5):
+            A = x @ x.t().contiguous()
+            x = a * x + (b * A + c * (A @ A)) @ x
+        x = x.t() if m > n else x
+        assert float((got[k].double() - x).norm() / x.norm()) <= OWN + BF16
