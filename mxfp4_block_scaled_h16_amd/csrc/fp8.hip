@@ -11,7 +11,9 @@ namespace {
 // One workgroup quantizes a 128 x 128 tile of x, which holds whole blocks along both axes; 256 threads of
 // 8 x 8 values each (rows 8 (t / 16) .., columns 8 (t % 16) ..), in registers throughout. Row
 // maxima join the 16 lanes of a row, column maxima the 16 threads of a column through the LDS.
-// Bound by memory: a bf16 value is read once (2 bytes) and a code written per axis (1 byte each).
+// Bound by memory: a bf16 value is read once (2 bytes) and a code written per axis (1 byte each). 8192 x 4096 and
+// 6144 x 4096 along their rows in one launch: 45 us, 3.9 TB/s of the 4.97 that a copy reaches; 8192 x 14336 and 8192 x
+// 4096 along their columns: 118 us, 3.8 TB/s.
 struct Fp8Args {
     Fp8Input item[kFp8Group];
     int first[kFp8Group + 1];   // workgroups before each item

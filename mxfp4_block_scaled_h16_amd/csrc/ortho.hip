@@ -6,7 +6,8 @@
 // products run on the FP16 matrix cores with FP32 accumulation. FP16 holds 2^10 X, 2^10 A and
 // 2^10 (b A + c A A): every entry of X stays below 1.3 and of the others below 3 in magnitude
 // (singular values of X lie in [0, 1.3] at every step for the usual coefficients), so nothing
-// overflows (other coefficients are checked on the host to stay within FP16, t is held to 16), and entries down to 2^-24 keep all 11 bits. X itself is carried from step to step in two FP16
+// overflows (other coefficients are checked on the host to stay within FP16, t below is held to 16), and
+// entries down to 2^-24 keep all 11 bits. X itself is carried from step to step in two FP16
 // numbers, value and remainder (22 bits): the term a X, which carries the small singular values,
 // loses nothing, and what the 11-bit operands add stays below the rounding of a bf16 result
 // (with X in FP16 alone a matrix of a few strong directions was off by 0.011, with bf16 operands by 0.09).
@@ -18,11 +19,17 @@
 // t = -(b + c), the two before it a half and a quarter of it, and the others none. Relative error in five steps
 // (16 x 16 to 486 x 900, heavy tails): 0.0007 to 0.0016, without t 0.0014 to 0.0029; a few strong directions
 // over noise 1/1000 of them: 0.0016, without t 0.0004, with t = -(b + c) in every step 0.03. A bf16 result's own
-// rounding is 0.0017.
+// rounding is 0.0017. A's diagonal carried in FP32 beside it took 16 x 5000, the worst shape here, from 0.0022 to
+// 0.0018 and cost 1 to 4% of the time: not taken.
 //
 // Per step three launches: A (symmetric: the lower triangle of tiles, written twice), b A + c A A
 // (symmetric too), and the update, which writes X in both orientations for the next step's
 // products, each of which contracts along rows.
+//
+// Bound by the matrix cores: 4096 x 4096 in 1.44 to 1.52 ms, of which the updates 133 us each (1.03 PFLOP/s; they
+// write X three times) and the symmetric products 103 us, whose 136 tiles leave 120 CUs idle (in
+// 128 x 128 tiles, which fill them, they take longer). 14336 x 4096: 4.1 to 4.2 ms; an update 477 + 28 us for the
+// half round of its 896 tiles that is split. Small ones by their launches: 256 x 512 takes 79 us in 17, each 4 to 6 us.
 #include <algorithm>
 
 #include "slab_gemm.h"
@@ -208,7 +215,7 @@ __device__ __forceinline__ void read_g8(const void *g, int64_t at, float (&v)[8]
 }
 
 // Sums of squares, one per workgroup, in 64 bits (the squares of FP32 numbers leave FP32's range). Bound by
-// memory. vec: 16-byte aligned rows of whole eights.
+// memory: 14336 x 4096 in FP32 51 us, 4.6 TB/s. vec: 16-byte aligned rows of whole eights.
 template <bool F32>
 __global__ __launch_bounds__(256) void norm_kernel(const void *__restrict__ g, int64_t m, int64_t n, int64_t ldg, int64_t batch_g,
                                                    int vec, double *__restrict__ part)
@@ -244,7 +251,8 @@ __global__ __launch_bounds__(256) void norm_kernel(const void *__restrict__ g, i
 
 // X = G / (|G| + eps), times 2^10, in value and remainder and (the value) transposed, with zeros around it.
 // 128 x 128 tiles: a thread takes 8 x 8 values and transposes them in registers; 256-byte lines of
-// the transposed are put together in the LDS. Bound by memory: 4 (or 2) bytes in, 6 out.
+// the transposed are put together in the LDS. Bound by memory: 4 (or 2) bytes in, 6 out; 14336 x 4096 from FP32
+// 101 us (5.8 TB/s, some of it from the cache that the norm's read has filled).
 template <bool F32>
 __global__ __launch_bounds__(256) void first_kernel(const void *__restrict__ g, int64_t m, int64_t n, int64_t ldg, int64_t batch_g,
                                                     int vec, const double *__restrict__ part, int parts, float eps,

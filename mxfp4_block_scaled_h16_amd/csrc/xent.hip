@@ -9,6 +9,12 @@
 // orientations; dX = G W adds up over the pieces in FP32, dW = G^T X has its rows of the piece written
 // once. The second operands of these are FP16 copies of W's piece and of X, transposed, so that every
 // product contracts along rows.
+//
+// Bound by the matrix cores, under the card's power cap: at T 8192, K 4096, V 128256 27 ms, of which the loss' product
+// 6.5 (1.32 PFLOP/s; the library's plain product, which stores its logits, 5.9), and in each of eight pieces G's 0.91,
+// dX's 0.87 and dW's 0.79 (1.19, 1.25 and 1.37 PFLOP/s). At T 2048, K 2048, V 50257 the loss takes 360 us, the
+// library's product alone 391. What is not products: 3% at the large size (copies 50 us a piece, ranges 0.2 ms), at T 1537,
+// K 1024 a tenth of 0.87 ms; at T 128, K 512, V 1000 a call is bound by its 7 launches and the host.
 #include <algorithm>
 
 #include "mx_device.h"
@@ -97,7 +103,8 @@ struct StatsEpi {
     }
 };
 
-// Joins the column tiles of 32 rows: 8 threads per row, each every eighth tile.
+// Joins the column tiles of 32 rows: 8 threads per row, each every eighth tile. Few bytes (8 a row and tile), read
+// with a wait after each step: 10 us at 2048 rows of 197 tiles, 31 at 8192 of 501.
 __global__ __launch_bounds__(256) void xent_join_kernel(const float2 *__restrict__ part, int tiles, int T, int64_t V,
                                                         const float *__restrict__ zt, const int64_t *__restrict__ target,
                                                         int64_t ignore_index, float *__restrict__ loss,
@@ -227,7 +234,7 @@ __device__ __forceinline__ float block_max(float v)
 }
 
 // Largest |value| of a bf16 matrix over this workgroup's share of it; a NaN or infinity counts as infinity.
-// Bound by memory, 2 bytes a value. vec: 16-byte aligned rows of whole 16 bytes.
+// Bound by memory, 2 bytes a value: 8192 x 4096 and 128256 x 4096 in 202 us, 5.5 TB/s. vec: 16-byte aligned rows of whole 16 bytes.
 __device__ __forceinline__ float share_max(const uint16_t *p, int64_t ld, int64_t rows, int64_t cols, bool vec,
                                            const RowWeights &weights)
 {
@@ -317,7 +324,8 @@ struct Turn {
     int tiles;
 };
 // One or two of them, X's and that of a piece of W. 128 x 128 tiles: a thread transposes 8 x 8 values in
-// registers, then 256-byte lines are put together in the LDS. Bound by memory: 2 bytes in, 2 out.
+// registers, then 256-byte lines are put together in the LDS. Bound by memory: 2 bytes in, 2 out; a piece of 16128 x
+// 4096 in 50 us, 5.3 TB/s.
 // blocks > 0: the ranges are joined here.
 __global__ __launch_bounds__(256) void turn_kernel(Turn tx, Turn tw, RowWeights weights, const float *part, int blocks,
                                                    Ranges *ranges)
