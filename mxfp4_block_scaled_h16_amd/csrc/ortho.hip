@@ -266,7 +266,10 @@ __global__ __launch_bounds__(256) void first_kernel(const void *__restrict__ g, 
     for (int k = 32; k >= 1; k >>= 1) sum += __shfl_xor(sum, k);
     if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = sum;
     __syncthreads();
-    const float inv = (float)(1024.0 / (sqrt((slots[0] + slots[1]) + (slots[2] + slots[3])) + (double)eps));
+    // the factor may lie outside FP32's range where G's entries do not: a power of two apart from it
+    const double norm = sqrt((slots[0] + slots[1]) + (slots[2] + slots[3])) + (double)eps;
+    const int power = norm > 0.0 && norm <= 1e300 ? ilogb(norm) : 0;
+    const float inv = (float)(1024.0 / ldexp(norm, -power));
 
     const int64_t r0 = (int64_t)blockIdx.x * 128, c0 = (int64_t)blockIdx.y * 128;
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
@@ -285,7 +288,7 @@ __global__ __launch_bounds__(256) void first_kernel(const void *__restrict__ g, 
         u32x4 value, rest;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float a = v[2 * e] * inv, b = v[2 * e + 1] * inv;
+            const float a = ldexpf(v[2 * e], -power) * inv, b = ldexpf(v[2 * e + 1], -power) * inv;
             h[i][2 * e] = f16_bits(a);
             h[i][2 * e + 1] = f16_bits(b);
             value[e] = (uint32_t)h[i][2 * e] | (uint32_t)h[i][2 * e + 1] << 16;

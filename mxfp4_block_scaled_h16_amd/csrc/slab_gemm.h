@@ -621,7 +621,7 @@ struct StoreEpi {
         constexpr int kElem = BF16_OUT ? 2 : 4;
         const bool vec = ldc % 8 == 0 && (uintptr_t)c % 16 == 0 && (batch_c % 8 == 0 || w.batch == 0);
         // the whole tile in 16-byte stores of nothing but the product
-        const bool plain = vec && beta == 0.0f && !add && w.m0 + G::kTileM <= op.M && w.n0 + G::kTileN <= op.N;
+        const bool plain = vec && beta == 0.0f && !add && G::kTileM <= op.M - w.m0 && G::kTileN <= op.N - w.n0;
         const int line = w.lane / B::kLanes, c8 = w.lane % B::kLanes, n = w.n0 + w.col0 + 8 * c8;
 #pragma unroll 1
         for (int blk = w.block0; blk < w.block1; ++blk) {
@@ -861,8 +861,8 @@ inline Plan unsplit(Plan p, int64_t nk)
 template <class E, class G, class Epi>
 hipError_t launch_planned(Operands op, const Epi &epi, const Plan &plan, void *partials, hipStream_t stream)
 {
-    op.tiles_m = (op.M + G::kTileM - 1) / G::kTileM;
-    op.tiles_n = (op.N + G::kTileN - 1) / G::kTileN;
+    op.tiles_m = (op.M - 1) / G::kTileM + 1;   // M + 255 may leave 32 bits
+    op.tiles_n = (op.N - 1) / G::kTileN + 1;
     if (plan.whole < 0) return hipErrorInvalidValue;
     op.whole = plan.whole;
     op.splits = plan.splits;

@@ -73,3 +73,15 @@ def test_orthogonalize(batch, m, n):
             x = a * x + (b * A + c * (A @ A)) @ x
         x = x.t() if m > n else x
         assert float((got[k].double() - x).norm() / x.norm()) <= OWN + BF16
+
+
+def test_orthogonalize_at_the_ends_of_fp32():
+    """Entries near FP32's largest and its smallest normal numbers: powers of two do not change the result."""
+    g = torch.randn(40, 50, generator=torch.Generator().manual_seed(1)).clamp(-3, 3).cuda()
+    g[g.abs() < 2.0 ** -10] = 0.25
+    want = _mx().orthogonalize(g, eps=0.0)
+    assert bool(torch.isfinite(want).all())
+    # 24 bits below 2^-10 are still above the smallest subnormal, 2^-149; 3 * 2^126 is below the largest
+    for k in (-115, 100, 126):
+        announce("orthogonalize, scale 2^", k)
+        assert torch.equal(_mx().orthogonalize(torch.ldexp(g.cpu(), torch.tensor(k)).cuda(), eps=0.0), want)
