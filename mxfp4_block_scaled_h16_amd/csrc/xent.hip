@@ -302,13 +302,20 @@ __global__ __launch_bounds__(256) void range_kernel(const uint16_t *x, int64_t l
 // leaves them for those that follow.
 __device__ __forceinline__ Ranges join_ranges(const float *part, int blocks)
 {
-    float s[3];
-#pragma unroll 1
+    __shared__ float slots[3][4];
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    for (int i = threadIdx.x; i < blocks; i += 256)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) s[k] = fmaxf(s[k], part[k * kRangeBlocks + i]);
+#pragma unroll
     for (int k = 0; k < 3; ++k) {
-        float top = 0.0f;
-        for (int i = threadIdx.x; i < blocks; i += 256) top = fmaxf(top, part[k * kRangeBlocks + i]);
-        s[k] = range_scale(block_max(top));
+        for (int d = 32; d >= 1; d >>= 1) s[k] = fmaxf(s[k], __shfl_xor(s[k], d));
+        if ((threadIdx.x & 63) == 0) slots[k][threadIdx.x >> 6] = s[k];
     }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        s[k] = range_scale(fmaxf(fmaxf(slots[k][0], slots[k][1]), fmaxf(slots[k][2], slots[k][3])));
     return Ranges{s[0], s[1], s[2], {1.0f / s[0], 1.0f / s[2]}, {1.0f / s[0], 1.0f / s[1]}};
 }
 
@@ -331,13 +338,6 @@ __global__ __launch_bounds__(256) void turn_kernel(Turn tx, Turn tw, RowWeights 
                                                    Ranges *ranges)
 {
     __shared__ __attribute__((aligned(16))) uint16_t tile[128 * 128];   // [column][row], 16-byte pieces permuted
-    Ranges now;
-    if (blocks > 0) {
-        now = join_ranges(part, blocks);
-        if (blockIdx.x == 0 && threadIdx.x == 0) *ranges = now;
-    } else {
-        now = *ranges;
-    }
     const bool is_w = (int)blockIdx.x >= tx.tiles;
     const Turn &t = is_w ? tw : tx;
     const int index = (int)blockIdx.x - (is_w ? tx.tiles : 0);
@@ -348,7 +348,6 @@ __global__ __launch_bounds__(256) void turn_kernel(Turn tx, Turn tw, RowWeights 
     if (is_w) weights.target = nullptr;   // every row of W counts
     const int64_t r0 = (int64_t)(index / t.across) * 128, c0 = (int64_t)(index % t.across) * 128;
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
-    const float s = is_w ? now.w : now.x;
     u32x4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -365,6 +364,15 @@ __global__ __launch_bounds__(256) void turn_kernel(Turn tx, Turn tw, RowWeights 
             }
         }
     }
+    // behind the loads, whose wait it shares
+    Ranges now;
+    if (blocks > 0) {
+        now = join_ranges(part, blocks);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *ranges = now;
+    } else {
+        now = *ranges;
+    }
+    const float s = is_w ? now.w : now.x;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         u32x4 o;
