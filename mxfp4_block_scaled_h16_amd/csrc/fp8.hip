@@ -12,8 +12,8 @@ namespace {
 // 8 x 8 values each (rows 8 (t / 16) .., columns 8 (t % 16) ..), in registers throughout. Row
 // maxima join the 16 lanes of a row, column maxima the 16 threads of a column through the LDS.
 // Bound by memory: a bf16 value is read once (2 bytes) and a code written per axis (1 byte each). 8192 x 4096 and
-// 6144 x 4096 along their rows in one launch: 45 us, 3.9 TB/s of the 4.97 that a copy reaches; 8192 x 14336 and 8192 x
-// 4096 along their columns: 118 us, 3.8 TB/s.
+// 6144 x 4096 along their rows in one launch: 42 us, 4.2 TB/s of the 4.97 that a copy reaches; 8192 x 14336 and 8192 x
+// 4096 along their columns: 101 us, 4.5 TB/s.
 struct Fp8Args {
     Fp8Input item[kFp8Group];
     int first[kFp8Group + 1];   // workgroups before each item
@@ -103,9 +103,11 @@ __device__ __forceinline__ void load8(const Fp8Input &it, int64_t row, int64_t c
 }
 
 // F32: the tensors' type. RAGGED: some row's length is no multiple of eight (its end is then read value by
-// value, in code that the others need not fetch).
+// value, in code that the others need not fetch). Four workgroups a CU (128 registers) instead of three, where that
+// spills nothing: 8192 x (14336 + 4096) along the columns 118 -> 101 us; with five, or in the ragged ones, it spills
+// (1111 x 2001 and 2001 x 1000: 12 -> 18 us).
 template <bool F32, bool RAGGED>
-__global__ __launch_bounds__(256) void fp8_quantize_kernel(Fp8Args args)
+__global__ __launch_bounds__(256, RAGGED ? 2 : 4) void fp8_quantize_kernel(Fp8Args args)
 {
     __shared__ uint32_t cmax[16][128 + 4];
     __shared__ uint32_t wmax[4];
