@@ -146,7 +146,8 @@ mxfp4_status_t mxfp4_linear_xent_backward(const float *dloss, const float *dlse,
  * (the Gram matrix along the shorter side). g: bf16 or FP32, row stride ldg, matrices batch_stride_g
  * elements apart; out: FP32 or bf16 with ldo and batch_stride_o; out may be read only when beta != 0
  * and must not overlap g. The products take FP16 operands and accumulate in FP32; X is carried in 22
- * bits. A matrix that holds a NaN or an infinity gives NaN (that matrix only).
+ * bits; five steps are off by 0.0006 to 0.0016 of the result's norm before its rounding (0.0022 with one side of 16
+ * to 20). A matrix that holds a NaN or an infinity gives NaN (that matrix only).
  * Coefficients: finite, and such that singular values that start in [0, 1] stay within 4 and |b x + c x x|
  * within 32 for their squares x at every step (MXFP4_ERR_ARG otherwise: FP16 would overflow);
  * (3.4445, -4.7750, 2.0315) with 5 steps stay within 1.3 and 2.9.

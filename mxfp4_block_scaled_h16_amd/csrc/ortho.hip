@@ -64,7 +64,8 @@ struct GramEpi {
     uint16_t *out;
     int64_t ld, batch_out;
     template <class G>
-    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds, uint8_t *) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds,
+                                        uint8_t *) const
     {
         uint16_t *o = out + w.batch * batch_out;
         store_tile16<G>(acc, w, lds, [](float a, float b) { return pack_f16(a, b); }, [](int, int) { return 0; },
@@ -84,7 +85,8 @@ struct PolyEpi {
     int64_t ld, batch_out;
     float b, c, t;
     template <class G>
-    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds, uint8_t *) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds,
+                                        uint8_t *) const
     {
         const uint16_t *in = gram + w.batch * batch_out;
         uint16_t *o = out + w.batch * batch_out;
@@ -132,7 +134,8 @@ struct UpdateEpi {
     int64_t ld, ld_turned, batch_x;
     float a;
     template <class G>
-    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds, uint8_t *) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &, uint8_t *lds,
+                                        uint8_t *) const
     {
         const int64_t base = w.batch * batch_x;
         store_tile16<G>(acc, w, lds, [](float x, float y) { return pack_f16(x, y); },
@@ -165,7 +168,8 @@ struct LastEpi {
     float a;
     StoreEpi<BF16_OUT> store;   // alpha covers X's 2^10
     template <class G>
-    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds, [[maybe_unused]] uint8_t *info_at) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds,
+                                        uint8_t *) const
     {
         const int64_t base = w.batch * batch_x;
         store.template run_with<G>(acc, w, op, lds, [&](int m, int n) { return two_part(hi, lo, base + (int64_t)m * ld + n); },

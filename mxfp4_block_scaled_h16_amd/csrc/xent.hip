@@ -42,7 +42,8 @@ struct StatsEpi {
     const int64_t *target;
 
     template <class G>
-    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds, [[maybe_unused]] uint8_t *info_at) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds,
+                                        uint8_t *) const
     {
         const int r = w.lane & 15, q = w.lane >> 4;
         float2 *slots = reinterpret_cast<float2 *>(lds);   // [wave column][row of the tile]
@@ -183,7 +184,8 @@ struct GradEpi {
     int64_t ldg, ldt;
 
     template <class G>
-    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds, [[maybe_unused]] uint8_t *info_at) const
+    __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds,
+                                        uint8_t *info_at) const
     {
         // of each row of the tile: scaled dl and dp, lse in base 2, and the target's column in the piece (-1: no
         // column of it, or a row without a gradient of its loss)
@@ -234,7 +236,8 @@ __device__ __forceinline__ float block_max(float v)
 }
 
 // Largest |value| of a bf16 matrix over this workgroup's share of it; a NaN or infinity counts as infinity.
-// Bound by memory, 2 bytes a value: 8192 x 4096 and 128256 x 4096 in 202 us, 5.5 TB/s. vec: 16-byte aligned rows of whole 16 bytes.
+// Bound by memory, 2 bytes a value: 8192 x 4096 and 128256 x 4096 in 202 us, 5.5 TB/s. vec: 16-byte aligned rows of whole
+// 16 bytes.
 __device__ __forceinline__ float share_max(const uint16_t *p, int64_t ld, int64_t rows, int64_t cols, bool vec,
                                            const RowWeights &weights)
 {
