@@ -32,7 +32,7 @@ __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_ex
 
 // ------------------------------------------------------------------------ the loss' product ---
 // Per row of the tile: the largest z and the sum of exp(z - largest) over the tile's columns
-// (statistics in base 2, times log2 e), and the target's z where the tile holds it. A lane holds 16
+// and the target's z where the tile holds it. A lane holds 16
 // columns of a row per 16-row tile, the lanes 16, 32 and 48 further the others of the wavefront's 64;
 // the wavefronts of a row join through the LDS.
 struct StatsEpi {
@@ -70,7 +70,7 @@ struct StatsEpi {
                         hit = z;
                         found = true;
                     }
-                    z = c < nleft ? z * kLog2e : -INFINITY;
+                    z = c < nleft ? z : -INFINITY;
                     acc[i][j][t] = z;
                     top = fmaxf(top, z);
                 }
@@ -82,7 +82,7 @@ struct StatsEpi {
 #pragma unroll
             for (int j = 0; j < G::FJ; ++j)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) sum += fast_exp2(acc[i][j][t] - ref);
+                for (int t = 0; t < 4; ++t) sum += fast_exp2((acc[i][j][t] - ref) * kLog2e);
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
             if (q == 0) slots[wn * G::kTileM + row] = make_float2(top, sum);
@@ -96,7 +96,7 @@ struct StatsEpi {
             for (int k = 1; k < G::kWavesN; ++k) {
                 const float2 o = slots[k * G::kTileM + row];
                 const float top = fmaxf(s.x, o.x), ref = top == -INFINITY ? 0.0f : top;
-                s = make_float2(top, s.y * fast_exp2(s.x - ref) + o.y * fast_exp2(o.x - ref));
+                s = make_float2(top, s.y * fast_exp2((s.x - ref) * kLog2e) + o.y * fast_exp2((o.x - ref) * kLog2e));
             }
             const int m = w.m0 + row;
             if (m < op.M) part[(int64_t)(w.n0 / G::kTileN) * op.M + m] = s;
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const float2 *__restrict
     const int t = blockIdx.x * 32 + lr;
     auto join = [](float2 s, float2 o) {
         const float top = fmaxf(s.x, o.x), ref = top == -INFINITY ? 0.0f : top;
-        return make_float2(top, s.y * fast_exp2(s.x - ref) + o.y * fast_exp2(o.x - ref));
+        return make_float2(top, s.y * fast_exp2((s.x - ref) * kLog2e) + o.y * fast_exp2((o.x - ref) * kLog2e));
     };
     float2 s = make_float2(-INFINITY, 0.0f);
     if (t < T)
@@ -125,11 +125,12 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const float2 *__restrict
     __syncthreads();
     if (slice != 0 || t >= T) return;
     for (int k = 1; k < 8; ++k) s = join(s, slots[k][lr]);
-    const float l = (s.x + log2f(s.y)) * kLn2;
-    lse[t] = l;
+    // the loss not from lse: a confident row's is small beside it
+    const float rest = log2f(s.y) * kLn2;
+    lse[t] = s.x + rest;
     const int64_t tg = target[t];
     float v = 0.0f;
-    if (tg != ignore_index) v = tg >= 0 && tg < V ? l - zt[t] : NAN;
+    if (tg != ignore_index) v = tg >= 0 && tg < V ? s.x - zt[t] + rest : NAN;
     loss[t] = v;
 }
 

@@ -85,3 +85,28 @@ def test_orthogonalize_at_the_ends_of_fp32():
     for k in (-115, 100, 126):
         announce("orthogonalize, scale 2^", k)
         assert torch.equal(_mx().orthogonalize(torch.ldexp(g.cpu(), torch.tensor(k)).cuda(), eps=0.0), want)
+
+
+def test_small_losses_beside_large_logits():
+    """A row whose target is far ahead: its loss is log(1 + (V - 1) exp(z - z_target)), however large the logits are that
+    cancel in it. One product a logit, all exact: the loss is off by its own operations' roundings (an exponent of
+    some 12, an exponential of 2^-22, a sum of 1 and little, a logarithm) alone, 2^-19 at most, where lse's rounding is 2^-17."""
+    V, K = 600, 64
+    x, w = torch.zeros(40, K), torch.zeros(V, K)
+    target = torch.arange(40) * 13 % V
+    gap = torch.arange(40) * 0.25 + 6.0
+    big = 128.0
+    x[:, 0], w[:, 0] = 1.0, big                      # z = 128 everywhere
+    for t in range(40):                              # and 128 + gap at the target
+        x[t, 1 + t % 60] = 1.0
+    x[:, 0] = 1.0
+    for t in range(40):
+        w[target[t], 1 + t % 60] = gap[t]
+    loss, lse = _mx().linear_xent_forward(x.to(torch.bfloat16).cuda(), w.to(torch.bfloat16).cuda(), target.cuda())
+    want = torch.log1p((V - 1) * torch.exp(-gap.double()))
+    # 1 + s is added up in FP32, in an order of the kernel's: each addition to what holds the 1 already may be off by
+    # 2^-24, and there are at most 16 in a lane, 2 across lanes, 3 across wavefronts, 10 across tiles: below 32 * 2^-24;
+    # s is held to 16 * 2^-23 of itself, the logarithm to 2^-22 and its own 2^-23
+    tol = 2.0 ** -22 + 2.0 ** -19 + want * 2.0 ** -18
+    assert bool(((loss.cpu().double() - want).abs() <= tol).all())
+    assert bool(((lse.cpu().double() - (big + gap.double() + want)).abs() <= tol + 2.0 ** -16).all())
