@@ -590,7 +590,7 @@ private:
 
 // c = alpha * A B^T + beta * c (+ add) in FP32 or bf16 (rounded once, after the sums); c is read only when
 // beta != 0, add (FP32 [M][ld_add], 16-byte aligned rows, readable up to a multiple of 4 columns) only
-// when it is not NULL. factors: NULL, or two powers of two in device memory that alpha is multiplied by.
+// when it is not NULL. power: NULL, or an exponent in device memory: alpha 2^power takes the place of alpha.
 template <bool BF16_OUT>
 struct StoreEpi {
     static constexpr bool kSym = false;
@@ -599,7 +599,7 @@ struct StoreEpi {
     float alpha, beta;
     const float *add = nullptr;
     int64_t ld_add = 0;
-    const float *factors = nullptr;
+    const int *power = nullptr;
 
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds,
@@ -616,8 +616,13 @@ struct StoreEpi {
     {
         using B = Block32<G>;
         uint8_t *block = lds + w.wave * G::kEpiWave;
-        // one after the other: their product may leave FP32's range where the result does not
-        const float f0 = factors ? alpha * factors[0] : alpha, f1 = factors ? factors[1] : 1.0f;
+        // an exponent of its own: 2^power may leave FP32's range where the result does not
+        const int up = power ? *power : 0;
+        const auto scaled = [&](f32x4 x) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = ldexpf(x[e] * alpha, up);
+            return x;
+        };
         constexpr int kElem = BF16_OUT ? 2 : 4;
         const bool vec = ldc % 8 == 0 && (uintptr_t)c % 16 == 0 && (batch_c % 8 == 0 || w.batch == 0);
         // the whole tile in 16-byte stores of nothing but the product
@@ -639,8 +644,8 @@ struct StoreEpi {
                     f32x4 v[2];
                     B::get(block, B::kLinesPerPass * p + line, c8, v);
                     make(v, got[p]);
-                    v[0] = v[0] * f0 * f1;
-                    v[1] = v[1] * f0 * f1;
+                    v[0] = scaled(v[0]);
+                    v[1] = scaled(v[1]);
                     if constexpr (BF16_OUT) {
                         *reinterpret_cast<u32x4 *>(at) = u32x4{pack_bf16(v[0][0], v[0][1]), pack_bf16(v[0][2], v[0][3]),
                                                                pack_bf16(v[1][0], v[1][1]), pack_bf16(v[1][2], v[1][3])};
@@ -663,7 +668,7 @@ struct StoreEpi {
                     for (int h = 0; h < 2; ++h) {
                         const int nn = n + 4 * h;
                         if (nn >= op.N) break;
-                        f32x4 x = v[h] * f0 * f1;
+                        f32x4 x = scaled(v[h]);
                         if (add) x += *reinterpret_cast<const f32x4 *>(add + (int64_t)mm * ld_add + nn);
                         put(w.batch * batch_c + (int64_t)mm * ldc + nn, x, vec && nn + 4 <= op.N, op.N - nn);
                     }

@@ -135,20 +135,17 @@ __global__ __launch_bounds__(256) void xent_join_kernel(const float2 *__restrict
 }
 
 // -------------------------------------------------------------------- the gradient's product --
-// How far the FP16 operands of the gradients' products are scaled: powers of two that bring the
-// largest |G|, |X| and |W| to [2^14, 2^15), and their reciprocals.
+// How far the FP16 operands of the gradients' products are scaled: the exponents of powers of two that bring the
+// largest |G|, |X| and |W| to [2^14, 2^15), and what undoes them in dX and dW.
 struct Ranges {
-    float g, x, w;
-    float inv_gw[2], inv_gx[2];   // 1 / g, 1 / w and 1 / g, 1 / x
+    int g, x, w;
+    int up_gw, up_gx;   // -(g + w) and -(g + x)
 };
 
-// 2^k with 2^14 <= 2^k top < 2^15, k within [-120, 120]; 1 for zero and for what is not finite
-__device__ __forceinline__ float range_scale(float top)
+// k with 2^14 <= 2^k top < 2^15; 0 for zero and for what is not finite
+__device__ __forceinline__ int range_shift(float top)
 {
-    const uint32_t bits = __float_as_uint(top);
-    if (bits == 0u || bits >= 0x7F800000u) return 1.0f;
-    const int k = 14 - ((int)(bits >> 23) - 127);   // a subnormal top counts as 2^-127
-    return __uint_as_float((uint32_t)(127 + max(-120, min(120, k))) << 23);
+    return top > 0.0f && top < INFINITY ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
 }
 
 // Which rows of X add something to the gradients: the others are taken as zeros in the transposed
@@ -191,7 +188,7 @@ struct GradEpi {
         // of each row of the tile: scaled dl and dp, lse in base 2, and the target's column in the piece (-1: no
         // column of it, or a row without a gradient of its loss)
         f32x4 *info = reinterpret_cast<f32x4 *>(info_at);
-        const float scale = ranges->g;
+        const int up = ranges->g;
         for (int row = threadIdx.x; row < G::kTileM; row += 64 * G::NW) {
             const int m = w.m0 + row;
             f32x4 v = {0.0f, 0.0f, 0.0f, __int_as_float(-1)};
@@ -199,7 +196,7 @@ struct GradEpi {
                 float dl, dp;
                 weights.of(m, dl, dp);
                 const int64_t at = weights.target[m] - v0;
-                v = f32x4{dl * scale, dp * scale, lse[m] * kLog2e,
+                v = f32x4{ldexpf(dl, up), ldexpf(dp, up), lse[m] * kLog2e,
                           __int_as_float(dl != 0.0f && at >= 0 && at < op.N ? (int)at : -1)};
             }
             info[row] = v;
@@ -317,10 +314,11 @@ __device__ __forceinline__ Ranges join_ranges(const float *part, int blocks)
         if ((threadIdx.x & 63) == 0) slots[k][threadIdx.x >> 6] = s[k];
     }
     __syncthreads();
+    int e[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-        s[k] = range_scale(fmaxf(fmaxf(slots[k][0], slots[k][1]), fmaxf(slots[k][2], slots[k][3])));
-    return Ranges{s[0], s[1], s[2], {1.0f / s[0], 1.0f / s[2]}, {1.0f / s[0], 1.0f / s[1]}};
+        e[k] = range_shift(fmaxf(fmaxf(slots[k][0], slots[k][1]), fmaxf(slots[k][2], slots[k][3])));
+    return Ranges{e[0], e[1], e[2], -(e[0] + e[2]), -(e[0] + e[1])};
 }
 
 // ------------------------------------------------------------------------------- copies -------
@@ -376,14 +374,15 @@ __global__ __launch_bounds__(256) void turn_kernel(Turn tx, Turn tw, RowWeights 
     } else {
         now = *ranges;
     }
-    const float s = is_w ? now.w : now.x;
+    const int up = is_w ? now.w : now.x;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         u32x4 o;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const uint32_t a = v[2 * k][e / 2], b = v[2 * k + 1][e / 2];
-            o[k] = e & 1 ? pack_f16(bf16_hi(a) * s, bf16_hi(b) * s) : pack_f16(bf16_lo(a) * s, bf16_lo(b) * s);
+            o[k] = e & 1 ? pack_f16(ldexpf(bf16_hi(a), up), ldexpf(bf16_hi(b), up))
+                         : pack_f16(ldexpf(bf16_lo(a), up), ldexpf(bf16_lo(b), up));
         }
         const int c = 8 * cg + e;
         *reinterpret_cast<u32x4 *>(tile + c * 128 + 8 * (rg ^ (cg & 15))) = o;
@@ -614,11 +613,11 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             const float *add = first ? nullptr : l.dx;
             hipError_t e;
             if (!last)
-                e = run(StoreEpi<false>{l.dx, ld_acc, 0, 1.0f, 0.0f, add, ld_acc, l.ranges->inv_gw});
+                e = run(StoreEpi<false>{l.dx, ld_acc, 0, 1.0f, 0.0f, add, ld_acc, &l.ranges->up_gw});
             else if (dx_bf16)
-                e = run(StoreEpi<true>{dx, p.K, 0, 1.0f, 0.0f, add, ld_acc, l.ranges->inv_gw});
+                e = run(StoreEpi<true>{dx, p.K, 0, 1.0f, 0.0f, add, ld_acc, &l.ranges->up_gw});
             else
-                e = run(StoreEpi<false>{dx, p.K, 0, 1.0f, 0.0f, add, ld_acc, l.ranges->inv_gw});
+                e = run(StoreEpi<false>{dx, p.K, 0, 1.0f, 0.0f, add, ld_acc, &l.ranges->up_gw});
             if (e) return e;
         }
         if (dw) {
@@ -632,8 +631,8 @@ hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const 
             q.nk = (int)(rows_done / 64);
             auto run = [&](const auto &e) { return launch_product<F16>(q, e, plans.dw, l.partials, stream); };
             const hipError_t e =
-                dw_bf16 ? run(StoreEpi<true>{static_cast<uint16_t *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, l.ranges->inv_gx})
-                        : run(StoreEpi<false>{static_cast<float *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, l.ranges->inv_gx});
+                dw_bf16 ? run(StoreEpi<true>{static_cast<uint16_t *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, &l.ranges->up_gx})
+                        : run(StoreEpi<false>{static_cast<float *>(dw) + v0 * p.K, p.K, 0, 1.0f, 0.0f, nullptr, 0, &l.ranges->up_gx});
             if (e) return e;
         }
     }
