@@ -1,4 +1,4 @@
-"""The head's gradients at the ends of FP32's range."""
+"""The head's gradients at the ends of FP32's range, and beside infinities in a row's gradient and in W."""
 import pytest
 import torch
 
@@ -8,6 +8,7 @@ from tests.test_gpu_xent import _problem, _tol
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
+INF, NAN = float("inf"), float("nan")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -51,3 +52,66 @@ def test_row_gradients_at_the_ends_of_fp32(power, ex, ew):
                            (dw, rdw, 1.01 * (off.t() @ x.double().abs()) + g.abs().sum(0)[:, None] * 2.0 ** -39 * float(x.abs().max()))):
         held = want.abs() < 2.0 ** 127
         assert bool(((got.double() - want).abs() <= tol + half * want.abs() + tiny)[held].all())
+
+
+@pytest.mark.parametrize("bad", [dict(dloss=INF), dict(dloss=-INF), dict(dloss=NAN), dict(dlse=INF), dict(dlse=NAN),
+                                 dict(dloss=INF, dlse=-INF), dict(dlse=3e38, dloss=3e38)])
+@pytest.mark.parametrize("T,K,V", [(40, 64, 5000), (300, 96, 700)])
+def test_an_infinite_row_gradient_leaves_the_other_rows(bad, T, K, V):
+    """dX of the other rows is, bit for bit, what it is when the bad row has no gradient: the range that G is scaled to
+    counts finite rows only. (Unscaled, G's entries of 1/8192 * 1e-4 would be nothing in FP16.)"""
+    x, w, target, _, _ = _problem(T, K, V)
+    dloss, dlse = torch.full((T,), 1.0 / 8192), torch.zeros(T)
+    row = int((target != -100).nonzero()[T // 3, 0])
+    dloss[row] = dlse[row] = 0.0
+    announce("xent infinite row", bad, T, K, V)
+    want, _ = _gradients(x, w, target, dloss, dlse)
+    dloss[row], dlse[row] = bad.get("dloss", 0.0), bad.get("dlse", 0.0)
+    dx, dw = _gradients(x, w, target, dloss, dlse)
+    others = torch.arange(T) != row
+    assert torch.equal(dx[others], want[others])
+    assert not torch.isfinite(dx[row]).any() and not torch.isfinite(dw).any()
+
+
+def test_the_largest_finite_row_gradients():
+    """|dloss| + |dloss + dlse| beyond FP32's range where neither is: G is still scaled, and the result finite."""
+    x, w, target, _, _ = _problem(20, 64, 300)
+    target = target.clamp(min=0)
+    top = 2.0 ** 127
+    dloss, dlse = torch.full((20,), top), torch.zeros(20)
+    x = (x.float() * 2.0 ** -40).to(BF)                   # every p is 1 / 300 to 2^-30
+    announce("xent largest rows")
+    dx, dw = _gradients(x, w, target, dloss, dlse)
+    _, _, rdx, rdw, g, _ = ref.xent(x, w, target, -100, dloss, dlse)
+    # G to half a step of FP16 and 2^-39 of the largest 2 top, p to 2^-20; FP32 sums of at most 300 terms
+    off = (2.0 ** -11 + 2.0 ** -20) * g.abs() + 2.0 ** -38 * top
+    assert bool(((dx.double() - rdx).abs() <= 1.01 * (off @ w.double().abs())).all())
+    assert bool(((dw.double() - rdw).abs() <= 1.01 * (off.t() @ x.double().abs())).all())
+
+
+@pytest.mark.parametrize("power", [-30, 0, 20, 40])
+def test_a_mask_of_minus_infinity_in_w(power):
+    """W[v][0] = -inf with X[t][0] = 1 masks word v out. The formula gives NaN in dX's column 0 (0 * inf) and the cut
+    vocabulary's gradients everywhere else, at any magnitude of W's other entries: FP16 would take those below 2^-24 for
+    nothing and those above 65504 for infinities, were they not scaled."""
+    T, K, V, kept = 30, 64, 300, 100
+    x, w, target, dloss, dlse = _problem(T, K, V, seed=power)
+    target = torch.where(target >= 0, target % kept, target)
+    x, w = (x.float() * 2.0 ** -power).to(BF), (w.float() * 2.0 ** power).to(BF)
+    x[:, 0], w[:, 0] = 1.0, 0.0
+    w[kept:, 0] = -INF
+    announce("xent mask in w", power)
+    dx, dw = _gradients(x, w, target, dloss, dlse)
+    cut = w[:kept]
+    rl, rlse, rdx, rdw, g, soft = ref.xent(x, cut, target, -100, dloss, dlse)
+    t = _tol(K, float((x.double().norm(dim=1)[:, None] * cut.double().norm(dim=1)[None]).amax()))
+    t += 2.0 ** -21 * (1.0 + float(rlse.abs().max()))
+    g_top = float((dloss.abs() * 2 + dlse.abs()).max())
+    off = 2.0 ** -11 * g.abs() + 2.5 * t * soft + 2.0 ** -39 * g_top
+    half = 2.0 ** -24
+    x_top, w_top = float(x.abs().max()), float(w[torch.isfinite(w)].abs().max())
+    tol = (off @ cut.double().abs()) * 1.01 + g.abs().sum(1, True) * 2.0 ** -39 * w_top + half * rdx.abs()
+    # the masked words' G is exactly 0, and 0 times their finite entries nothing
+    assert torch.isnan(dx[:, 0]).all() and bool(((dx.double() - rdx).abs() <= tol)[:, 1:].all())
+    tol = (off.t() @ x.double().abs()) * 1.01 + g.abs().sum(0)[:, None] * 2.0 ** -39 * x_top + half * rdw.abs()
+    assert bool(((dw[:kept].double() - rdw).abs() <= tol).all()) and not dw[kept:].any()
