@@ -120,7 +120,8 @@ mxfp4_status_t mxfp4_fp8_linear_wgrad(const void *dy_bf16, const void *x_bf16, i
  * counts with dloss_t = 0. A row with dloss_t = dlse_t = 0 adds nothing, whatever it holds (NaN in X
  * included). lse is the forward call's. The products of the gradients take FP16 operands, G, X and W each
  * scaled by a power of two to FP16's range: an entry of G is rounded to half a step of FP16 (2^-11 of
- * itself), and entries of G, X and W below 2^-28 of the largest finite one (of |dloss| + |dloss + dlse|
+ * itself) after the exponential has taken over the roundings of z and of lse (an error d of z - lse is one
+ * of d |dloss + dlse| p, at the target too, where p - 1 may be small beside it), and entries of G, X and W below 2^-28 of the largest finite one (of |dloss| + |dloss + dlse|
  * for G) to 2^-39 of that. A NaN or an infinity in one row's gradient or in W has the products it has in
  * the formula, and no say in those scales. dx [T][K] and dw [V][K], dense, FP32 or bf16; either
  * may be NULL, and is then not computed.

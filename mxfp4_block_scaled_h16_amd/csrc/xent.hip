@@ -184,7 +184,7 @@ struct GradEpi {
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds,
                                         uint8_t *info_at) const
     {
-        // of each row of the tile: scaled dl and dp, lse in base 2, and the target's column in the piece (-1: no
+        // of each row of the tile: scaled dl and dp, lse, and the target's column in the piece (-1: no
         // column of it, or a row without a gradient of its loss)
         f32x4 *info = reinterpret_cast<f32x4 *>(info_at);
         const int up = ranges->g;
@@ -195,7 +195,7 @@ struct GradEpi {
                 float dl, dp;
                 weights.of(m, dl, dp);
                 const int64_t at = weights.target[m] - v0;
-                v = f32x4{ldexpf(dl, up), ldexpf(dp, up), lse[m] * kLog2e,
+                v = f32x4{ldexpf(dl, up), ldexpf(dp, up), lse[m],
                           __int_as_float(dl != 0.0f && at >= 0 && at < op.N ? (int)at : -1)};
             }
             info[row] = v;
@@ -208,7 +208,9 @@ struct GradEpi {
                             const int want = __float_as_int(row[3]) - n, left = op.N - n;
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                float v = fast_exp2(fmaf(z[e / 4][e % 4], kLog2e, -ref)) * dp;
+                                // z - lse first: it is exact where the two are close, so that p is 1 as nearly as
+                                // lse tells, and p - 1 at a confident row's target no remainder of lse log2(e)
+                                float v = fast_exp2((z[e / 4][e % 4] - ref) * kLog2e) * dp;
                                 // dp == 0: nothing of the exponentials counts, whatever they are
                                 v = e < left && dp != 0.0f ? v : 0.0f;
                                 z[e / 4][e % 4] = e == want ? v - dl : v;

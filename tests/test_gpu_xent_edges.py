@@ -1,4 +1,5 @@
-"""The head's gradients at the ends of FP32's range, and beside infinities in a row's gradient and in W."""
+"""The head's gradients at the ends of FP32's range, beside infinities in a row's gradient and in W, and of
+confident rows with large logits."""
 import pytest
 import torch
 
@@ -115,3 +116,29 @@ def test_a_mask_of_minus_infinity_in_w(power):
     assert torch.isnan(dx[:, 0]).all() and bool(((dx.double() - rdx).abs() <= tol)[:, 1:].all())
     tol = (off.t() @ x.double().abs()) * 1.01 + g.abs().sum(0)[:, None] * 2.0 ** -39 * x_top + half * rdw.abs()
     assert bool(((dw[:kept].double() - rdw).abs() <= tol).all()) and not dw[kept:].any()
+
+
+@pytest.mark.parametrize("big", [0.0, 96.0, 128.0, 250.0, 1000.0, -40.0, -250.0])
+def test_confident_rows_beside_large_logits(big):
+    """Rows whose target leads by 28 or more, all logits shifted by `big`. One product of small integers a logit, all exact, so
+    lse is the target's logit, rounded by less than (V - 1) exp(-gap) < 4.2e-10: G at the target, which is
+    -(V - 1) exp(-gap) / (1 + ...) dloss, may be off by that much of dloss, and by nothing that grows with |lse|. Column
+    1 + t of X is row t's alone, so dW[target(t)][1 + t] is G there."""
+    T, K, V = 60, 64, 600
+    x, w = torch.zeros(T, K), torch.zeros(V, K)
+    rows = torch.arange(T)
+    target = rows * 13 % V
+    gap = 28.0 + rows % 30
+    # big in two parts that bf16 holds exactly
+    x[:, 0] = x[:, 61] = 1.0
+    w[:, 0] = torch.tensor(big).to(BF).float()
+    w[:, 61] = big - w[:, 0]
+    x[rows, 1 + rows] = 1.0
+    w[target, 1 + rows] = gap
+    dloss = 0.5 + rows / 128.0
+    announce("xent confident", big)
+    _, dw = _gradients(x.to(BF), w.to(BF), target, dloss)
+    at = dw[target, 1 + rows].double()
+    rest = (V - 1) * torch.exp(-gap.double())
+    want = -rest / (1.0 + rest) * dloss.double()
+    assert bool(((at - want).abs() <= 1.01 * rest * dloss.double()).all())
