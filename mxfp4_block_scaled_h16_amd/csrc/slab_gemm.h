@@ -33,6 +33,7 @@
 #include <utility>
 
 #include "internal.h"
+#include "train_internal.h"
 
 namespace mx {
 namespace slab {
@@ -797,6 +798,7 @@ struct Plan {
     size_t partial_bytes;
 };
 constexpr int kTileSide[3] = {256, 128, 64};
+constexpr int kThreads[3] = {64 * Big::NW, 64 * Small::NW, 64 * Tiny::NW};
 
 inline int64_t count_tiles(int64_t M, int64_t N, bool sym, int side)
 {
@@ -819,7 +821,7 @@ inline double round_time(int geo, int64_t n, int64_t per)
     }
 }
 
-// The plan with the least time by that account: full rounds of as many workgroups as the chip holds, and the
+// The plan with the least time by that account (whole < 0: the product has more tiles than a grid): full rounds of as many workgroups as the chip holds, and the
 // tiles left over, each worked by several workgroups if that is quicker; then their sums' kernel too, whose
 // workgroups read one split after the other (0.9, 0.5 and 0.3 us each by tile size). 1024 x 1024 x
 // 8192: 137 us in 256 x 256 tiles, 54 split eight ways, 35 in 128 x 128 tiles split four ways, 30 in 64 x 64
@@ -831,11 +833,11 @@ inline Plan plan_product(int64_t M, int64_t N, int64_t nk, bool sym, int64_t bat
     Plan best{0, -1, 0, 1, 1, 0};
     double least = 0.0;
     if (nk < 1) nk = 1;   // an empty contraction asks for no workspace
-    // more tiles than a grid is counted in here: no plan (such operands fit no memory)
+    // more tiles than a grid has in any of the sizes: no plan
     if ((double)M * (double)N * (double)batch > 1e15) return Plan{0, -1, 0, 1, (int)nk, 0};
     for (int g = 0; g < 3; ++g) {
         const int64_t tiles = count_tiles(M, N, sym, kTileSide[g]) * batch;
-        if (tiles > 1 << 26) continue;
+        if (tiles > kMaxItems / kThreads[g]) continue;
         const int64_t full = tiles / kSlots[g] * kSlots[g], left = tiles - full;
         const double rounds = (double)(tiles / kSlots[g]) * round_time(g, kSlots[g], nk);
         double t = rounds + (left ? round_time(g, left, nk) : 0.0);
@@ -845,7 +847,7 @@ inline Plan plan_product(int64_t M, int64_t N, int64_t nk, bool sym, int64_t bat
         }
         for (int64_t s = 2; s <= 16 && left > 0 && nk / s >= 4; ++s) {
             const int64_t per = (nk + s - 1) / s, used = (nk + per - 1) / per, n = left * used;
-            if (used != s) continue;
+            if (used != s || full + n > kMaxItems / kThreads[g]) continue;
             const double bytes = (double)n * kTileSide[g] * kTileSide[g] * 4;
             t = rounds + (double)(n / kSlots[g]) * round_time(g, kSlots[g], per) +
                 (n % kSlots[g] ? round_time(g, n % kSlots[g], per) : 0.0) + 3.0 + (double)used * kJoin[g] + bytes / 4.0e6;

@@ -8,6 +8,9 @@
 
 namespace mx {
 
+// a grid holds fewer than 2^32 work-items along an axis
+constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;
+
 constexpr int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // ------------------------------------------------------------------------------- E4M3 ---------

@@ -41,6 +41,7 @@ struct StatsEpi {
     float2 *part;            // [tiles_n][T]
     float *zt;               // [T]
     const int64_t *target;
+    int64_t v0;              // the launch's first column
 
     template <class G>
     __device__ __forceinline__ void run(f32x4 (&acc)[G::FI][G::FJ], const Where &w, const Operands &op, uint8_t *lds,
@@ -56,7 +57,7 @@ struct StatsEpi {
             const int row = w.row0 + 16 * i + r;
             const int m = min(w.m0 + row, op.M - 1);
             // the target's place among this lane's columns; far outside when it is not an index
-            const int64_t tc = target[m] - (w.n0 + w.col0 + 4 * q);
+            const int64_t tc = target[m] - v0 - (w.n0 + w.col0 + 4 * q);
             const int want = tc >= 0 && tc < 64 ? (int)tc : -1;
             float top = -INFINITY;
             float hit = 0.0f;
@@ -446,6 +447,16 @@ int64_t piece_columns(int64_t T, int64_t V)
     return round_up((V + pieces - 1) / pieces, 256);
 }
 
+// The loss keeps no logits, so its tiles may be more than a grid holds: then a launch takes as many columns
+// of the vocabulary as make 2^23 - 1 tiles of 256 x 256. part holds the launches' tiles one after the other.
+int64_t loss_columns(int64_t T, int64_t V)
+{
+    const int64_t most = kMaxItems / kThreads[0] / ((T + 255) / 256) * 256;
+    return V < most ? V : most;
+}
+Plan loss_plan(int64_t T, int64_t K, int64_t cols) { return plan_product(T, cols, round_up(K, 64) / 64, false, 1); }
+int64_t loss_tiles(const Plan &plan, int64_t cols) { return (cols + kTileSide[plan.geo] - 1) / kTileSide[plan.geo]; }
+
 // The products of a piece: G covers whole tiles, and the products over it run to the end of the last one.
 struct PiecePlans {
     Plan g, dx, dw;
@@ -493,11 +504,18 @@ Layout carve(Carve &c, int64_t T, int64_t K, int64_t V, bool backward)
         l.wp = static_cast<uint16_t *>(c.take(2 * V * kp));
     }
     if (!backward) {
-        const Plan plan = plan_product(T, V, kp / 64, false, 1);
-        const int64_t side = kTileSide[plan.geo];
-        l.part = static_cast<float2 *>(c.take(8 * T * ((V + side - 1) / side)));
+        const int64_t step = loss_columns(T, V), rest = V % step;
+        const Plan plan = loss_plan(T, K, step);
+        int64_t tiles = V / step * loss_tiles(plan, step);
+        size_t most = plan.partial_bytes;
+        if (rest) {
+            const Plan end = loss_plan(T, K, rest);
+            tiles += loss_tiles(end, rest);
+            most = std::max(most, end.partial_bytes);
+        }
+        l.part = static_cast<float2 *>(c.take(8 * T * tiles));
         l.zt = static_cast<float *>(c.take(4 * T));
-        l.partials = c.take(plan.partial_bytes);
+        l.partials = c.take(most);
         return l;
     }
     const int64_t tp = round_up(T, 256), vc = piece_columns(T, V);
@@ -565,14 +583,21 @@ hipError_t launch_xent_forward(const XentProblem &p, void *ws, float *loss, floa
 {
     Carve c{static_cast<uint8_t *>(ws)};
     const Layout l = carve(c, p.T, p.K, p.V, false);
-    Operands op{};
-    if (hipError_t e = logits_operands(p, l, op, stream)) return e;
-    op.N = (int)p.V;
-    const StatsEpi epi{l.part, l.zt, p.target};
-    const Plan plan = plan_product(p.T, p.V, op.nk, false, 1);
-    if (hipError_t e = launch_product<BF16>(op, epi, plan, l.partials, stream)) return e;
-    const int tiles = (int)((p.V + kTileSide[plan.geo] - 1) / kTileSide[plan.geo]);
-    return launch(xent_join_kernel, dim3((unsigned)((p.T + 31) / 32)), dim3(256), 0, stream, l.part, tiles, (int)p.T, p.V,
+    Operands lo{};
+    if (hipError_t e = logits_operands(p, l, lo, stream)) return e;
+    const int64_t step = loss_columns(p.T, p.V);
+    int64_t tiles = 0;
+    for (int64_t v0 = 0; v0 < p.V; v0 += step) {
+        const int64_t cols = p.V - v0 < step ? p.V - v0 : step;
+        Operands op = lo;
+        op.b = lo.b + v0 * lo.ldb;
+        op.N = (int)cols;
+        const Plan plan = loss_plan(p.T, p.K, cols);
+        const StatsEpi epi{l.part + tiles * p.T, l.zt, p.target, v0};
+        if (hipError_t e = launch_product<BF16>(op, epi, plan, l.partials, stream)) return e;
+        tiles += loss_tiles(plan, cols);
+    }
+    return launch(xent_join_kernel, dim3((unsigned)((p.T + 31) / 32)), dim3(256), 0, stream, l.part, (int)tiles, (int)p.T, p.V,
                   l.zt, p.target, p.ignore_index, loss, lse);
 }
 

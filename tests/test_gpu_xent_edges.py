@@ -142,3 +142,27 @@ def test_confident_rows_beside_large_logits(big):
     rest = (V - 1) * torch.exp(-gap.double())
     want = -rest / (1.0 + rest) * dloss.double()
     assert bool(((at - want).abs() <= 1.01 * rest * dloss.double()).all())
+
+
+def test_a_loss_of_more_tiles_than_a_grid():
+    """2^21 - 1 tokens against 2^18 + 5 words: 2^23 tiles of 256 x 256, which the loss takes in two launches. Rows from all over
+    the batch, their targets on both sides of the cut (column 261888), against the formula."""
+    mx = _mx()
+    T, K, V, cut = (1 << 21) - 1, 64, (1 << 18) + 5, 261888
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, K, generator=g, device="cuda").to(BF)
+    w = (torch.randn(V, K, generator=g, device="cuda") / 8).to(BF)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    rows = torch.cat([torch.arange(8), torch.tensor([255, 256, 1 << 20, T - 257, T - 2, T - 1]),
+                      torch.randint(0, T, (50,), generator=torch.Generator().manual_seed(1))]).cuda()
+    target[rows[::2]] = cut + torch.arange(rows[::2].numel(), device="cuda") % (V - cut)
+    target[rows[1]], target[rows[3]], target[rows[5]] = cut - 1, 0, -100
+    announce("xent of two launches")
+    loss, lse = mx.linear_xent_forward(x, w, target)
+    z = x[rows].double() @ w.double().t().contiguous()
+    want = torch.logsumexp(z, dim=1)
+    at = target[rows]
+    wl = torch.where(at != -100, want - z[torch.arange(rows.numel(), device="cuda"), at.clamp(min=0)], 0.0)
+    t = _tol(K, float(x[rows].double().norm(dim=1).max() * w.double().norm(dim=1).max())) + 2.0 ** -21 * (1.0 + float(want.abs().max()))
+    assert float((lse[rows].double() - want).abs().max()) <= t and float((loss[rows].double() - wl).abs().max()) <= 2 * t
+    assert bool(torch.isfinite(loss).all()) and bool((lse > 0).all())
