@@ -236,7 +236,7 @@ hipError_t launch_fp8_quantize(const Fp8Input *items, int count, hipStream_t str
         ++n;
     }
     if (n == 0) return hipSuccess;
-    if (total > INT32_MAX) return hipErrorInvalidValue;
+    if (total > kFp8Tiles) return hipErrorInvalidValue;
     for (int i = n; i <= kFp8Group; ++i) args.first[i] = (int)total;
     bool ragged = false;
     for (int i = 0; i < n; ++i) ragged = ragged || args.item[i].cols % 8 != 0;

@@ -41,6 +41,8 @@ bool valid_out(int t) { return t == MXFP4_OUT_F32 || t == MXFP4_OUT_BF16; }
 size_t out_size(int t) { return t == MXFP4_OUT_BF16 ? 2 : 4; }
 bool in_range(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
 
+int64_t fp8_tiles(int64_t rows, int64_t cols) { return (rows + 127) / 128 * ((cols + 127) / 128); }
+
 mxfp4_status_t check_fp8_out(const uint8_t *q, int64_t ldq, const uint8_t *s, int64_t lds, int64_t L)
 {
     if (ldq < mx::round_up(L, 128) || lds < (L + 127) / 128 || lds < 1) return MXFP4_ERR_ARG;
@@ -66,11 +68,14 @@ bool linear_plan(int pass, int64_t M, int64_t K, int64_t N, LinearPlan &p)
 {
     if (!in_range(M, 0, kMaxLinear) || !in_range(K, 0, kMaxLinear) || !in_range(N, 0, kMaxLinear)) return false;
     switch (pass) {
-    case MXFP4_FPROP: p = {{M, K}, {N, K}}; return true;
-    case MXFP4_DGRAD: p = {{M, N}, {K, N}}; return true;
-    case MXFP4_WGRAD: p = {{N, M}, {K, M}}; return true;
+    case MXFP4_FPROP: p = {{M, K}, {N, K}}; break;
+    case MXFP4_DGRAD: p = {{M, N}, {K, N}}; break;
+    case MXFP4_WGRAD: p = {{N, M}, {K, M}}; break;
     default: return false;
     }
+    // what the two launches can hold
+    return fp8_tiles(p.a.outer, p.a.L) + fp8_tiles(p.b.outer, p.b.L) <= mx::kFp8Tiles &&
+           mx::product_fits_grid(p.a.outer, p.b.outer);
 }
 size_t linear_bytes(const LinearPlan &p)
 {
@@ -131,7 +136,8 @@ bool ortho_sizes(int64_t batch, int64_t m, int64_t n)
 {
     const int64_t most = (int64_t)1 << 20;
     if (!in_range(batch, 0, 65535) || !in_range(m, 0, most) || !in_range(n, 0, most)) return false;
-    return batch == 0 || m == 0 || n == 0 || n <= ((int64_t)1 << 31) / batch / m;
+    if (batch == 0 || m == 0 || n == 0) return true;
+    return n <= ((int64_t)1 << 31) / batch / m && mx::product_fits_grid(m, n, batch);
 }
 // The scalar iteration on a grid of starting singular values, against the range that FP16 holds.
 bool ortho_bounded(int steps, float a, float b, float c)
@@ -162,7 +168,7 @@ mxfp4_status_t mxfp4_fp8_quantize(const void *x, mxfp4_dtype_t dtype, int64_t ro
     if (dtype != MXFP4_IN_BF16 && dtype != MXFP4_IN_F32) return MXFP4_ERR_ARG;
     if (block != MXFP4_FP8_ROW && block != MXFP4_FP8_TILE) return MXFP4_ERR_ARG;
     if (!in_range(rows, 0, kMaxDim) || !in_range(cols, 0, kMaxDim)) return MXFP4_ERR_SHAPE;
-    if (cols > 0 && (rows + 127) / 128 > kMaxDim / ((cols + 127) / 128)) return MXFP4_ERR_SHAPE;
+    if (fp8_tiles(rows, cols) > mx::kFp8Tiles) return MXFP4_ERR_SHAPE;
     if (ldx < cols || ldx < 1) return MXFP4_ERR_ARG;
     if (rows == 0 || cols == 0) return MXFP4_OK;
     if (!x || (!q1 && !q0)) return MXFP4_ERR_NULL;
@@ -180,7 +186,7 @@ mxfp4_status_t mxfp4_fp8_quantize(const void *x, mxfp4_dtype_t dtype, int64_t ro
 
 size_t mxfp4_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K)
 {
-    if (!in_range(M, 1, kMaxDim) || !in_range(N, 1, kMaxDim) || !in_range(K, 1, kMaxDim)) return 0;
+    if (!in_range(M, 1, kMaxDim) || !in_range(N, 1, kMaxDim) || !in_range(K, 1, kMaxDim) || !mx::product_fits_grid(M, N)) return 0;
     return mx::fp8_gemm_workspace_bytes(M, N, K);
 }
 
@@ -196,6 +202,7 @@ mxfp4_status_t mxfp4_fp8_gemm(const uint8_t *aq, int64_t lda, const uint8_t *as,
     if (!in_range(lda, kp, most) || !in_range(ldb, kp, most) || !in_range(ldas, kb, most) || !in_range(ldbs, kb, most))
         return MXFP4_ERR_ARG;
     if (M == 0 || N == 0) return MXFP4_OK;
+    if (!mx::product_fits_grid(M, N)) return MXFP4_ERR_SHAPE;
     if (!c || (K > 0 && (!aq || !as || !bq || !bs))) return MXFP4_ERR_NULL;
     if (!aligned(c, out_size(c_dtype))) return MXFP4_ERR_ALIGN;
     if (K > 0 && (!aligned(aq, 16) || !aligned(bq, 16) || !aligned(as, 16) || !aligned(bs, 16) || lda % 16 || ldb % 16 ||
@@ -238,7 +245,7 @@ size_t mxfp4_linear_xent_forward_workspace_bytes(int64_t T, int64_t K, int64_t V
 }
 size_t mxfp4_linear_xent_backward_workspace_bytes(int64_t T, int64_t K, int64_t V)
 {
-    return T > 0 && xent_sizes(T, K, V) ? mx::xent_backward_workspace_bytes(T, K, V) : 0;
+    return T > 0 && xent_sizes(T, K, V) && mx::xent_backward_fits_grid(T, K, V) ? mx::xent_backward_workspace_bytes(T, K, V) : 0;
 }
 
 mxfp4_status_t mxfp4_linear_xent_forward(const void *x, int64_t ldx, const void *w, int64_t ldw, const int64_t *target,
@@ -263,6 +270,7 @@ mxfp4_status_t mxfp4_linear_xent_backward(const float *dloss, const float *dlse,
 {
     if ((dx && !valid_out(dx_dtype)) || (dw && !valid_out(dw_dtype))) return MXFP4_ERR_ARG;
     if (mxfp4_status_t e = check_xent(x, ldx, w, ldw, target, T, K, V)) return e;
+    if (T > 0 && !mx::xent_backward_fits_grid(T, K, V)) return MXFP4_ERR_SHAPE;
     if (!dx && !dw) return MXFP4_OK;
     if ((dx && !aligned(dx, out_size(dx_dtype))) || (dw && !aligned(dw, out_size(dw_dtype)))) return MXFP4_ERR_ALIGN;
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -8,8 +8,13 @@
 
 namespace mx {
 
-// a grid holds fewer than 2^32 work-items along an axis
+// A grid holds fewer than 2^32 work-items along an axis. A product always has a plan when its tiles of 256 x 256, of 512
+// threads each, fit one.
 constexpr int64_t kMaxItems = ((int64_t)1 << 32) - 1;
+constexpr bool product_fits_grid(int64_t M, int64_t N, int64_t batch = 1)
+{
+    return (M + 255) / 256 * ((N + 255) / 256) * batch <= kMaxItems / 512;
+}
 
 constexpr int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
@@ -31,7 +36,9 @@ struct Fp8Input {
     Fp8Out axis1, axis0;
 };
 constexpr int kFp8Group = 2;
-// up to kFp8Group tensors of one type in one launch
+// up to kFp8Group tensors of one type in one launch, of at most kFp8Tiles tiles of 128 x 128 together (256
+// threads each)
+constexpr int64_t kFp8Tiles = kMaxItems / 256;
 hipError_t launch_fp8_quantize(const Fp8Input *items, int count, hipStream_t stream);
 
 // c = alpha A B^T + beta c, FP32 or bf16. K is the row length the scales cover; rows hold
@@ -54,6 +61,7 @@ struct XentProblem {
 };
 size_t xent_forward_workspace_bytes(int64_t T, int64_t K, int64_t V);
 size_t xent_backward_workspace_bytes(int64_t T, int64_t K, int64_t V);
+bool xent_backward_fits_grid(int64_t T, int64_t K, int64_t V);
 hipError_t launch_xent_forward(const XentProblem &p, void *ws, float *loss, float *lse, hipStream_t stream);
 // dloss, dlse: [T] or NULL (zeros); dx, dw: NULL or the gradients [T][K], [V][K], FP32 or bf16
 hipError_t launch_xent_backward(const XentProblem &p, const float *dloss, const float *dlse, const float *lse, void *ws,

@@ -579,6 +579,13 @@ size_t xent_backward_workspace_bytes(int64_t T, int64_t K, int64_t V)
     return c.at;
 }
 
+// the transposing copies' 128 x 128 tiles, of 256 threads; the products have fewer than half as many
+bool xent_backward_fits_grid(int64_t T, int64_t K, int64_t V)
+{
+    const int64_t down = round_up(T, 256) / 128 + round_up(piece_columns(T, V), 128) / 128;
+    return down * ((K + 127) / 128) <= kMaxItems / 256;
+}
+
 hipError_t launch_xent_forward(const XentProblem &p, void *ws, float *loss, float *lse, hipStream_t stream)
 {
     Carve c{static_cast<uint8_t *>(ws)};
