@@ -238,6 +238,8 @@ def fp8_gemm(aq, as_, bq, bs, alpha=1.0, beta=0.0, out=None, out_dtype=None, k=N
         if isinstance(workspace, str):
             need = fp8_gemm_workspace_bytes(M, N, K)
             workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        elif workspace is not None:
+            workspace = _room(workspace, 0, device)
         ws = (None, 0) if workspace is None else (workspace.data_ptr(), _bytes(workspace))
         _check(train_lib().mxfp4_fp8_gemm(aq.data_ptr(), aq.stride(0), as_.data_ptr(), as_.stride(0), bq.data_ptr(),
                                           bq.stride(0), bs.data_ptr(), bs.stride(0), M, N, K, float(alpha), float(beta),
