@@ -139,18 +139,28 @@ bool ortho_sizes(int64_t batch, int64_t m, int64_t n)
     if (batch == 0 || m == 0 || n == 0) return true;
     return n <= ((int64_t)1 << 31) / batch / m && mx::product_fits_grid(m, n, batch);
 }
-// The scalar iteration on a grid of starting singular values, against the range that FP16 holds.
-bool ortho_bounded(int steps, float a, float b, float c)
+// The scalar iteration against the range that FP16 holds. The values reached from [0, 1] are, up to their sign, an interval
+// [0, top] at every step (the step is continuous, odd, and 0 at 0), whose next end is the largest |step| at its end or where
+// the slope a + 3 b x + 5 c x x, x the square, vanishes. (A grid of starting values misses narrow ranges of them that
+// leave it after several steps.)
+bool ortho_bounded(int steps, float af, float bf, float cf)
 {
-    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
-    for (int i = 0; i <= 256; ++i) {
-        double s = i / 256.0;
-        for (int k = 0; k < steps; ++k) {
-            const double x = s * s, p = b * x + c * x * x;
-            if (std::fabs(p) > 32.0) return false;
-            s = (a + p) * s;
-            if (std::fabs(s) > 4.0) return false;
-        }
+    if (!std::isfinite(af) || !std::isfinite(bf) || !std::isfinite(cf)) return false;
+    const double a = af, b = bf, c = cf;
+    const auto poly = [&](double x) { return b * x + c * x * x; };
+    // places of extrema; those that do not exist come out as NaN or outside every interval
+    const double vertex = -b / (2.0 * c), root = -1.5 * b - std::copysign(0.5 * std::sqrt(9.0 * b * b - 20.0 * a * c), b);
+    const double flat[2] = {root / (5.0 * c), a / root};
+    double top = 1.0;
+    for (int k = 0; k < steps; ++k) {
+        const double end = top * top;
+        double high = std::fabs(poly(end));
+        if (vertex > 0.0 && vertex < end) high = std::max(high, std::fabs(poly(vertex)));
+        if (high > 32.0) return false;
+        top = std::fabs((a + poly(end)) * top);
+        for (const double x : flat)
+            if (x > 0.0 && x < end) top = std::max(top, std::fabs((a + poly(x)) * std::sqrt(x)));
+        if (top > 4.0) return false;
     }
     return true;
 }
