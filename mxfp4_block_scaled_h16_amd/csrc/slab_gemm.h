@@ -100,6 +100,15 @@ __device__ __forceinline__ void barrier()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Between LDS accesses by which lanes of one wavefront hand values to each other: its LDS instructions are carried out in
+// their order, so it is the compiler alone that must not move one across; no instruction comes of it.
+__device__ __forceinline__ void lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+}
+
 // f(0), f(1), ... f(N - 1), the numbers as types
 template <class F, int... K>
 __device__ __forceinline__ void each_of(F f, std::integer_sequence<int, K...>)
@@ -567,7 +576,9 @@ struct Block32 {
     // make one piece of code with a variable index out of them (the accumulators would go to memory).
     static __device__ __forceinline__ void put(uint8_t *block, int lane, const f32x4 (&acc)[G::FI][G::FJ], int blk)
     {
+        lds_order();   // what the lanes have read there before
         put_blocks(block + (lane & 15) * kLine, lane, acc, blk, std::make_integer_sequence<int, kBlocks>());
+        lds_order();
     }
 
 private:
@@ -771,6 +782,7 @@ __device__ __forceinline__ void store_tile16(f32x4 (&acc)[G::FI][G::FJ], const W
             }
         }
         if (cols) {
+            lds_order();
 #pragma unroll
             for (int p = 0; p < B::kPasses; ++p)
 #pragma unroll
@@ -778,6 +790,7 @@ __device__ __forceinline__ void store_tile16(f32x4 (&acc)[G::FI][G::FJ], const W
                     const int c = 8 * c8 + (odd ? 4 : 0) + h, l = (B::kLinesPerPass * p + line) & ~1;
                     *reinterpret_cast<uint32_t *>(block + piece(c, l >> 3) + 2 * (l & 7)) = pairs[p][h];
                 }
+            lds_order();
             constexpr int kColsPerPass = 64 / kPieces;
             const int col = w.lane / kPieces, pc = w.lane % kPieces;
             uint16_t *to = cols + (int64_t)(w.n0 + w.col0 + col) * ld_cols + m + 8 * pc;
