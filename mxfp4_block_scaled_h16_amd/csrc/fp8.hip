@@ -12,8 +12,8 @@ namespace {
 // 8 x 8 values each (rows 8 (t / 16) .., columns 8 (t % 16) ..), in registers throughout. Row
 // maxima join the 16 lanes of a row, column maxima the 16 threads of a column through the LDS.
 // Bound by memory: a bf16 value is read once (2 bytes) and a code written per axis (1 byte each). 8192 x 4096 and
-// 6144 x 4096 along their rows in one launch: 42 us, 4.2 TB/s of the 4.97 that a copy reaches; 8192 x 14336 and 8192 x
-// 4096 along their columns: 101 us, 4.5 TB/s.
+// 6144 x 4096 along their rows in one launch: 39 us, 4.5 TB/s of the 4.97 that a copy reaches; 8192 x 14336 and 8192 x
+// 4096 along their columns: 102 us, 4.4 TB/s.
 struct Fp8Args {
     Fp8Input item[kFp8Group];
     int first[kFp8Group + 1];   // workgroups before each item

@@ -16,20 +16,24 @@
 // of the X that it is multiplied by count |b + c| times (2.7). A step may as well be (a - t) X +
 // (b A + c A A + t) X: with t = -(b + c) they count next to nothing there, but t times for the directions that
 // are still small, and what those pick up grows with them in the steps that follow. So the last step takes
-// t = -(b + c), the two before it a half and a quarter of it, and the others none. Relative error in five steps
-// (16 x 16 to 486 x 900, heavy tails): 0.0007 to 0.0016, without t 0.0014 to 0.0029; a few strong directions
-// over noise 1/1000 of them: 0.0016, without t 0.0004, with t = -(b + c) in every step 0.03. A bf16 result's own
-// rounding is 0.0017. A's diagonal carried in FP32 beside it took 16 x 5000, the worst shape here, from 0.0022 to
-// 0.0018 and cost 1 to 4% of the time: not taken.
+// t = -(b + c), the two before it a half and a quarter of it, and the others none. Relative error in five steps,
+// heavy tails: 0.0007 to 0.0016 (16 x 16 to 1000 x 1500, medians; up to 0.0024 with a side of 16 to 64), without t
+// 0.0014 to 0.0029. One strong direction over noise gains from no t (0.0004) and pays for it: 0.0005 over noise of
+// 1/100, 0.0026 over 1/1000, 0.0032 over less, where the noise's directions hold little but those roundings; with t =
+// -(b + c) in every step 0.03. Sides of 1 to 15 have too few roundings to average: 0.001 to 0.004, now and then 0.01.
+// A bf16 result's own rounding is 0.0017. A's diagonal carried in FP32 beside it took 16 x 5000 from 0.0022 to 0.0018 and
+// cost 1 to 4% of the time: not taken.
 //
 // Per step three launches: A (symmetric: the lower triangle of tiles, written twice), b A + c A A
 // (symmetric too), and the update, which writes X in both orientations for the next step's
 // products, each of which contracts along rows.
 //
-// Bound by the matrix cores: 4096 x 4096 in 1.44 to 1.52 ms, of which the updates 133 us each (1.03 PFLOP/s; they
-// write X three times) and the symmetric products 103 us, whose 136 tiles leave 120 CUs idle (in
-// 128 x 128 tiles, which fill them, they take longer). 14336 x 4096: 4.1 to 4.2 ms; an update 477 + 28 us for the
-// half round of its 896 tiles that is split. Small ones by their launches: 256 x 512 takes 79 us in 17, each 4 to 6 us.
+// Bound by the matrix cores: 4096 x 4096 in 1.45 ms, of which the four updates 121 us each (1.14 PFLOP/s; they write X
+// three times), the last one 110, and the ten symmetric products 82 each, whose 136 tiles leave 120 CUs idle (in 128 x 128
+// tiles, which fill them, they take longer); norm and first operands 32. 14336 x 4096: 4.09 ms; an update 429 us + 27 for the
+// half round of its 896 tiles that is split, the last 386 + 20, A 226 + 26, b A + c A A 89, norm and first operands 151. 2 x
+// 1024 x 4096: 0.32 ms; 22, 9 and 30 us a step. Small ones by each launch's own latency: 256 x 512 takes 79 us in 17, each 4
+// to 6 us. (Kernels and wholes from one session, 60 calls on end.)
 #include <algorithm>
 
 #include "slab_gemm.h"
@@ -219,7 +223,7 @@ __device__ __forceinline__ void read_g8(const void *g, int64_t at, float (&v)[8]
 }
 
 // Sums of squares, one per workgroup, in 64 bits (the squares of FP32 numbers leave FP32's range). Bound by
-// memory: 14336 x 4096 in FP32 51 us, 4.6 TB/s. vec: 16-byte aligned rows of whole eights.
+// memory: 14336 x 4096 in FP32 52 us, 4.5 TB/s. vec: 16-byte aligned rows of whole eights.
 template <bool F32>
 __global__ __launch_bounds__(256) void norm_kernel(const void *__restrict__ g, int64_t m, int64_t n, int64_t ldg, int64_t batch_g,
                                                    int vec, double *__restrict__ part)
@@ -256,7 +260,7 @@ __global__ __launch_bounds__(256) void norm_kernel(const void *__restrict__ g, i
 // X = G / (|G| + eps), times 2^10, in value and remainder and (the value) transposed, with zeros around it.
 // 128 x 128 tiles: a thread takes 8 x 8 values and transposes them in registers; 256-byte lines of
 // the transposed are put together in the LDS. Bound by memory: 4 (or 2) bytes in, 6 out; 14336 x 4096 from FP32
-// 101 us (5.8 TB/s, some of it from the cache that the norm's read has filled).
+// 99 us (5.9 TB/s, some of it from the cache that the norm's read has filled).
 template <bool F32>
 __global__ __launch_bounds__(256) void first_kernel(const void *__restrict__ g, int64_t m, int64_t n, int64_t ldg, int64_t batch_g,
                                                     int vec, const double *__restrict__ part, int parts, float eps,

@@ -14,8 +14,9 @@
 // over the second half of a stage instead of bunched behind the barrier: 1360; a second barrier
 // that leaves them half a stage longer: 1340.
 //
-// In FP8 a stage takes as long, for twice the values: 8192 x 6144 x 4096 167 us, 2.47 PFLOP/s (the library with
-// one scale for each matrix: 158 us); what is left is the power cap and the epilogue, which the next tile does not
+// In FP8 a stage takes as long, for twice the values: 8192 x 6144 x 4096 174 to 215 us by the power that the card
+// has left, 187 on average, 2.2 PFLOP/s (the library with one scale for each matrix, in turn with it: 142 to 177, 154);
+// 4096 x 14336 x 8192 376 us, 2.56 PFLOP/s (316). What is left is the power cap and the epilogue, which the next tile does not
 // overlap. A workgroup per CU that walks over its tiles with the next tile's loads ahead of the epilogue needs
 // registers that are not there (9 to 28 spilled) and was slower: FP16 896 tiles 17%, bf16 heads 2%.
 //

@@ -10,11 +10,13 @@
 // once. The second operands of these are FP16 copies of W's piece and of X, transposed, so that every
 // product contracts along rows.
 //
-// Bound by the matrix cores, under the card's power cap: at T 8192, K 4096, V 128256 27 ms, of which the loss' product
-// 6.5 (1.32 PFLOP/s; the library's plain product, which stores its logits, 5.9), and in each of eight pieces G's 0.91,
-// dX's 0.87 and dW's 0.79 (1.19, 1.25 and 1.37 PFLOP/s). At T 2048, K 2048, V 50257 the loss takes 360 us, the
-// library's product alone 391. What is not products: 3% at the large size (copies 50 us a piece, ranges 0.2 ms), at T 1537,
-// K 1024 a tenth of 0.87 ms; at T 128, K 512, V 1000 a call is bound by its 7 launches and the host.
+// Bound by the matrix cores, under the card's power cap: at T 8192, K 4096, V 128256 26.9 ms, of which the loss' product
+// 6.14 (1.40 PFLOP/s; the library's plain product, which stores its logits, 5.8 in turn with it), and in each of eight
+// pieces G's 0.89, dX's 0.85 and dW's 0.78 (1.21, 1.26 and 1.38 PFLOP/s). At T 2048, K 2048, V 50257 the loss takes 376 us, of
+// which the product 354 and the joining of its rows and of its last tiles 10 each; the library's product alone, in turn
+// with it, 401 to 370. What is not products: 3% at the large size (copies 49 us a piece, ranges 0.2 ms), at T 1537, K 1024 a
+// tenth of 0.87 ms; at T 128, K 512, V 1000 a call's 42 us are 7 launches one after the other, of 3 to 6 us. (Kernels and
+// wholes from one session, 20 to 60 calls on end.)
 #include <algorithm>
 #include <cfloat>
 
@@ -238,7 +240,7 @@ __device__ __forceinline__ float block_max(float v)
 // Largest finite |value| of a bf16 matrix over this workgroup's share of it. The magnitudes' bits are moved up
 // by 0x80, which carries those of NaN and infinity (0x7F80 and above) into the sign: as signed numbers they are
 // below every finite one, two values an instruction.
-// Bound by memory, 2 bytes a value: 8192 x 4096 and 128256 x 4096 in 202 us, 5.5 TB/s. vec: 16-byte aligned rows of whole
+// Bound by memory, 2 bytes a value: 8192 x 4096 and 128256 x 4096 in 208 us, 5.4 TB/s. vec: 16-byte aligned rows of whole
 // 16 bytes.
 __device__ __forceinline__ float share_max(const uint16_t *p, int64_t ld, int64_t rows, int64_t cols, bool vec,
                                            const RowWeights &weights)
@@ -344,7 +346,7 @@ struct Turn {
 };
 // One or two of them, X's and that of a piece of W. 128 x 128 tiles: a thread transposes 8 x 8 values in
 // registers, then 256-byte lines are put together in the LDS. Bound by memory: 2 bytes in, 2 out; a piece of 16128 x
-// 4096 in 50 us, 5.3 TB/s.
+// 4096 in 49 us, 5.4 TB/s.
 // blocks > 0: the ranges are joined here.
 __global__ __launch_bounds__(256) void turn_kernel(Turn tx, Turn tw, RowWeights weights, const float *part, int blocks,
                                                    Ranges *ranges)
@@ -436,8 +438,9 @@ Turn turn_of(const void *in, int64_t ld_in, int64_t rows, int64_t cols, uint16_t
 }
 
 // ------------------------------------------------------------------------------ workspace -----
-// Pieces of the vocabulary: G takes at most 256 MB per orientation, so that a piece stays near the
-// last-level cache, and a piece has at least 2048 columns.
+// Pieces of the vocabulary, as even as whole tiles allow: of as many columns as give G 256 MB per orientation, which
+// stays near the last-level cache, but of 2048 before they are evened out if that is more (1280 columns at T 70000, V 2100;
+// from 65536 tokens on G is larger: 8 GB at 2^21).
 int64_t piece_columns(int64_t T, int64_t V)
 {
     const int64_t tp = round_up(T, 256);

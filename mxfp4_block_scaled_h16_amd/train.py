@@ -324,7 +324,8 @@ def _per_row(t, T, name):
 def linear_xent_forward(x, w, target, ignore_index=-100, workspace=None, stream=None):
     """Softmax cross entropy of the logits X[T,K] W[V,K]^T, which are not kept. Returns (loss, lse), FP32
     [T]: lse_t = log sum_v exp z_tv and loss_t = lse_t - z_t,target, 0 where target is ignore_index, NaN
-    where it is no index."""
+    where it is no index. x and w bf16 of unit column stride; with K a multiple of 64 their rows have to start at
+    multiples of 16 bytes, any other K is copied and needs no alignment."""
     device = _same_device(x=x, w=w, target=target, workspace=workspace)
     ldx, ldw = _xent_operands(x, w, target)
     (T, K), V = x.shape, w.shape[0]
@@ -343,7 +344,8 @@ def linear_xent_backward(dloss, x, w, target, lse, dlse=None, ignore_index=-100,
                          dx_dtype=torch.bfloat16, dw_dtype=torch.bfloat16, dx=None, dw=None, workspace=None, stream=None):
     """Gradients (dX[T,K], dW[V,K]) of linear_xent_forward, from the gradients of each row's loss (dloss,
     FP32 [T] or None) and of each row's lse (dlse, likewise), and the forward call's lse. need_dx or need_dw
-    false: None in that place. Outputs bf16 or FP32."""
+    false: None in that place. Outputs bf16 or FP32 (the products' operands are FP16 either way, scaled). x and w as in
+    linear_xent_forward."""
     device = _same_device(x=x, w=w, target=target, lse=lse, dloss=dloss, dlse=dlse, dx=dx, dw=dw, workspace=workspace)
     ldx, ldw = _xent_operands(x, w, target)
     (T, K), V = x.shape, w.shape[0]
