@@ -17,12 +17,10 @@
 // (b A + c A A + t) X: with t = -(b + c) they count next to nothing there, but t times for the directions that
 // are still small, and what those pick up grows with them in the steps that follow. So the last step takes
 // t = -(b + c), the two before it a half and a quarter of it, and the others none. Relative error in five steps,
-// heavy tails: 0.0007 to 0.0016 (16 x 16 to 1000 x 1500, medians; up to 0.0024 with a side of 16 to 64), without t
-// 0.0014 to 0.0029. One strong direction over noise gains from no t (0.0004) and pays for it: 0.0005 over noise of
-// 1/100, 0.0026 over 1/1000, 0.0032 over less, where the noise's directions hold little but those roundings; with t =
-// -(b + c) in every step 0.03. Sides of 1 to 15 have too few roundings to average: 0.001 to 0.004, now and then 0.01.
-// A bf16 result's own rounding is 0.0017. A's diagonal carried in FP32 beside it took 16 x 5000 from 0.0022 to 0.0018 and
-// cost 1 to 4% of the time: not taken.
+// heavy tails (100 x 1000 to 1000 x 1500): 0.0007 to 0.0013, without t 0.0014 to 0.0029. One strong direction over noise
+// gains from no t (0.0004) and pays for it: 0.0005 over noise of 1/100, 0.0026 over 1/1000, 0.0032 over less, where the
+// noise's directions hold little but those roundings; with t = -(b + c) in every step 0.03. A bf16 result's own rounding is
+// 0.0017. Matrices with a side of at most 64 are worked in FP32 (below).
 //
 // Per step three launches: A (symmetric: the lower triangle of tiles, written twice), b A + c A A
 // (symmetric too), and the update, which writes X in both orientations for the next step's
@@ -257,6 +255,21 @@ __global__ __launch_bounds__(256) void norm_kernel(const void *__restrict__ g, i
     if (threadIdx.x == 0) part[blockIdx.z * kNormBlocks + blockIdx.x] = (slots[0] + slots[1]) + (slots[2] + slots[3]);
 }
 
+// `times` / (|G| + eps), from the partial sums of blockIdx.z's matrix: 2^-power times the result (the factor may lie outside
+// FP32's range where G's entries do not). By every workgroup of 256 threads, with a barrier.
+__device__ __forceinline__ float norm_factor(const double *part, int parts, float eps, double times, int &power)
+{
+    __shared__ double slots[4];
+    double sum = 0.0;
+    for (int k = threadIdx.x; k < parts; k += 256) sum += part[blockIdx.z * kNormBlocks + k];
+    for (int k = 32; k >= 1; k >>= 1) sum += __shfl_xor(sum, k);
+    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    const double norm = sqrt((slots[0] + slots[1]) + (slots[2] + slots[3])) + (double)eps;
+    power = norm > 0.0 && norm <= 1e300 ? ilogb(norm) : 0;
+    return (float)(times / ldexp(norm, -power));
+}
+
 // X = G / (|G| + eps), times 2^10, in value and remainder and (the value) transposed, with zeros around it.
 // 128 x 128 tiles: a thread takes 8 x 8 values and transposes them in registers; 256-byte lines of
 // the transposed are put together in the LDS. Bound by memory: 4 (or 2) bytes in, 6 out; 14336 x 4096 from FP32
@@ -268,16 +281,8 @@ __global__ __launch_bounds__(256) void first_kernel(const void *__restrict__ g, 
                                                     uint16_t *__restrict__ turned, int64_t mp, int64_t np, int64_t batch_x)
 {
     __shared__ __attribute__((aligned(16))) uint16_t tile[128 * 128];   // [column][row], 16-byte pieces permuted
-    __shared__ double slots[4];
-    double sum = 0.0;
-    for (int k = threadIdx.x; k < parts; k += 256) sum += part[blockIdx.z * kNormBlocks + k];
-    for (int k = 32; k >= 1; k >>= 1) sum += __shfl_xor(sum, k);
-    if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = sum;
-    __syncthreads();
-    // the factor may lie outside FP32's range where G's entries do not: a power of two apart from it
-    const double norm = sqrt((slots[0] + slots[1]) + (slots[2] + slots[3])) + (double)eps;
-    const int power = norm > 0.0 && norm <= 1e300 ? ilogb(norm) : 0;
-    const float inv = (float)(1024.0 / ldexp(norm, -power));
+    int power;
+    const float inv = norm_factor(part, parts, eps, 1024.0, power);
 
     const int64_t r0 = (int64_t)blockIdx.x * 128, c0 = (int64_t)blockIdx.y * 128;
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
@@ -321,6 +326,20 @@ __global__ __launch_bounds__(256) void first_kernel(const void *__restrict__ g, 
     }
 }
 
+// out[at] = v + beta out[at], which is read only when beta != 0
+__device__ __forceinline__ void put_out(void *out, int bf16, int64_t at, float v, float beta)
+{
+    if (bf16) {
+        uint16_t *p = static_cast<uint16_t *>(out) + at;
+        if (beta != 0.0f) v += beta * bf16_float(*p);
+        *p = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu);
+    } else {
+        float *p = static_cast<float *>(out) + at;
+        if (beta != 0.0f) v += beta * *p;
+        *p = v;
+    }
+}
+
 // steps == 0: out = alpha X + beta out from the first operands
 __global__ __launch_bounds__(256) void copy_out_kernel(const uint16_t *__restrict__ hi, const uint16_t *__restrict__ lo, int64_t np,
                                                        int64_t batch_x, int64_t m, int64_t n, float alpha, float beta, void *out,
@@ -329,17 +348,231 @@ __global__ __launch_bounds__(256) void copy_out_kernel(const uint16_t *__restric
     const int64_t total = m * n;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / n, c = i % n, at = blockIdx.z * batch_x + r * np + c, o = blockIdx.z * batch_o + r * ldo + c;
-        float v = alpha * ((f16_float(hi[at]) + f16_float(lo[at]) * kLoUnscale) * kUnscale);
-        if (bf16) {
-            uint16_t *p = static_cast<uint16_t *>(out) + o;
-            if (beta != 0.0f) v += beta * bf16_float(*p);
-            *p = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu);
-        } else {
-            float *p = static_cast<float *>(out) + o;
-            if (beta != 0.0f) v += beta * *p;
-            *p = v;
-        }
+        put_out(out, bf16, o, alpha * ((f16_float(hi[at]) + f16_float(lo[at]) * kLoUnscale) * kUnscale), beta);
     }
+}
+
+// ----------------------------------------------------------------------------- thin matrices --
+// A short side of at most 64: FP32 throughout, on the FP32 matrix cores. The few roundings of FP16 operands do not average
+// out here (an error of 0.0012 to 0.0037, below 16 now and then 0.01; so 1e-6 to 7e-5), and the work is little. Y, X with its
+// long side down, is [lp][64]; a step is one kernel: every workgroup forms Q = a + b A + c A A for itself, turns its rows of Y
+// into Y Q in place, and adds up their part of the next A. With more than kThinFew parts thin_sum_kernel adds them up in
+// between.
+// Bound by each launch's own latency: in us, with FP16 operands in 128 x 128 padding and so: 16 x 16 67 and 44; 20 x 10368 120
+// and 76; 64 x 14336 130 and 82; 8 of 16 x 14336 553 and 205; 1024 of 64 x 64 1712 and 120. (65 x 4096 in FP16: 101.)
+constexpr int kThin = 64, kThinTile = kThin * kThin;
+constexpr int kThinLine = kThin + 4;   // floats from a row to the next in the LDS: 16 rows of 4 values meet 64 distinct banks
+constexpr int kThinChunks = 256;       // workgroups a matrix is worked by, at most
+constexpr int kThinFew = 8;
+
+struct Thin {
+    const void *g;
+    int f32, bf16, wide;        // G's type, out's type; wide: the short side runs down G
+    int64_t s, l, ldg, batch_g; // the short and the long side
+    const double *norms;
+    int norm_parts;
+    float eps;
+    float *y;
+    int64_t lp;
+    int blocks;                 // of 64 rows, for each workgroup
+    const float *gram;          // [batch][parts][64][64]
+    int parts;
+    float *gram_out;            // [batch][gridDim.x][64][64]
+    float a, b, c, alpha, beta;
+    void *out;
+    int64_t ldo, batch_o;
+};
+
+// acc[j], 16 rows from `rows` against 16 j .. of `cols`, over 64 values along both their rows; element t: row 4 (lane / 16) + t,
+// column 16 j + lane % 16
+__device__ __forceinline__ void thin_product(const float *rows, const float *cols, int lane, f32x4 (&acc)[4])
+{
+    const int at = (lane & 15) * kThinLine + (lane >> 4);
+#pragma unroll 4
+    for (int k = 0; k < kThin; k += 4) {
+        const float x = rows[at + k];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, cols[at + 16 * j * kThinLine + k], acc[j], 0, 0, 0);
+    }
+}
+
+// FIRST: from G, scaled to norm 1, instead of a step. LAST: into the caller's matrix.
+template <bool FIRST, bool LAST>
+__global__ __launch_bounds__(256) void thin_kernel(Thin p)
+{
+    __shared__ __attribute__((aligned(16))) float q[kThin * kThinLine], y[kThin * kThinLine];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, low = lane >> 4;
+    const int64_t z = blockIdx.z;
+    int power = 0;
+    float inv = 0.0f;
+    if constexpr (FIRST) {
+        inv = norm_factor(p.norms, p.norm_parts, p.eps, 1.0, power);
+    } else {
+        const float *gram = p.gram + z * p.parts * kThinTile;
+        for (int e = 4 * tid; e < kThinTile; e += 1024) {
+            f32x4 v = *reinterpret_cast<const f32x4 *>(gram + e);
+            for (int k = 1; k < p.parts; ++k) v += *reinterpret_cast<const f32x4 *>(gram + k * kThinTile + e);
+            *reinterpret_cast<f32x4 *>(y + e / kThin * kThinLine + e % kThin) = v;
+        }
+        __syncthreads();
+        // A is symmetric to the bit (both places add the same products in one order), and so is Q
+        f32x4 acc[4] = {};
+        thin_product(y + 16 * wave * kThinLine, y, lane, acc);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int i = 16 * wave + 4 * low + t, col = 16 * j + r, at = i * kThinLine + col;
+                const float v = p.b * y[at] + p.c * acc[j][t];
+                q[at] = i == col ? v + p.a : v;
+            }
+        __syncthreads();
+    }
+    f32x4 sum[4] = {};
+    for (int k = 0; k < p.blocks; ++k) {
+        const int64_t row0 = ((int64_t)blockIdx.x * p.blocks + k) * kThin;
+        if (row0 >= p.lp) break;
+        float *rows = p.y + (z * p.lp + row0) * kThin;
+        if constexpr (FIRST) {
+            for (int e = tid; e < kThinTile; e += 256) {
+                // neighbouring threads along G's rows
+                const int i = p.wide ? e % kThin : e / kThin, j = p.wide ? e / kThin : e % kThin;
+                float v = 0.0f;
+                if (row0 + i < p.l && j < p.s) {
+                    const int64_t at = z * p.batch_g + (p.wide ? j * p.ldg + row0 + i : (row0 + i) * p.ldg + j);
+                    v = p.f32 ? read_g<true>(p.g, at) : read_g<false>(p.g, at);
+                }
+                y[i * kThinLine + j] = ldexpf(v, -power) * inv;
+            }
+            __syncthreads();
+        } else {
+            for (int e = 4 * tid; e < kThinTile; e += 1024)
+                *reinterpret_cast<f32x4 *>(y + e / kThin * kThinLine + e % kThin) = *reinterpret_cast<const f32x4 *>(rows + e);
+            __syncthreads();
+            f32x4 acc[4] = {};
+            thin_product(y + 16 * wave * kThinLine, q, lane, acc);
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) y[(16 * wave + 4 * low + t) * kThinLine + 16 * j + r] = acc[j][t];
+            __syncthreads();
+        }
+        if constexpr (LAST) {
+            for (int e = tid; e < kThinTile; e += 256) {
+                const int i = p.wide ? e % kThin : e / kThin, j = p.wide ? e / kThin : e % kThin;
+                if (row0 + i >= p.l || j >= p.s) continue;
+                const int64_t at = z * p.batch_o + (p.wide ? j * p.ldo + row0 + i : (row0 + i) * p.ldo + j);
+                put_out(p.out, p.bf16, at, p.alpha * y[i * kThinLine + j], p.beta);
+            }
+        } else {
+            for (int e = 4 * tid; e < kThinTile; e += 1024)
+                *reinterpret_cast<f32x4 *>(rows + e) = *reinterpret_cast<const f32x4 *>(y + e / kThin * kThinLine + e % kThin);
+#pragma unroll 4
+            for (int n = 0; n < kThin; n += 4) {
+                const float *at = y + (n + low) * kThinLine + r;
+                const float x = at[16 * wave];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(x, at[16 * j], sum[j], 0, 0, 0);
+            }
+        }
+        __syncthreads();
+    }
+    if constexpr (!LAST) {
+        float *out = p.gram_out + (z * gridDim.x + blockIdx.x) * kThinTile;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) out[(16 * wave + 4 * low + t) * kThin + 16 * j + r] = sum[j][t];
+    }
+}
+
+// A from its parts, in an order that does not depend on the batch: 8 threads an entry, each every eighth part
+__global__ __launch_bounds__(256) void thin_sum_kernel(const float *__restrict__ in, int parts, float *__restrict__ out)
+{
+    __shared__ float slots[8][32];
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    in += (int64_t)blockIdx.z * parts * kThinTile + e;
+    float v = 0.0f;
+#pragma unroll 8
+    for (int k = slice; k < parts; k += 8) v += in[k * kThinTile];
+    slots[slice][lane] = v;
+    __syncthreads();
+    if (slice != 0) return;
+    for (int k = 1; k < 8; ++k) v += slots[k][lane];
+    out[(int64_t)blockIdx.z * kThinTile + e] = v;
+}
+
+struct ThinSpace {
+    double *norms;
+    float *y, *gram[2], *sum;
+    int64_t lp;
+    int blocks, chunks;
+    size_t bytes;
+};
+ThinSpace thin_space(uint8_t *base, int64_t batch, int64_t l)
+{
+    ThinSpace s{};
+    s.lp = round_up(l, kThin);
+    s.blocks = (int)((s.lp / kThin + kThinChunks - 1) / kThinChunks);
+    s.chunks = (int)((s.lp / kThin + s.blocks - 1) / s.blocks);
+    auto take = [&](int64_t bytes) {
+        uint8_t *p = base ? base + s.bytes : nullptr;
+        s.bytes += (size_t)round_up(bytes, 256);
+        return p;
+    };
+    s.norms = reinterpret_cast<double *>(take(8 * kNormBlocks * batch));
+    s.y = reinterpret_cast<float *>(take(4 * kThin * s.lp * batch));
+    for (int k = 0; k < 2; ++k) s.gram[k] = reinterpret_cast<float *>(take(4 * kThinTile * s.chunks * batch));
+    s.sum = reinterpret_cast<float *>(take(4 * kThinTile * batch));
+    return s;
+}
+
+hipError_t launch_thin(const OrthoProblem &p, const ThinSpace &s, int norm_parts, hipStream_t stream)
+{
+    Thin t{};
+    t.g = p.g;
+    t.f32 = p.f32;
+    t.bf16 = p.out_bf16;
+    t.wide = p.m <= p.n;
+    t.s = t.wide ? p.m : p.n;
+    t.l = t.wide ? p.n : p.m;
+    t.ldg = p.ldg;
+    t.batch_g = p.batch_g;
+    t.norms = s.norms;
+    t.norm_parts = norm_parts;
+    t.eps = p.eps;
+    t.y = s.y;
+    t.lp = s.lp;
+    t.blocks = s.blocks;
+    t.gram_out = s.gram[0];
+    t.a = p.a;
+    t.b = p.b;
+    t.c = p.c;
+    t.alpha = p.alpha;
+    t.beta = p.beta;
+    t.out = p.out;
+    t.ldo = p.ldo;
+    t.batch_o = p.batch_o;
+    const dim3 grid((unsigned)s.chunks, 1, (unsigned)p.batch), block(256);
+    if (p.steps == 0) return launch(thin_kernel<true, true>, grid, block, 0, stream, t);
+    hipError_t e = launch(thin_kernel<true, false>, grid, block, 0, stream, t);
+    for (int k = 0; k < p.steps && e == hipSuccess; ++k) {
+        t.gram = s.gram[k & 1];
+        t.parts = s.chunks;
+        if (s.chunks > kThinFew) {
+            e = launch(thin_sum_kernel, dim3(kThinTile / 32, 1, (unsigned)p.batch), block, 0, stream, t.gram, s.chunks, s.sum);
+            if (e) return e;
+            t.gram = s.sum;
+            t.parts = 1;
+        }
+        // not where other workgroups of the launch still read
+        t.gram_out = s.gram[(k + 1) & 1];
+        e = k + 1 < p.steps ? launch(thin_kernel<false, false>, grid, block, 0, stream, t)
+                            : launch(thin_kernel<false, true>, grid, block, 0, stream, t);
+    }
+    return e;
 }
 
 // ------------------------------------------------------------------------------ workspace -----
@@ -412,23 +645,27 @@ hipError_t product(const Plan &plan, const Operands &op, const Epi &epi, const S
 
 size_t ortho_workspace_bytes(int64_t batch, int64_t m, int64_t n)
 {
+    if (std::min(m, n) <= kThin) return thin_space(nullptr, batch, std::max(m, n)).bytes;
     return carve(nullptr, batch, sizes_of(batch, m, n)).bytes;
 }
 
 hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
 {
-    const Sizes z = sizes_of(p.batch, p.m, p.n);
-    const Space s = carve(static_cast<uint8_t *>(ws), p.batch, z);
-    const int64_t bx = z.mp * z.np, ba = z.sp * z.sp;
     const int64_t esize = p.f32 ? 4 : 2;
     const int vec = p.n % 8 == 0 && (uintptr_t)p.g % 16 == 0 && p.ldg * esize % 16 == 0 && (p.batch == 1 || p.batch_g * esize % 16 == 0);
     const int64_t want = p.m * p.n / kNormTile + 1, most = p.m < kNormBlocks ? p.m : kNormBlocks;
     const int parts = (int)(want < most ? want : most);
     const dim3 ngrid((unsigned)parts, 1, (unsigned)p.batch);
-    const dim3 fgrid((unsigned)(z.mp / 128), (unsigned)(z.np / 128), (unsigned)p.batch);
-    hipError_t e = p.f32 ? launch(norm_kernel<true>, ngrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, vec, s.part)
-                         : launch(norm_kernel<false>, ngrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, vec, s.part);
+    double *norms = static_cast<double *>(ws);   // first in either workspace
+    hipError_t e = p.f32 ? launch(norm_kernel<true>, ngrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, vec, norms)
+                         : launch(norm_kernel<false>, ngrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, vec, norms);
     if (e) return e;
+    if (std::min(p.m, p.n) <= kThin)
+        return launch_thin(p, thin_space(static_cast<uint8_t *>(ws), p.batch, std::max(p.m, p.n)), parts, stream);
+    const Sizes z = sizes_of(p.batch, p.m, p.n);
+    const Space s = carve(static_cast<uint8_t *>(ws), p.batch, z);
+    const int64_t bx = z.mp * z.np, ba = z.sp * z.sp;
+    const dim3 fgrid((unsigned)(z.mp / 128), (unsigned)(z.np / 128), (unsigned)p.batch);
     e = p.f32 ? launch(first_kernel<true>, fgrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, vec, s.part, parts, p.eps,
                        s.hi[0], s.lo, s.turned[0], z.mp, z.np, bx)
               : launch(first_kernel<false>, fgrid, dim3(256), 0, stream, p.g, p.m, p.n, p.ldg, p.batch_g, vec, s.part, parts, p.eps,

@@ -1,5 +1,6 @@
-"""How far the Newton-Schulz update may be from its steps in 64 bits: small sides, whose few roundings do not average out, and
-one or a few strong directions over weak noise, where what the shifted polynomial adds to the noise's directions grows."""
+"""How far the Newton-Schulz update with FP16 operands may be from its steps in 64 bits: the smallest sides that take them, whose
+roundings average least, and one or a few strong directions over weak noise, where what the shifted polynomial adds to the
+noise's directions grows."""
 import pytest
 import torch
 
@@ -53,21 +54,20 @@ def spread(g, draws=200):
 STRONG = (OWN ** 2 + (SHIFT * 2.0 ** -12) ** 2 * ((1.60 * A * A / 4) ** 2 + (1.03 * A / 2) ** 2 + 1.57 ** 2)) ** 0.5
 
 
-@pytest.mark.parametrize("m,n", [(1, 1), (1, 3), (1, 5000), (2, 2), (3, 5), (5, 3), (4, 64), (5, 5), (3, 2000), (8, 8), (7, 9), (300, 8),
-                                 (12, 64), (15, 15), (15, 2000)])
+@pytest.mark.parametrize("m,n", [(65, 65), (65, 1000), (300, 70), (90, 128), (128, 700)])
 @pytest.mark.parametrize("kind", ["normal", "heavy", "strong"])
-def test_small_sides(m, n, kind):
+def test_smallest_sides(m, n, kind):
     """Within three times the root mean square: the roundings of a few numbers are bounded (the largest is 3 ** 0.5 times the
     root mean square of its range), and independent."""
     mx = _mx()
-    announce("orthogonalize small side", m, n, kind)
-    for seed in range(10):
+    announce("orthogonalize smallest sides", m, n, kind)
+    for seed in range(3):
         g = _grad(m, n, kind, 1000 * seed)
         got = mx.orthogonalize(g.cuda(), out_dtype=torch.float32)
-        assert _rel(got, ref.newton_schulz(g, 5, COEFFS, 1e-7)) <= 3.0 * spread(g), seed
+        assert _rel(got, ref.newton_schulz(g, 5, COEFFS, 1e-7)) <= 3.0 * spread(g, 20), seed
 
 
-@pytest.mark.parametrize("m,n", [(16, 300), (64, 64), (300, 64), (256, 512), (500, 900), (1000, 1500)])
+@pytest.mark.parametrize("m,n", [(65, 300), (300, 96), (128, 128), (256, 512), (500, 900), (1000, 1500)])
 @pytest.mark.parametrize("noise", [1e-1, 1e-2, 1e-3, 1e-4, 1e-5, 0.0])
 @pytest.mark.parametrize("few", [False, True])
 def test_strong_directions_over_noise(m, n, noise, few):
