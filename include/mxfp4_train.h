@@ -155,8 +155,8 @@ mxfp4_status_t mxfp4_linear_xent_backward(const float *dloss, const float *dlse,
  * elements apart; out: FP32 or bf16 with ldo and batch_stride_o; out may be read only when beta != 0
  * and must not overlap g. With a side of at most 64 everything is held in FP32; five steps
  * are off by 1e-6 to 1e-4 of the result's norm. Larger matrices' products take FP16 operands and accumulate
- * in FP32, X is carried in 22 bits: five steps are off by 0.0003 to 0.002, and by up to 0.0033 where one or a
- * few directions stand 1000 times and more above the rest. A bf16 result's own rounding is 0.0017.
+ * in FP32, X is carried in 22 bits: five steps are off by 0.0003 to 0.0018. A bf16 result's own rounding is
+ * 0.0017.
  * A matrix that holds a NaN or an infinity gives NaN (that matrix only).
  * Coefficients: finite, and such that singular values that start in [0, 1] stay within 4 and |b x + c x x|
  * within 32 for their squares x at every step (MXFP4_ERR_ARG otherwise: FP16 would overflow);

@@ -16,11 +16,11 @@
 // of the X that it is multiplied by count |b + c| times (2.7). A step may as well be (a - t) X +
 // (b A + c A A + t) X: with t = -(b + c) they count next to nothing there, but t times for the directions that
 // are still small, and what those pick up grows with them in the steps that follow. So the last step takes
-// t = -(b + c), the two before it a half and a quarter of it, and the others none. Relative error in five steps,
-// heavy tails (100 x 1000 to 1000 x 1500): 0.0007 to 0.0013, without t 0.0014 to 0.0029. One strong direction over noise
-// gains from no t (0.0004) and pays for it: 0.0005 over noise of 1/100, 0.0026 over 1/1000, 0.0032 over less, where the
-// noise's directions hold little but those roundings; with t = -(b + c) in every step 0.03. A bf16 result's own rounding is
-// 0.0017. Matrices with a side of at most 64 are worked in FP32 (below).
+// t = -(b + c), the one before it a half of it, and the others none. Relative error in five steps,
+// sides of 65 to 2048: heavy tails 0.0008 to 0.0017, without t 0.0012 to 0.0020; one strong direction over noise of 1/10
+// 0.0004, of 1/1000 0.0014, of less 0.0016 to 0.0018 (without t 0.0002 to 0.0007: the noise's directions then hold little but
+// these roundings). A quarter of t in the third last step as well: 0.0008 to 0.0014, but 0.0032 over little noise; t in every
+// step 0.03. A bf16 result's own rounding is 0.0017. Matrices with a side of at most 64 are worked in FP32 (below).
 //
 // Per step three launches: A (symmetric: the lower triangle of tiles, written twice), b A + c A A
 // (symmetric too), and the update, which writes X in both orientations for the next step's
@@ -680,7 +680,7 @@ hipError_t launch_ortho(const OrthoProblem &p, void *ws, hipStream_t stream)
     for (int k = 0; k < p.steps; ++k) {
         const uint16_t *x = s.hi[k & 1], *t = s.turned[k & 1];
         const int after = p.steps - 1 - k;
-        const float shift = after < 3 ? std::min(16.0f, std::max(-16.0f, -(p.b + p.c))) / (float)(1 << after) : 0.0f;
+        const float shift = after < 2 ? std::min(16.0f, std::max(-16.0f, -(p.b + p.c))) / (float)(1 << after) : 0.0f;
         Operands op{};
         // A: rows of X (wide) or of its transpose
         op.a = op.b = reinterpret_cast<const uint8_t *>(wide ? x : t);

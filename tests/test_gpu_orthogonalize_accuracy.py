@@ -10,8 +10,8 @@ from tests.test_gpu_orthogonalize import COEFFS, OWN, _grad, _rel
 
 pytestmark = pytest.mark.gpu
 A, B, C = COEFFS
-SHIFT = -(B + C)                 # of the last step; the two before take a half and a quarter of it, the others none
-SHIFTS = [0.0, 0.0, SHIFT / 4, SHIFT / 2, SHIFT]
+SHIFT = -(B + C)                 # of the last step; the one before takes a half of it, the others none
+SHIFTS = [0.0, 0.0, 0.0, SHIFT / 2, SHIFT]
 HALF = 2.0 ** -11                # half a step of the products' FP16 operands
 
 
@@ -49,9 +49,9 @@ def spread(g, draws=200):
 
 # One direction of singular value s near 1 over directions that are next to nothing: rounding X beside the shift t scatters
 # t 2^-12 |X| (root mean square) over all of those, and they grow by a = 3.44 in each step that follows. The strong value
-# goes 1 -> 0.70 -> 1.11 -> 0.72 -> 1.09 -> 0.70, so relative to the result the last three steps' roundings are 1.60, 1.03
-# and 1.57 of 2^-12; they are independent, of each other and of the others (OWN).
-STRONG = (OWN ** 2 + (SHIFT * 2.0 ** -12) ** 2 * ((1.60 * A * A / 4) ** 2 + (1.03 * A / 2) ** 2 + 1.57 ** 2)) ** 0.5
+# goes 1 -> 0.70 -> 1.11 -> 0.72 -> 1.09 -> 0.70, so relative to the result the last two steps' roundings are 1.03 and 1.57 of
+# 2^-12; they are independent, of each other and of the others (OWN).
+STRONG = (OWN ** 2 + (SHIFT * 2.0 ** -12) ** 2 * ((1.03 * A / 2) ** 2 + 1.57 ** 2)) ** 0.5
 
 
 @pytest.mark.parametrize("m,n", [(65, 65), (65, 1000), (300, 70), (90, 128), (128, 700)])
