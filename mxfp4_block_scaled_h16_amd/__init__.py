@@ -17,7 +17,7 @@ __all__ = [
     "Mxfp4Error", "RHT", "ORTHO", "SCALE_NOCLIP", "quantize", "quantize_dual", "gemm", "linear_fprop",
     "linear_dgrad", "linear_wgrad", "linear_forward", "linear_backward", "step_workspace_bytes", "workspace_bytes", "library_path", "lib", "RNE", "SR", "FPROP", "DGRAD", "WGRAD", "ROWS", "TILED",
     "tiled_sizes", "gemm_workspace_bytes", "linear_fprop_noalloc", "NOALLOC_SCRATCH_BYTES",
-]  # and those of train.py, below
+]  # and those of train.py and layer.py, below
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmxfp4.so")
@@ -530,3 +530,9 @@ from . import train as _train  # noqa: E402
 from .train import *  # noqa: E402,F401,F403
 
 __all__ += _train.__all__
+
+# RMS norm, gated activation and the gradients' norm (libmxfp4_layer.so)
+from . import layer as _layer  # noqa: E402
+from .layer import *  # noqa: E402,F401,F403
+
+__all__ += _layer.__all__

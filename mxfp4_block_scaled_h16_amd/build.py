@@ -1,6 +1,6 @@
 """Build the HIP libraries in-tree for gfx950 with hipcc: libmxfp4.so (the quantizers, GEMMs and
-C ABI), libmxfp4_train.so (8-bit products, the head's loss, the orthogonalised update) and
-libmxfp4_ceiling.so (the HBM and matrix-core ceiling kernels the benchmark reports)."""
+C ABI), libmxfp4_train.so (8-bit products, the head's loss, the orthogonalised update),
+libmxfp4_layer.so (RMS norm, gated activation, the gradients' norm) and libmxfp4_ceiling.so (the HBM and matrix-core ceiling kernels the benchmark reports)."""
 import os
 import shutil
 import subprocess
@@ -13,7 +13,11 @@ SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "noalloc.hip"]
 HEADERS = ["internal.h", "mx_device.h"]
 TRAIN_LIB = os.path.join(HERE, "libmxfp4_train.so")
 TRAIN_SOURCES = ["train_api.cpp", "fp8.hip", "xent.hip", "ortho.hip"]
-TRAIN_HEADERS = ["internal.h", "mx_device.h", "slab_gemm.h", "train_internal.h"]
+TRAIN_HEADERS = ["internal.h", "mx_device.h", "fp8_device.h", "host_checks.h", "slab_gemm.h", "train_internal.h"]
+LAYER_LIB = os.path.join(HERE, "libmxfp4_layer.so")
+LAYER_SOURCES = ["layer_api.cpp", "norm.hip", "gate.hip", "clip.hip"]
+LAYER_HEADERS = ["internal.h", "mx_device.h", "fp8_device.h", "host_checks.h", "layer_device.h", "layer_internal.h",
+                 "train_internal.h"]
 CEILING_LIB = os.path.join(HERE, "libmxfp4_ceiling.so")
 CEILING_SOURCES = ["ceiling.hip"]
 
@@ -64,6 +68,11 @@ def build(force: bool = True, verbose: bool = False) -> str:
     if force or not os.path.exists(TRAIN_LIB) or any(
             os.path.getmtime(f) > os.path.getmtime(TRAIN_LIB) for f in train_inputs):
         _compile(TRAIN_SOURCES, TRAIN_LIB, verbose)
+    layer_inputs = [os.path.join(CSRC, s) for s in LAYER_SOURCES + LAYER_HEADERS]
+    layer_inputs += [os.path.join(HERE, "..", "include", h) for h in ("mxfp4.h", "mxfp4_layer.h")]
+    if force or not os.path.exists(LAYER_LIB) or any(
+            os.path.getmtime(f) > os.path.getmtime(LAYER_LIB) for f in layer_inputs):
+        _compile(LAYER_SOURCES, LAYER_LIB, verbose)
     ceiling_inputs = [os.path.join(CSRC, s) for s in CEILING_SOURCES]
     ceiling_inputs.append(os.path.join(HERE, "..", "include", "mxfp4_ceiling.h"))
     if force or not os.path.exists(CEILING_LIB) or any(

@@ -1,0 +1,102 @@
+// The gated activation a = silu(g) u and its gradients, in 16 / 32 bits and as 8-bit codes along both axes.
+//
+//   s = 1 / (1 + exp(-g));  a = g s u
+//   du = da g s,  dg = da u s (1 + g (1 - s))
+//
+// One pass: a workgroup works a tile of 128 x 128 values, which holds whole blocks along both axes.
+#include "internal.h"
+#include "layer_device.h"
+
+namespace mx {
+namespace {
+
+// s and 1 - s, neither by cancellation: e = exp(-|g|) <= 1, s = 1 / (1 + e) or e / (1 + e). The exponent's rounding (|g| 2^-24 of e,
+// which is s where g is far below zero) is taken back in the first order. The hardware's exponential and reciprocal are
+// off by 2^-23 each, so s and 1 - s are by at most 7 * 2^-24; e below 2^-126 is zero.
+__device__ __forceinline__ void sigmoid(float g, float &s, float &t)
+{
+    constexpr float kLog2e = 1.44269504088896340736f, kRest = 1.9259629911266174681e-8f;   // log2(e) in two parts
+    const float x = fabsf(g), y = x * -kLog2e;
+    const float off = fmaf(x, -kRest, fmaf(x, -kLog2e, -y));
+    float e = __builtin_amdgcn_exp2f(y);
+    e = x < 126.0f ? fmaf(e, off * 0.69314718055994530942f, e) : 0.0f;
+    const float r = __builtin_amdgcn_rcpf(1.0f + e), q = e * r;
+    s = g >= 0.0f ? r : q;
+    t = g >= 0.0f ? q : r;
+}
+
+// GRAD: the gradients, from da; DF32: da's type. F32: that of g and u.
+template <bool GRAD, bool DF32, bool F32, bool RAGGED>
+__global__ __launch_bounds__(512) void gate_kernel(Gate p, int tiles_n)
+{
+    __shared__ TileShared<4> sh;
+    const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
+    const int64_t tm = blockIdx.x / (unsigned)tiles_n, tn = blockIdx.x % (unsigned)tiles_n;
+    const int64_t row0 = tm * 128 + 4 * rg, col0 = tn * 128 + 8 * cg;
+    Raw8<F32> g[4], u[4];
+    Raw8<DF32> d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t row = row0 + i;
+        g[i].zero();
+        u[i].zero();
+        d[i].zero();
+        if (row >= p.rows) continue;
+        g[i] = load_raw<F32, RAGGED>(at<F32>(p.g.p, row * p.g.ld), col0, p.cols);
+        u[i] = load_raw<F32, RAGGED>(at<F32>(p.u.p, row * p.u.ld), col0, p.cols);
+        if constexpr (GRAD) d[i] = load_raw<DF32, RAGGED>(at<DF32>(p.da.p, row * p.da.ld), col0, p.cols);
+    }
+    float v[GRAD ? 2 : 1][4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a[8], b[8], c[8];
+        g[i].get(a);
+        u[i].get(b);
+        if constexpr (GRAD) d[i].get(c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float s, t;
+            sigmoid(a[e], s, t);
+            if constexpr (GRAD) {
+                v[0][i][e] = c[e] * b[e] * (s * fmaf(a[e], t, 1.0f));
+                v[1][i][e] = c[e] * (a[e] * s);
+            } else {
+                v[0][i][e] = a[e] * s * b[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < (GRAD ? 2 : 1); ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = row0 + i;
+            if (row >= p.rows) break;
+            if (p.out[k].p)
+                store_any<RAGGED>(p.out_f32, v[k][i],
+                                  p.out_f32 ? at<true>(p.out[k].p, row * p.out[k].ld) : at<false>(p.out[k].p, row * p.out[k].ld),
+                                  col0, p.cols);
+            if (p.q1[k].q) store_row_codes(p.q1[k], row, col0, p.cols, v[k][i]);
+        }
+        if (p.q0[k].q) store_tile_columns<4>(p.q0[k], tm, tn, p.cols, v[k], sh);
+    }
+}
+
+template <bool GRAD, bool DF32, bool F32>
+hipError_t run(const Gate &p, hipStream_t stream)
+{
+    const int64_t tiles_n = (p.cols + 127) / 128;
+    const dim3 grid((unsigned)((p.rows + 127) / 128 * tiles_n)), block(512);
+    return p.cols % 8 ? launch(gate_kernel<GRAD, DF32, F32, true>, grid, block, 0, stream, p, (int)tiles_n)
+                      : launch(gate_kernel<GRAD, DF32, F32, false>, grid, block, 0, stream, p, (int)tiles_n);
+}
+
+}  // namespace
+
+hipError_t launch_gate(const Gate &p, hipStream_t stream)
+{
+    if (!p.da.p) return p.f32 ? run<false, true, true>(p, stream) : run<false, false, false>(p, stream);
+    if (p.da_f32) return p.f32 ? run<true, true, true>(p, stream) : run<true, true, false>(p, stream);
+    return p.f32 ? run<true, false, true>(p, stream) : run<true, false, false>(p, stream);
+}
+
+}  // namespace mx

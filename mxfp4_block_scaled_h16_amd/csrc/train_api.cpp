@@ -2,13 +2,12 @@
 // Every argument check happens before the first HIP call, so an invalid call launches nothing,
 // touches no output and needs no device.
 #include <algorithm>
-#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
-#include <cstring>
 
 #include "../../include/mxfp4_train.h"
+#include "host_checks.h"
 #include "train_internal.h"
 
 namespace {
@@ -16,40 +15,9 @@ namespace {
 constexpr int64_t kMaxDim = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxLinear = (int64_t)1 << 23;
 
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-mxfp4_status_t check_device()
-{
-    // gfx950 check, cached per device ordinal: 0 = unknown, 1 = gfx950, 2 = other
-    static std::atomic<int> cache[64];
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return MXFP4_ERR_DEVICE;
-    if (dev < 64) {
-        const int known = cache[dev].load(std::memory_order_relaxed);
-        if (known) return known == 1 ? MXFP4_OK : MXFP4_ERR_DEVICE;
-    }
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return MXFP4_ERR_DEVICE;
-    const bool ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    if (dev < 64) cache[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
-    return ok ? MXFP4_OK : MXFP4_ERR_DEVICE;
-}
-
-mxfp4_status_t from_hip(hipError_t e) { return e == hipSuccess ? MXFP4_OK : MXFP4_ERR_LAUNCH; }
-
-bool valid_out(int t) { return t == MXFP4_OUT_F32 || t == MXFP4_OUT_BF16; }
-size_t out_size(int t) { return t == MXFP4_OUT_BF16 ? 2 : 4; }
-bool in_range(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
+using mx::aligned, mx::check_device, mx::check_fp8_out, mx::from_hip, mx::in_range, mx::out_size, mx::valid_out;
 
 int64_t fp8_tiles(int64_t rows, int64_t cols) { return (rows + 127) / 128 * ((cols + 127) / 128); }
-
-mxfp4_status_t check_fp8_out(const uint8_t *q, int64_t ldq, const uint8_t *s, int64_t lds, int64_t L)
-{
-    if (ldq < mx::round_up(L, 128) || lds < (L + 127) / 128 || lds < 1) return MXFP4_ERR_ARG;
-    if (!s) return MXFP4_ERR_NULL;
-    if (!aligned(q, 16) || ldq % 16 != 0) return MXFP4_ERR_ALIGN;
-    return MXFP4_OK;
-}
 
 // Quantized operand of a linear call in the workspace.
 struct Operand {

@@ -1,0 +1,157 @@
+"""The gated activation on the GPU, forward and backward, against the formulas in 64 bits; the 8-bit outputs bit for bit."""
+import pytest
+import torch
+
+from tests.gpu_util import announce, require_gpu
+from tests.layer_util import BF, F32, HALF, TINY, assert_within, check_axes, check_codes, gate_backward, gate_forward, heavy
+
+pytestmark = pytest.mark.gpu
+SIZES = [(1, 1), (1, 14336), (3, 7), (128, 128), (5, 129), (130, 384), (257, 1000), (129, 2001), (2, 256)]
+OWN = 2.0 ** -20
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _mx():
+    import mxfp4_block_scaled_h16_amd as mx
+    return mx
+
+
+def _data(rows, cols, dtype, spread=2.0):
+    g = torch.Generator().manual_seed(rows * 13 + cols)
+    gate, up = spread * torch.randn(rows, cols, generator=g), torch.randn(rows, cols, generator=g)
+    gate.view(-1)[::11] *= 20                        # far tails of the exponential
+    return gate.to(dtype), up.to(dtype), heavy((rows, cols), rows + cols, 1e-3)
+
+
+def _tol(exact, basis, dtype, factor):
+    """factor: what s is multiplied with. s below 2^-126 may be lost (exp(-|g|) counts as zero there), which the product makes
+    2^-126 |factor|: with g = -90 and u = 2 that is 180 * 2^-126, of a value of 7e-38 = 8 * 2^-126 and less."""
+    tol = OWN * basis + TINY * (1 + factor.double().abs())
+    return tol + (HALF[dtype] * (exact.abs() + tol) if dtype == BF else 0.0)
+
+
+@pytest.mark.parametrize("rows,cols", SIZES)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_forward(rows, cols, dtype):
+    mx = _mx()
+    gate, up, _ = _data(rows, cols, dtype)
+    announce("gate forward", rows, cols, dtype)
+    exact = gate_forward(gate, up)
+    for axis, out in ((None, BF), ("both", F32), (1, F32), (0, F32)):
+        o = mx.swiglu_forward(gate.cuda(), up.cuda(), axis=axis, out_dtype=out)
+        assert_within(o.a, exact, _tol(exact, exact.abs(), out, gate.double() * up.double()), "a")
+        if out == F32:
+            check_axes(o, o.a.cpu(), axis)              # the codes are those of the FP32 values
+            full = o
+    o = mx.swiglu_forward(gate.cuda(), up.cuda(), axis="both", out_dtype=None)
+    assert o.a is None
+    check_axes(o, full.a.cpu(), "both")
+    assert torch.equal(mx.swiglu_forward(gate.cuda(), up.cuda()).a, full.a.to(BF))
+
+
+@pytest.mark.parametrize("rows,cols", SIZES)
+@pytest.mark.parametrize("dtype,dtype_a", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
+def test_backward(rows, cols, dtype, dtype_a):
+    mx = _mx()
+    gate, up, da = _data(rows, cols, dtype)
+    da = da.to(dtype_a)
+    dg, du, basis = gate_backward(da, gate, up)
+    dev = da.cuda(), gate.cuda(), up.cuda()
+    announce("gate backward", rows, cols, dtype, dtype_a)
+    o = mx.swiglu_backward(*dev, axis="both", out_dtype=F32, joined=False)
+    assert_within(o.dgate, dg, _tol(dg, basis, F32, da.double() * up.double() * (1 + gate.double().abs())), "dgate")
+    assert_within(o.dup, du, _tol(du, du.abs(), F32, da.double() * gate.double()), "dup")
+    check_axes(o.gate, o.dgate.cpu(), "both", "dgate")
+    check_axes(o.up, o.dup.cpu(), "both", "dup")
+    wide = torch.cat([o.dgate, o.dup], dim=1).cpu()
+    b = mx.swiglu_backward(*dev)
+    assert torch.equal(b.dgate, o.dgate.to(BF)) and torch.equal(b.dup, o.dup.to(BF)) and b.q1 is None
+    assert b.dgate.stride(0) == 2 * cols or rows == 1
+    # as one operand of 2 F: columns with any F, rows with whole blocks
+    j = mx.swiglu_backward(*dev, axis="both" if cols % 128 == 0 else 0, out_dtype=None)
+    assert j.dgate is None
+    check_codes(j.q0, j.s0, wide.t().contiguous(), "columns of both")
+    if cols % 128 == 0:
+        check_codes(j.q1, j.s1, wide, "rows of both")
+
+
+def test_halves_strides_and_in_place():
+    mx = _mx()
+    for rows, cols in ((200, 384), (30, 1001)):
+        gate, up, da = _data(rows, cols, BF)
+        da = da.to(BF)
+        announce("gate strides", rows, cols)
+        base, grad = mx.swiglu_forward(gate.cuda(), up.cuda()), mx.swiglu_backward(da.cuda(), gate.cuda(), up.cuda())
+        both = torch.cat([gate, up], dim=1).cuda()
+        g, u = both[:, :cols], both[:, cols:]
+        wide = torch.zeros(rows, cols + 9, dtype=BF).cuda()
+        a = mx.swiglu_forward(g, u, a=wide[:, 3:3 + cols]).a
+        assert torch.equal(a, base.a) and not bool(wide[:, :3].any()) and not bool(wide[:, 3 + cols:].any())
+        off = torch.zeros(rows, cols + 1, dtype=BF).cuda()[:, 1:]
+        off.copy_(da)
+        got = mx.swiglu_backward(off, g, u)
+        assert torch.equal(got.dgate, grad.dgate) and torch.equal(got.dup, grad.dup)
+        d = both.clone()
+        got = mx.swiglu_backward(off, d[:, :cols], d[:, cols:], dgate=d[:, :cols], dup=d[:, cols:])        # over gate and up
+        assert torch.equal(got.dgate, grad.dgate) and torch.equal(d[:, cols:], grad.dup)
+        d = both.clone()
+        got = mx.swiglu_backward(off, d[:, :cols], d[:, cols:], dgate=off, dup=d[:, :cols])                 # over da and gate
+        assert torch.equal(off, grad.dgate) and torch.equal(d[:, :cols], grad.dup)
+        for k in (0, 1):
+            d = both.clone()
+            mx.swiglu_forward(d[:, :cols], d[:, cols:], a=(d[:, :cols], d[:, cols:])[k])
+            assert torch.equal((d[:, :cols], d[:, cols:])[k], base.a)
+
+
+def test_empty():
+    mx = _mx()
+    for shape in ((0, 300), (5, 0)):
+        z = torch.zeros(*shape, dtype=BF).cuda()
+        o = mx.swiglu_forward(z, z, axis="both")
+        assert o.a.shape == shape
+        mx.swiglu_backward(z, z, z, axis="both", joined=False)
+
+
+def test_ends_of_the_range():
+    """Gates from far below to far above zero, infinities and NaN."""
+    mx = _mx()
+    gate = torch.cat([torch.linspace(-130, 130, 2048), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 2e38, -2e38, 80.0, -80.0])])[None]
+    up = torch.ones_like(gate) * 1.5
+    exact = gate_forward(gate, up)
+    announce("gate ends")
+    o = mx.swiglu_forward(gate.cuda(), up.cuda(), out_dtype=F32)
+    # exp(-|g|) that is lost at its end is below 2^-126: times |g u|
+    lost = 2.0 ** -126 * (gate.double() * up.double()).abs()
+    assert_within(o.a, exact, OWN * exact.abs() + lost + 2.0 ** -149)
+    da = torch.full_like(gate, 0.75)
+    dg, du, basis = gate_backward(da, gate, up)
+    b = mx.swiglu_backward(da.cuda(), gate.cuda(), up.cuda(), out_dtype=F32)
+    assert_within(b.dgate, dg, OWN * basis + lost + 2.0 ** -126 + 2.0 ** -149)
+    assert_within(b.dup, du, OWN * du.abs() + lost + 2.0 ** -149)
+    inf, nan = float("inf"), float("nan")
+    gate, up = torch.tensor([[inf, nan, 1.0, 1.0, 2.0]]), torch.tensor([[1.0, 1.0, inf, nan, 3.0]])
+    a = mx.swiglu_forward(gate.cuda(), up.cuda(), axis="both", out_dtype=F32)
+    assert float(a.a[0, 0]) == inf and float(a.a[0, 2]) == inf and bool(torch.isnan(a.a[0, 1])) and bool(torch.isnan(a.a[0, 3]))
+    assert int(a.s1[0, 0]) == 255 and a.s0[:5, 0].cpu().tolist()[:4] == [255] * 4 and int(a.s0[4, 0]) != 255
+    assert not bool(a.q1.any())
+
+
+def test_backward_against_differences():
+    mx = _mx()
+    g = torch.Generator().manual_seed(3)
+    r = lambda: torch.randn(40, 100, generator=g).cuda()  # noqa: E731
+    gate, up, c = 2 * r(), r(), r()
+    value = lambda p, q: float((mx.swiglu_forward(p, q, out_dtype=F32).a.double() * c.double()).sum())  # noqa: E731
+    got = mx.swiglu_backward(c, gate, up, out_dtype=F32)
+    step = 2.0 ** -7
+    for _ in range(4):
+        p, q = r(), r()
+        slope = (value(gate + step * p, up + step * q) - value(gate - step * p, up - step * q)) / (2 * step)
+        want = float((got.dgate.double() * p.double()).sum() + (got.dup.double() * q.double()).sum())
+        # 4000 outputs of about two, each off by 2^-20 (in the root mean square far less), over 2 step; third
+        # derivatives of silu are at most one half: 4000 random terms of that size, times step^2 / 6
+        assert abs(slope - want) <= 4000 * 2.0 ** -20 / (2 * step) + 10 * 4000 ** 0.5 * step ** 2 / 6
