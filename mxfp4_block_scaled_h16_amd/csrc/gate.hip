@@ -4,32 +4,28 @@
 //   du = da g s,  dg = da u s (1 + g (1 - s))
 //
 // One pass: a workgroup works a tile of 128 x 128 values, which holds whole blocks along both axes.
+#include <cfloat>
+
 #include "internal.h"
 #include "layer_device.h"
 
 namespace mx {
 namespace {
 
-// s and 1 - s, neither by cancellation: e = exp(-|g|) <= 1, s = 1 / (1 + e) or e / (1 + e). The exponent's rounding (|g| 2^-24 of e,
-// which is s where g is far below zero) is taken back in the first order. The hardware's exponential and reciprocal are
-// off by 2^-23 each, so s and 1 - s are by at most 7 * 2^-24; e below 2^-126 is zero.
-__device__ __forceinline__ void sigmoid(float g, float &s, float &t)
+// s = 1 / (1 + e) and 1 - s = e s, e = exp(-g). The hardware's exponential and reciprocal are off by 2^-23 each, and the
+// exponent's rounding, |g| 2^-24, is one of e: s and 1 - s are off by at most (8 + 1.3 |g|) 2^-24 of themselves, the larger of the
+// two by far less. Below g = -88 e is infinite and s zero, where it is below 2^-126 (1 - s is multiplied with it).
+__device__ __forceinline__ float sigmoid(float g, float &e)
 {
-    constexpr float kLog2e = 1.44269504088896340736f, kRest = 1.9259629911266174681e-8f;   // log2(e) in two parts
-    const float x = fabsf(g), y = x * -kLog2e;
-    const float off = fmaf(x, -kRest, fmaf(x, -kLog2e, -y));
-    float e = __builtin_amdgcn_exp2f(y);
-    e = x < 126.0f ? fmaf(e, off * 0.69314718055994530942f, e) : 0.0f;
-    const float r = __builtin_amdgcn_rcpf(1.0f + e), q = e * r;
-    s = g >= 0.0f ? r : q;
-    t = g >= 0.0f ? q : r;
+    e = __builtin_amdgcn_exp2f(g * -1.44269504088896340736f);
+    return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 // GRAD: the gradients, from da; DF32: da's type. F32: that of g and u.
 template <bool GRAD, bool DF32, bool F32, bool RAGGED>
-__global__ __launch_bounds__(512) void gate_kernel(Gate p, int tiles_n)
+__global__ __launch_bounds__(512, 4) void gate_kernel(Gate p, int tiles_n)
 {
-    __shared__ TileShared<4> sh;
+    __shared__ TileShared sh;
     const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
     const int64_t tm = blockIdx.x / (unsigned)tiles_n, tn = blockIdx.x % (unsigned)tiles_n;
     const int64_t row0 = tm * 128 + 4 * rg, col0 = tn * 128 + 8 * cg;
@@ -55,11 +51,14 @@ __global__ __launch_bounds__(512) void gate_kernel(Gate p, int tiles_n)
         if constexpr (GRAD) d[i].get(c);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float s, t;
-            sigmoid(a[e], s, t);
+            float x;
+            const float s = sigmoid(a[e], x);
             if constexpr (GRAD) {
+                const float t = fminf(x, FLT_MAX) * s;
                 v[0][i][e] = c[e] * b[e] * (s * fmaf(a[e], t, 1.0f));
                 v[1][i][e] = c[e] * (a[e] * s);
+                // both now, while the inputs leave their registers: formed where they are used, they hold 186 instead
+                asm volatile("" : "+v"(v[1][i][e]));
             } else {
                 v[0][i][e] = a[e] * s * b[e];
             }
@@ -77,7 +76,7 @@ __global__ __launch_bounds__(512) void gate_kernel(Gate p, int tiles_n)
                                   col0, p.cols);
             if (p.q1[k].q) store_row_codes(p.q1[k], row, col0, p.cols, v[k][i]);
         }
-        if (p.q0[k].q) store_tile_columns<4>(p.q0[k], tm, tn, p.cols, v[k], sh);
+        if (p.q0[k].q) store_tile_columns(p.q0[k], tm, tn, p.cols, v[k], sh);
     }
 }
 

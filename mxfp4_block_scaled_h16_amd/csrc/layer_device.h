@@ -166,92 +166,123 @@ __device__ __forceinline__ T wave_sum(T v)
 }
 
 // ---------------------------------------------------------------------------- 8-bit outputs ---
+// Bit pattern of the largest of N magnitudes, that of a NaN if one is (v_maximum3_f32 takes two more values at a time and keeps
+// NaN, where comparing bit patterns needs the sign off each first).
+template <int N>
+__device__ __forceinline__ uint32_t largest(const float (&v)[N])
+{
+    float m = fabsf(v[0]);
+#pragma unroll
+    for (int i = 1; i < N; ++i) m = __builtin_elementwise_maximum(m, fabsf(v[i]));
+    return __float_as_uint(m);
+}
+
+// Scale bytes that the conversion below does not take: 0 (2^-127, which FP32 does not hold as a normal number) and 0xFF
+// (no number). Blocks of zeros, of tiny values, and those that hold a NaN or an infinity.
+__device__ __forceinline__ bool special(uint32_t s) { return s - 1u > 253u; }
+
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+
+// Four values over 2^(S - 127), S in [1, 247], as E4M3 codes, rounded to nearest even; the quotient is at most 448. One
+// instruction divides and rounds two of them, where encode4 multiplies each first.
+__device__ __forceinline__ uint32_t divide4(float a, float b, float c, float d, float scale)
+{
+    i16x2 w = {0, 0};
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
+    return __builtin_bit_cast(uint32_t, w);
+}
+// The same with any S: codes 0 for 0xFF.
+__device__ __forceinline__ uint32_t divide4_any(float a, float b, float c, float d, uint32_t s)
+{
+    return s == 0xFFu ? 0u : encode4(a, b, c, d, inverse_scale(s));
+}
+
 // Eight values of a row in each of 16 lanes side by side, which are one block (col a multiple of 8, the block's
 // first lane at a multiple of 128): its codes, zeros behind the row's end up to the block's, and its scale.
 __device__ __forceinline__ void store_row_codes(const Fp8Out &out, int64_t row, int64_t col, int64_t cols, const float (&v)[8])
 {
-    const uint32_t s = e8m0_of(row16_max(amax_bits<8>(v)));
-    const float inv = inverse_scale(s == 0xFFu ? 0u : s);
-    u32x2 w = {0u, 0u};
-    if (s != 0xFFu) w = u32x2{encode4(v[0], v[1], v[2], v[3], inv), encode4(v[4], v[5], v[6], v[7], inv)};
+    const uint32_t s = e8m0_of(row16_max(largest(v)) & 0x7FFFFFFFu);
+    u32x2 w;
+    if (__any(special(s))) {
+        w = u32x2{divide4_any(v[0], v[1], v[2], v[3], s), divide4_any(v[4], v[5], v[6], v[7], s)};
+    } else {
+        const float scale = __uint_as_float(s << 23);
+        w = u32x2{divide4(v[0], v[1], v[2], v[3], scale), divide4(v[4], v[5], v[6], v[7], scale)};
+    }
     if ((col & ~(int64_t)127) >= cols) return;
     *reinterpret_cast<u32x2 *>(out.q + row * out.ldq + col) = w;
     if ((col & 127) == 0) out.s[row * out.lds + (col >> 7)] = (uint8_t)s;
 }
 
-// A tile of 128 x 128 values in 16 * 128 / N threads of N x 8: thread t has rows N (t / 16) .. and columns
-// 8 (t % 16) .. . Along the columns a block is a column of the tile: its maximum joins the four row groups of
-// a wavefront by lane swaps and the wavefronts through the LDS, which also turns the codes.
-template <int N>
+// A tile of 128 x 128 values in 512 threads of 4 x 8: thread t has rows 4 (t / 16) .. and columns 8 (t % 16) .. .
+// Along the columns a block is a column of the tile: its maximum joins the four row groups of a wavefront by
+// lane swaps and the wavefronts through the LDS, which also turns the codes.
 struct TileShared {
-    static constexpr int kWaves = 16 * 128 / N / 64;
-    uint32_t cmax[kWaves][128];
-    uint32_t scale[128];
+    uint32_t top[8][128];
+    uint32_t scale[128];      // scale bytes as FP32's exponents
+    uint32_t special[2];
     // a column's 128 codes, in 16-byte chunks permuted by the column's bits 3-5 against bank conflicts
     __attribute__((aligned(16))) uint8_t turned[128 * 128];
 };
 
-__device__ __forceinline__ uint32_t rows_max(uint32_t v)
-{
-    auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = max(r[0], r[1]);
-    r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return max(r[0], r[1]);
-}
-
-// tm, tn: the tile's place. Values behind the matrix' ends are zeros. Every thread of the workgroup calls it; `sh` may be
-// used again after the next barrier.
-template <int N>
+// tm, tn: the tile's place. Values behind the matrix' ends are zeros. Every thread of the workgroup calls it, and may do so
+// again at once: what a call still reads behind its last barrier, the next one writes behind its first.
 __device__ __forceinline__ void store_tile_columns(const Fp8Out &out, int64_t tm, int64_t tn, int64_t cols,
-                                                   const float (&v)[N][8], TileShared<N> &sh)
+                                                   const float (&v)[4][8], TileShared &sh)
 {
-    constexpr int kThreads = 16 * 128 / N;
     const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
     uint32_t m[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        m[j] = 0u;
+        const float column[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
+        m[j] = largest(column);
+    }
+    // Lanes 16 further have the next four rows of the same columns. A swap of the odd groups of 16 lanes of one register with
+    // the even ones of another leaves both groups' maxima of one column beside each other, and another column's in the other
+    // group; so does one of the wavefront's halves. A lane ends with two columns' maxima over 16 rows.
 #pragma unroll
-        for (int i = 0; i < N; ++i) m[j] = max(m[j], abs_bits(v[i][j]));
-        m[j] = rows_max(m[j]);
+    for (int j = 0; j < 4; ++j) {
+        const auto r = __builtin_amdgcn_permlane16_swap(m[j], m[j + 4], false, false);
+        m[j] = max(r[0], r[1]);
     }
-    if ((tid & 48) == 0) {
-        u32x4 *to = reinterpret_cast<u32x4 *>(&sh.cmax[tid >> 6][8 * cg]);
-        to[0] = u32x4{m[0], m[1], m[2], m[3]};
-        to[1] = u32x4{m[4], m[5], m[6], m[7]};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const auto r = __builtin_amdgcn_permlane32_swap(m[j], m[j + 2], false, false);
+        m[j] = max(r[0], r[1]);
     }
+    *reinterpret_cast<u32x2 *>(&sh.top[tid >> 6][8 * cg + 4 * (rg & 1) + (rg & 2)]) = u32x2{m[0], m[1]};
     __syncthreads();
     if (tid < 128) {
-        uint32_t top = sh.cmax[0][tid];
+        uint32_t top = sh.top[0][tid];
 #pragma unroll
-        for (int i = 1; i < TileShared<N>::kWaves; ++i) top = max(top, sh.cmax[i][tid]);
-        sh.scale[tid] = e8m0_of(top);
+        for (int i = 1; i < 8; ++i) top = max(top, sh.top[i][tid]);
+        const uint32_t s = e8m0_of(top & 0x7FFFFFFFu);
+        sh.scale[tid] = s << 23;
+        const bool any = __any(special(s));
+        if ((tid & 63) == 0) sh.special[tid >> 6] = any ? 1u : 0u;
     }
     __syncthreads();
+    // four codes from row 4 rg on: bytes 4 (rg % 4) of chunk rg / 4 of the column
+    uint8_t *to = sh.turned + 8 * cg * 128 + 16 * ((rg >> 2) ^ (cg & 7)) + 4 * (rg & 3);
+    const u32x4 s0 = *reinterpret_cast<const u32x4 *>(sh.scale + 8 * cg), s1 = *reinterpret_cast<const u32x4 *>(sh.scale + 8 * cg + 4);
+    const bool slow = (sh.special[0] | sh.special[1]) != 0u;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int col = 8 * cg + j;
-        const uint32_t s = sh.scale[col];
-        const float inv = inverse_scale(s == 0xFFu ? 0u : s);
-        // N codes from row N rg on: chunk (N rg) / 16 of the column
-        uint8_t *to = sh.turned + col * 128 + 16 * (((N * rg) >> 4) ^ (cg & 7)) + ((N * rg) & 15);
-        if constexpr (N == 8)
-            *reinterpret_cast<u32x2 *>(to) = s == 0xFFu ? u32x2{0u, 0u}
-                                                        : u32x2{encode4(v[0][j], v[1][j], v[2][j], v[3][j], inv),
-                                                                encode4(v[4][j], v[5][j], v[6][j], v[7][j], inv)};
-        else
-            *reinterpret_cast<uint32_t *>(to) = s == 0xFFu ? 0u : encode4(v[0][j], v[1][j], v[2][j], v[3][j], inv);
+        const uint32_t s = j < 4 ? s0[j & 3] : s1[j & 3];
+        *reinterpret_cast<uint32_t *>(to + j * 128) = slow ? divide4_any(v[0][j], v[1][j], v[2][j], v[3][j], s >> 23)
+                                                           : divide4(v[0][j], v[1][j], v[2][j], v[3][j], __uint_as_float(s));
     }
     __syncthreads();
     // eight lanes write a column's 128 bytes
 #pragma unroll
-    for (int p = 0; p < 1024 / kThreads; ++p) {
-        const int col = (kThreads / 8) * p + (tid >> 3), chunk = tid & 7;
+    for (int p = 0; p < 2; ++p) {
+        const int col = 64 * p + (tid >> 3), chunk = tid & 7;
         const int64_t outer = tn * 128 + col;
         if (outer >= cols) continue;
         *reinterpret_cast<u32x4 *>(out.q + outer * out.ldq + tm * 128 + 16 * chunk) =
             *reinterpret_cast<const u32x4 *>(sh.turned + col * 128 + 16 * (chunk ^ ((col >> 3) & 7)));
-        if (chunk == 0) out.s[outer * out.lds + tm] = (uint8_t)sh.scale[col];
+        if (chunk == 0) out.s[outer * out.lds + tm] = (uint8_t)(sh.scale[col] >> 23);
     }
 }
 

@@ -172,7 +172,7 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(ForwardArgs arg
 template <bool SF32, bool RAGGED>
 __global__ __launch_bounds__(512) void norm_columns_kernel(NormForward p, Rows h, int tiles_n)
 {
-    __shared__ TileShared<4> sh;
+    __shared__ TileShared sh;
     const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
     const int64_t tm = blockIdx.x / (unsigned)tiles_n, tn = blockIdx.x % (unsigned)tiles_n;
     const int64_t row0 = tm * 128 + 4 * rg, col0 = tn * 128 + 8 * cg;
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(512) void norm_columns_kernel(NormForward p, Rows h
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] = row0 + i < p.rows ? v[i][e] * rstd[i] * w[e] : 0.0f;
     }
-    store_tile_columns<4>(p.q0, tm, tn, p.cols, v, sh);
+    store_tile_columns(p.q0, tm, tn, p.cols, v, sh);
 }
 
 template <bool XF32, bool SF32, bool RES, bool RAGGED, int TPR, int C>

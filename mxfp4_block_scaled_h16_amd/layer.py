@@ -14,12 +14,13 @@ zero codes behind L; s: uint8 [outer, round_up(ceil(L / 128), 16)], ceil(L / 128
 import array
 import ctypes
 import functools
+import operator
 import os
 from typing import NamedTuple, Optional
 
 import torch  # imported first: the library binds to the HIP runtime torch has loaded
 
-from .train import _bytes, _check, _current, _fp8_buffers, _on, _room, _rows, _same_device, _IN, _OUT
+from .train import _bytes, _check, _current, _on, _room, _rows, _same_device, _IN, _OUT
 
 __all__ = [
     "rmsnorm_forward", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes", "swiglu_forward", "swiglu_backward", "grad_norm",
@@ -107,34 +108,67 @@ def layer_lib():
     return L
 
 
+# A call's host time is what a small call takes in all: tensors are looked at once, with the cheapest question that settles the
+# usual case (a contiguous matrix on the first tensor's device), and sizes are given to torch.empty one by one, which takes
+# half the time of a tuple.
 _FLOATS = (torch.bfloat16, torch.float32)
-_AXES = (None, 0, 1, "both")
+_U8 = torch.uint8
+_empty = torch.empty
 
 
-def _axis(axis):
-    """(along the rows, along the columns)"""
-    if axis not in _AXES:
-        raise ValueError("axis must be None, 0, 1 or 'both'")
-    return axis in (1, "both"), axis in (0, "both")
+def _device(names, first, *others):
+    """The HIP device that all these tensors (None left out) lie on."""
+    try:
+        index = first.get_device()
+        if index >= 0:
+            for t in others:
+                if t is not None and t.get_device() != index:
+                    break
+            else:
+                return first.device
+    except AttributeError:
+        pass
+    return _same_device(**dict(zip(names.split(), (first,) + others)))
 
 
-def _codes(rows, cols, axis, device):
-    along, across = _axis(axis)
-    q1, s1 = _fp8_buffers(rows, cols, None, None, device, "axis 1") if along else (None, None)
-    q0, s0 = _fp8_buffers(cols, rows, None, None, device, "axis 0") if across else (None, None)
-    return q1, s1, q0, s0
-
-
-def _at(q, s):
-    return (None, 0, None, 0) if q is None else (q.data_ptr(), q.stride(0), s.data_ptr(), s.stride(0))
-
-
-def _like(t, shape, dtypes, name):
+def _ld(t, shape, dtypes, name):
     """Row stride of a matrix that has to be of this shape and one of these types."""
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous():
+        return shape[1] or 1
     ld = _rows(t, name, dtypes)
     if t.shape != shape:
         raise ValueError("%s must have shape %s" % (name, tuple(shape)))
     return ld
+
+
+def _first(t, name, dtypes=_FLOATS):
+    """Row stride of the matrix that gives a call its shape, one of these types."""
+    if t.dim() == 2 and t.dtype in dtypes and t.is_contiguous():
+        return t.shape[1] or 1
+    return _rows(t, name, dtypes)
+
+
+_AXES = {None: (False, False), 0: (False, True), 1: (True, False), "both": (True, True)}
+
+
+def _axis(axis):
+    """(along the rows, along the columns)"""
+    try:
+        return _AXES[axis]
+    except (KeyError, TypeError):
+        raise ValueError("axis must be None, 0, 1 or 'both'") from None
+
+
+_NO_CODES = (None, 0, None, 0)
+
+
+def _codes(outer, length, device):
+    """New codes and scales of `outer` rows of this length (whole 16 bytes of scales, as fp8_gemm reads them), and those as the
+    library takes them."""
+    blocks = (length + 127) // 128
+    ldq, lds = blocks * 128, (blocks + 15) // 16 * 16
+    q, s = _empty(outer, ldq, dtype=_U8, device=device), _empty(outer, lds, dtype=_U8, device=device)
+    return q, s, (q.data_ptr(), ldq, s.data_ptr(), lds)
 
 
 def _vector(t, n, dtypes, name):
@@ -160,33 +194,35 @@ def rmsnorm_forward(x, weight=None, residual=None, eps=1e-5, axis=None, y_dtype=
 
     x, residual and weight [K] bf16 or f32 each. `h` may be given, also residual itself (or x, the types being the same), and is
     then updated in place; so may y. Codes along the columns need h."""
-    given = dict(x=x, weight=weight, residual=residual, h=h, y=y)
-    device = _same_device(**given)
-    ldx = _rows(x, "x", _FLOATS)
+    device = _device("x weight residual h y", x, weight, residual, h, y)
+    ldx = _first(x, "x")
     rows, cols = shape = x.shape
     along, across = _axis(axis)
-    ldr = _like(residual, shape, _FLOATS, "residual") if residual is not None else 0
-    if residual is None and h is not None:
-        raise ValueError("h is an output of the addition: it needs a residual")
-    if h is not None and not need_h:
-        raise ValueError("an output is given that is not needed")
-    if across and residual is not None and not need_h:
-        raise ValueError("codes along the columns need h")
-    sdtype = x.dtype if residual is None else residual.dtype
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is an output of the addition: it needs a residual")
+        sdtype, need_h, ldr = x.dtype, False, 0
+    else:
+        sdtype, ldr = residual.dtype, _ld(residual, shape, _FLOATS, "residual")
+        if not need_h and (h is not None or across):
+            raise ValueError("h is given but not needed" if h is not None else "codes along the columns need h")
     w = (None, 0) if weight is None else (_vector(weight, cols, _FLOATS, "weight"), _IN[weight.dtype])
     with _on(device, stream):
-        if residual is not None and h is None and need_h:
-            h = torch.empty(shape, dtype=sdtype, device=device)
-        ldh = _like(h, shape, (sdtype,), "h") if h is not None else 0
-        if y is None and y_dtype is not None:
-            y = torch.empty(shape, dtype=_float(y_dtype, "y_dtype"), device=device)
-        ldy = _like(y, shape, _FLOATS, "y") if y is not None else 0
-        rstd = torch.empty(rows, dtype=torch.float32, device=device)
-        q1, s1, q0, s0 = _codes(rows, cols, axis, device)
+        if need_h and h is None:
+            h, ldh = _empty(rows, cols, dtype=sdtype, device=device), cols
+        else:
+            ldh = 0 if h is None else _ld(h, shape, (sdtype,), "h")
+        if y is not None:
+            ldy = _ld(y, shape, _FLOATS, "y")
+        elif y_dtype is not None:
+            y, ldy = _empty(rows, cols, dtype=_float(y_dtype, "y_dtype"), device=device), cols
+        rstd = _empty(rows, dtype=torch.float32, device=device)
+        q1, s1, at1 = _codes(rows, cols, device) if along else (None, None, _NO_CODES)
+        q0, s0, at0 = _codes(cols, rows, device) if across else (None, None, _NO_CODES)
         _check(layer_lib().mxfp4_rmsnorm_forward(
             x.data_ptr(), _IN[x.dtype], ldx, None if residual is None else residual.data_ptr(), ldr, _IN[sdtype], *w, rows, cols,
-            float(eps), None if h is None else h.data_ptr(), ldh, rstd.data_ptr(), None if y is None else y.data_ptr(),
-            0 if y is None else _OUT[y.dtype], ldy, *_at(q1, s1), *_at(q0, s0), _current()), "mxfp4_rmsnorm_forward")
+            eps, None if h is None else h.data_ptr(), ldh, rstd.data_ptr(), *((None, 0, 0) if y is None else (y.data_ptr(), _OUT[y.dtype], ldy)),
+            *at1, *at0, _current()), "mxfp4_rmsnorm_forward")
     return RmsNorm(x if residual is None else h, rstd, y, q1, s1, q0, s0)
 
 
@@ -200,29 +236,30 @@ def rmsnorm_backward(dy, h, rstd, weight=None, dres=None, dh=None, need_dweight=
     """Gradients of rmsnorm_forward: RmsNormGrad(dh, dweight) from dy [T, K], the forward call's h and rstd, its weight, and dres,
     the gradient that arrives at h along the residual stream (None: none). dh, of h's type, is the gradient of both x and
     residual; it may be given, also dres itself. dweight FP32 or bf16 [K]; None with need_dweight false."""
-    device = _same_device(dy=dy, h=h, rstd=rstd, weight=weight, dres=dres, dh=dh, dweight=dweight, workspace=workspace)
-    lddy = _rows(dy, "dy", _FLOATS)
+    device = _device("dy h rstd weight dres dh dweight workspace", dy, h, rstd, weight, dres, dh, dweight, workspace)
+    lddy = _first(dy, "dy")
     rows, cols = shape = dy.shape
-    ldh = _like(h, shape, _FLOATS, "h")
-    lddr = _like(dres, shape, (h.dtype,), "dres") if dres is not None else 0
+    ldh, sdtype = _ld(h, shape, _FLOATS, "h"), h.dtype
+    res = (None, 0) if dres is None else (dres.data_ptr(), _ld(dres, shape, (sdtype,), "dres"))
     r = _vector(rstd, rows, (torch.float32,), "rstd")
     w = (None, 0) if weight is None else (_vector(weight, cols, _FLOATS, "weight"), _IN[weight.dtype])
     if dweight is not None and not need_dweight:
-        raise ValueError("an output is given that is not needed")
+        raise ValueError("dweight is given but not needed")
     with _on(device, stream):
         if dh is None:
-            dh = torch.empty(shape, dtype=h.dtype, device=device)
-        lddh = _like(dh, shape, (h.dtype,), "dh")
+            dh, lddh = _empty(rows, cols, dtype=sdtype, device=device), cols
+        else:
+            lddh = _ld(dh, shape, (sdtype,), "dh")
         dw = ws = (None, 0)
         if need_dweight:
             if dweight is None:
-                dweight = torch.empty(cols, dtype=_float(dweight_dtype, "dweight_dtype"), device=device)
+                dweight = _empty(cols, dtype=_float(dweight_dtype, "dweight_dtype"), device=device)
             dw = (_vector(dweight, cols, _FLOATS, "dweight"), _OUT[dweight.dtype])
             workspace = _room(workspace, rmsnorm_backward_workspace_bytes(rows, cols), device)
             ws = (workspace.data_ptr(), _bytes(workspace))
         _check(layer_lib().mxfp4_rmsnorm_backward(
-            dy.data_ptr(), _IN[dy.dtype], lddy, None if dres is None else dres.data_ptr(), lddr, h.data_ptr(), ldh, _IN[h.dtype],
-            *w, r, rows, cols, dh.data_ptr(), lddh, *dw, *ws, _current()), "mxfp4_rmsnorm_backward")
+            dy.data_ptr(), _IN[dy.dtype], lddy, *res, h.data_ptr(), ldh, _IN[sdtype], *w, r, rows, cols, dh.data_ptr(), lddh, *dw,
+            *ws, _current()), "mxfp4_rmsnorm_backward")
     return RmsNormGrad(dh, dweight)
 
 
@@ -230,18 +267,22 @@ def rmsnorm_backward(dy, h, rstd, weight=None, dres=None, dh=None, need_dweight=
 def swiglu_forward(gate, up, axis=None, out_dtype=torch.bfloat16, a=None, stream=None):
     """a = silu(gate) * up of two matrices [T, F], bf16 or f32 alike (they may be the halves of one). Returns Swiglu(a, q1, s1,
     q0, s0): a of out_dtype (None: not formed) and the 8-bit outputs that `axis` asks for. `a` may be given, also gate or up."""
-    device = _same_device(gate=gate, up=up, a=a)
-    ldg = _rows(gate, "gate", _FLOATS)
+    device = _device("gate up a", gate, up, a)
+    ldg = _first(gate, "gate")
     rows, cols = shape = gate.shape
-    ldu = _like(up, shape, (gate.dtype,), "up")
+    dtype = gate.dtype
+    ldu = _ld(up, shape, (dtype,), "up")
+    along, across = _axis(axis)
     with _on(device, stream):
-        if a is None and out_dtype is not None:
-            a = torch.empty(shape, dtype=_float(out_dtype, "out_dtype"), device=device)
-        lda = _like(a, shape, _FLOATS, "a") if a is not None else 0
-        q1, s1, q0, s0 = _codes(rows, cols, axis, device)
+        if a is not None:
+            lda = _ld(a, shape, _FLOATS, "a")
+        elif out_dtype is not None:
+            a, lda = _empty(rows, cols, dtype=_float(out_dtype, "out_dtype"), device=device), cols or 1
+        q1, s1, at1 = _codes(rows, cols, device) if along else (None, None, _NO_CODES)
+        q0, s0, at0 = _codes(cols, rows, device) if across else (None, None, _NO_CODES)
         _check(layer_lib().mxfp4_swiglu_forward(
-            gate.data_ptr(), ldg, up.data_ptr(), ldu, _IN[gate.dtype], rows, cols, None if a is None else a.data_ptr(),
-            0 if a is None else _OUT[a.dtype], lda, *_at(q1, s1), *_at(q0, s0), _current()), "mxfp4_swiglu_forward")
+            gate.data_ptr(), ldg, up.data_ptr(), ldu, _IN[dtype], rows, cols, *((None, 0, 0) if a is None else (a.data_ptr(), _OUT[a.dtype], lda)),
+            *at1, *at0, _current()), "mxfp4_swiglu_forward")
     return Swiglu(a, q1, s1, q0, s0)
 
 
@@ -250,10 +291,11 @@ def swiglu_backward(da, gate, up, axis=None, out_dtype=torch.bfloat16, joined=Tr
     outputs that `axis` asks for. joined: they are those of [dgate | dup], as one product of 2 F columns reads them (q1 [T, 2 F],
     F then a multiple of 128; q0 [2 F, T]), and dgate and dup the halves of one new matrix; otherwise .gate and .up have
     the Codes of each. dgate and dup may be given, also da, gate or up themselves."""
-    device = _same_device(da=da, gate=gate, up=up, dgate=dgate, dup=dup)
-    ldda = _rows(da, "da", _FLOATS)
+    device = _device("da gate up dgate dup", da, gate, up, dgate, dup)
+    ldda = _first(da, "da")
     rows, cols = shape = da.shape
-    ldg, ldu = _like(gate, shape, _FLOATS, "gate"), _like(up, shape, (gate.dtype,), "up")
+    dtype = gate.dtype
+    ldg, ldu = _ld(gate, shape, _FLOATS, "gate"), _ld(up, shape, (dtype,), "up")
     along, across = _axis(axis)
     if (dgate is None) != (dup is None):
         raise ValueError("dgate and dup are given together")
@@ -262,37 +304,37 @@ def swiglu_backward(da, gate, up, axis=None, out_dtype=torch.bfloat16, joined=Tr
     if joined and along and cols % 128:
         raise ValueError("joined codes along the rows need a multiple of 128 columns")
     with _on(device, stream):
-        if dgate is None and out_dtype is not None:
+        if dgate is not None:
+            outs = (dgate.data_ptr(), _ld(dgate, shape, _FLOATS, "dgate"), dup.data_ptr(), _ld(dup, shape, _FLOATS, "dup"), _OUT[dgate.dtype])
+        elif out_dtype is None:
+            outs = (None, 0, None, 0, 0)
+        else:
             _float(out_dtype, "out_dtype")
             if joined:
-                both = torch.empty((rows, 2 * cols), dtype=out_dtype, device=device)
-                dgate, dup = both[:, :cols], both[:, cols:]
+                both = _empty(rows, 2 * cols, dtype=out_dtype, device=device)
+                dgate, dup, ld = both[:, :cols], both[:, cols:], 2 * cols or 1
             else:
-                dgate, dup = (torch.empty(shape, dtype=out_dtype, device=device) for _ in range(2))
-        outs = (None, 0, None, 0, 0)
-        if dgate is not None:
-            lds = _like(dgate, shape, _FLOATS, "dgate"), _like(dup, shape, _FLOATS, "dup")
-            outs = (dgate.data_ptr(), lds[0], dup.data_ptr(), lds[1], _OUT[dgate.dtype])
+                dgate, dup = (_empty(rows, cols, dtype=out_dtype, device=device) for _ in range(2))
+                ld = cols or 1
+            outs = (dgate.data_ptr(), ld, dup.data_ptr(), ld, _OUT[out_dtype])
         q1 = s1 = q0 = s0 = g = u = None
-        none = (None, None, 0, None, None, 0)
-        at1 = at0 = none
+        at1 = at0 = (None, None, 0, None, None, 0)
         if joined:
             if along:
-                q1, s1 = _fp8_buffers(rows, 2 * cols, None, None, device, "axis 1")
-                at1 = (q1.data_ptr(), q1.data_ptr() + cols, q1.stride(0), s1.data_ptr(), s1.data_ptr() + cols // 128, s1.stride(0))
+                q1, s1, (q, ldq, sc, lds) = _codes(rows, 2 * cols, device)
+                at1 = (q, q + cols, ldq, sc, sc + cols // 128, lds)
             if across:
-                q0, s0 = _fp8_buffers(2 * cols, rows, None, None, device, "axis 0")
-                at0 = (q0.data_ptr(), q0.data_ptr() + cols * q0.stride(0), q0.stride(0), s0.data_ptr(),
-                       s0.data_ptr() + cols * s0.stride(0), s0.stride(0))
+                q0, s0, (q, ldq, sc, lds) = _codes(2 * cols, rows, device)
+                at0 = (q, q + cols * ldq, ldq, sc, sc + cols * lds, lds)
         else:
-            g, u = (Codes(*_codes(rows, cols, axis, device)) for _ in range(2))
-            if along:
-                at1 = (g.q1.data_ptr(), u.q1.data_ptr(), g.q1.stride(0), g.s1.data_ptr(), u.s1.data_ptr(), g.s1.stride(0))
-            if across:
-                at0 = (g.q0.data_ptr(), u.q0.data_ptr(), g.q0.stride(0), g.s0.data_ptr(), u.s0.data_ptr(), g.s0.stride(0))
+            none = (None, None, _NO_CODES)
+            (gq1, gs1, g1), (uq1, us1, u1) = (_codes(rows, cols, device), _codes(rows, cols, device)) if along else (none, none)
+            (gq0, gs0, g0), (uq0, us0, u0) = (_codes(cols, rows, device), _codes(cols, rows, device)) if across else (none, none)
+            g, u = Codes(gq1, gs1, gq0, gs0), Codes(uq1, us1, uq0, us0)
+            at1, at0 = (g1[0], u1[0], g1[1], g1[2], u1[2], g1[3]), (g0[0], u0[0], g0[1], g0[2], u0[2], g0[3])
         _check(layer_lib().mxfp4_swiglu_backward(
-            da.data_ptr(), _IN[da.dtype], ldda, gate.data_ptr(), ldg, up.data_ptr(), ldu, _IN[gate.dtype], rows, cols, *outs, *at1,
-            *at0, _current()), "mxfp4_swiglu_backward")
+            da.data_ptr(), _IN[da.dtype], ldda, gate.data_ptr(), ldg, up.data_ptr(), ldu, _IN[dtype], rows, cols, *outs, *at1, *at0,
+            _current()), "mxfp4_swiglu_backward")
     return SwigluGrad(dgate, dup, q1, s1, q0, s0, g, u)
 
 
@@ -309,6 +351,25 @@ def _dense(t):
     return True
 
 
+def _check_grad(g, o, index):
+    if not isinstance(g, torch.Tensor) or not isinstance(o, torch.Tensor) or not g.is_cuda:
+        raise TypeError("gradients and outputs must be tensors on a HIP device")
+    if g.get_device() != index or o.get_device() != index:
+        raise ValueError("gradients and outputs must be on one device")
+    if g.dtype not in _IN or o.dtype not in _OUT:
+        raise TypeError("gradients and outputs must be bfloat16 or float32")
+    if not _dense(g):
+        raise ValueError("gradients must be dense")
+    if o is not g and (o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous()))):
+        raise ValueError("an output must have its gradient's shape and strides")
+
+
+_T = torch.Tensor
+_shape, _dtype = operator.attrgetter("shape"), operator.attrgetter("dtype")
+# types of a gradient and its output as the library's array holds them: two 32-bit words
+_TYPES = {(g, o): _IN[g] | _OUT[o] << 32 for g in _IN for o in _OUT}
+
+
 def _grads(grads, out):
     """The device, and the tensors as the library takes them."""
     grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)
@@ -317,23 +378,27 @@ def _grads(grads, out):
         raise ValueError("%d outputs for %d gradients" % (len(outs), len(grads)))
     if not grads:
         raise ValueError("no gradients")
-    items, index = [], None
-    for g, o in zip(grads, outs):
-        if not isinstance(g, torch.Tensor) or not isinstance(o, torch.Tensor) or not g.is_cuda:
-            raise TypeError("gradients and outputs must be tensors on a HIP device")
-        at = g.get_device()
-        if index is None:
-            index = at
-        if at != index or (o is not g and o.get_device() != index):
-            raise ValueError("gradients and outputs must be on one device")
-        if g.dtype not in _IN or o.dtype not in _OUT:
-            raise TypeError("gradients and outputs must be bfloat16 or float32")
-        if not _dense(g):
-            raise ValueError("gradients must be dense")
-        if o is not g and (o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous()))):
-            raise ValueError("an output must have its gradient's shape and strides")
-        items += (g.data_ptr(), o.data_ptr(), g.numel(), _IN[g.dtype] | _OUT[o.dtype] << 32)
-    return grads[0].device, array.array("q", items), len(grads)
+    if not isinstance(grads[0], torch.Tensor):
+        raise TypeError("gradients must be tensors")
+    index = grads[0].get_device()
+    # one question to all tensors at a time, in half the time of a loop over them; where one is not as usual, each by itself
+    try:
+        usual = {index} == set(map(_T.get_device, grads)) and index >= 0 and all(map(_T.is_contiguous, grads))
+        if usual and outs is not grads:
+            usual = ({index} == set(map(_T.get_device, outs)) and all(map(_T.is_contiguous, outs))
+                     and list(map(_shape, grads)) == list(map(_shape, outs)))
+        types = list(map(_TYPES.get, zip(map(_dtype, grads), map(_dtype, outs))))
+    except (AttributeError, TypeError):
+        usual, types = False, [None]
+    if not usual or None in types:
+        for g, o in zip(grads, outs):
+            _check_grad(g, o, index)
+    items = array.array("q", bytes(32 * len(grads)))
+    items[0::4] = array.array("q", map(_T.data_ptr, grads))
+    items[1::4] = items[0::4] if outs is grads else array.array("q", map(_T.data_ptr, outs))
+    items[2::4] = array.array("q", map(_T.numel, grads))
+    items[3::4] = array.array("q", types)
+    return grads[0].device, items, len(grads)
 
 
 def grad_norm_workspace_bytes(grads) -> int:

@@ -25,7 +25,7 @@ def recorded(monkeypatch):
     import mxfp4_block_scaled_h16_amd.layer as layer
     lib = Recorder()
     monkeypatch.setattr(layer, "layer_lib", lambda: lib)
-    monkeypatch.setattr(layer, "_same_device", lambda **tensors: torch.device("cpu"))
+    monkeypatch.setattr(layer, "_same_device", lambda **tensors: torch.device("cpu"))      # what a CPU tensor's check ends in
     monkeypatch.setattr(layer, "_on", lambda device, stream: contextlib.nullcontext())
     monkeypatch.setattr(layer, "_current", lambda: 0)
     layer.rmsnorm_backward_workspace_bytes.cache_clear()
