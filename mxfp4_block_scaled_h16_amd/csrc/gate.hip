@@ -22,12 +22,12 @@ __device__ __forceinline__ float sigmoid(float g, float &e)
 }
 
 // GRAD: the gradients, from da; DF32: da's type. F32: that of g and u.
-template <bool GRAD, bool DF32, bool F32, bool RAGGED>
+template <bool GRAD, bool DF32, bool F32, bool RAGGED, bool NT>
 __global__ __launch_bounds__(512, 4) void gate_kernel(Gate p, int tiles_n)
 {
     __shared__ TileShared sh;
     const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
-    const int64_t tm = blockIdx.x / (unsigned)tiles_n, tn = blockIdx.x % (unsigned)tiles_n;
+    const auto [tm, tn] = tile_of(tiles_n);
     const int64_t row0 = tm * 128 + 4 * rg, col0 = tn * 128 + 8 * cg;
     Raw8<F32> g[4], u[4];
     Raw8<DF32> d[4];
@@ -38,9 +38,9 @@ __global__ __launch_bounds__(512, 4) void gate_kernel(Gate p, int tiles_n)
         u[i].zero();
         d[i].zero();
         if (row >= p.rows) continue;
-        g[i] = load_raw<F32, RAGGED>(at<F32>(p.g.p, row * p.g.ld), col0, p.cols);
-        u[i] = load_raw<F32, RAGGED>(at<F32>(p.u.p, row * p.u.ld), col0, p.cols);
-        if constexpr (GRAD) d[i] = load_raw<DF32, RAGGED>(at<DF32>(p.da.p, row * p.da.ld), col0, p.cols);
+        g[i] = load_raw<F32, RAGGED, NT>(at<F32>(p.g.p, row * p.g.ld), col0, p.cols);
+        u[i] = load_raw<F32, RAGGED, NT>(at<F32>(p.u.p, row * p.u.ld), col0, p.cols);
+        if constexpr (GRAD) d[i] = load_raw<DF32, RAGGED, NT>(at<DF32>(p.da.p, row * p.da.ld), col0, p.cols);
     }
     float v[GRAD ? 2 : 1][4][8];
 #pragma unroll
@@ -80,13 +80,21 @@ __global__ __launch_bounds__(512, 4) void gate_kernel(Gate p, int tiles_n)
     }
 }
 
+// Where inputs and outputs are more than the last cache holds, the inputs' loads do not stay in it: 8192 x 14336 (704 MB) 142 ->
+// 121 us, 4096 x 14336 71 -> 63; where they fit, the input is mostly still there from the product that wrote it:
+// 2048 x 14336 (176 MB) 30 us, and 34 with such loads.
+constexpr int64_t kLastCache = (int64_t)256 << 20;
+
 template <bool GRAD, bool DF32, bool F32>
 hipError_t run(const Gate &p, hipStream_t stream)
 {
     const int64_t tiles_n = (p.cols + 127) / 128;
     const dim3 grid((unsigned)((p.rows + 127) / 128 * tiles_n)), block(512);
-    return p.cols % 8 ? launch(gate_kernel<GRAD, DF32, F32, true>, grid, block, 0, stream, p, (int)tiles_n)
-                      : launch(gate_kernel<GRAD, DF32, F32, false>, grid, block, 0, stream, p, (int)tiles_n);
+    int64_t bytes = (F32 ? 8 : 4) + (GRAD ? DF32 ? 4 : 2 : 0);
+    for (int k = 0; k < 2; ++k) bytes += (p.out[k].p ? p.out_f32 ? 4 : 2 : 0) + (p.q1[k].q ? 1 : 0) + (p.q0[k].q ? 1 : 0);
+    if (p.cols % 8) return launch(gate_kernel<GRAD, DF32, F32, true, false>, grid, block, 0, stream, p, (int)tiles_n);
+    return p.rows * p.cols > kLastCache / bytes ? launch(gate_kernel<GRAD, DF32, F32, false, true>, grid, block, 0, stream, p, (int)tiles_n)
+                                                : launch(gate_kernel<GRAD, DF32, F32, false, false>, grid, block, 0, stream, p, (int)tiles_n);
 }
 
 }  // namespace

@@ -18,16 +18,20 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 
 // -------------------------------------------------------------------- eight values of a row ---
 // As they lie in memory, so that a thread's loads can all be under way before the first is used. Rows are
-// aligned to their elements only.
+// aligned to their elements only. NT: loads that do not stay in the caches, for streams that are larger than those.
 template <bool F32>
 struct Raw8;
 template <>
 struct Raw8<false> {
     u32x4 w;
     __device__ __forceinline__ void zero() { w = u32x4{0u, 0u, 0u, 0u}; }
+    // what is formed of the values from here on is formed anew, and nothing formed before is kept for it
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(w)); }
+    template <bool NT>
     __device__ __forceinline__ void load(const void *p)
     {
-        w = *reinterpret_cast<const u32x4_any *>(p);
+        const u32x4_any *at = reinterpret_cast<const u32x4_any *>(p);
+        w = NT ? __builtin_nontemporal_load(at) : *at;
     }
     __device__ __forceinline__ void store(void *p) const { *reinterpret_cast<u32x4_any *>(p) = w; }
     __device__ __forceinline__ void get(float (&v)[8]) const
@@ -48,10 +52,14 @@ template <>
 struct Raw8<true> {
     f32x4 a, b;
     __device__ __forceinline__ void zero() { a = b = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(a), "+v"(b)); }
+    template <bool NT>
     __device__ __forceinline__ void load(const void *p)
     {
-        a = *reinterpret_cast<const f32x4_any *>(p);
-        b = *reinterpret_cast<const f32x4_any *>(static_cast<const float *>(p) + 4);
+        const f32x4_any *at = reinterpret_cast<const f32x4_any *>(p);
+        const f32x4_any *next = reinterpret_cast<const f32x4_any *>(static_cast<const float *>(p) + 4);
+        a = NT ? __builtin_nontemporal_load(at) : *at;
+        b = NT ? __builtin_nontemporal_load(next) : *next;
     }
     __device__ __forceinline__ void store(void *p) const
     {
@@ -89,12 +97,12 @@ __device__ __forceinline__ void *at(void *p, int64_t i)
 
 // Values col .. col + 7 of a row that starts at `row` and has `cols`; zeros behind its end. RAGGED: it may end within
 // these eight (they are then read one by one); otherwise col and cols are multiples of eight.
-template <bool F32, bool RAGGED>
+template <bool F32, bool RAGGED, bool NT = false>
 __device__ __forceinline__ Raw8<F32> load_raw(const void *row, int64_t col, int64_t cols)
 {
     Raw8<F32> r;
     if (RAGGED ? col + 8 <= cols : col < cols) {
-        r.load(at<F32>(row, col));
+        r.template load<NT>(at<F32>(row, col));
         return r;
     }
     r.zero();
@@ -218,6 +226,17 @@ __device__ __forceinline__ void store_row_codes(const Fp8Out &out, int64_t row, 
 // A tile of 128 x 128 values in 512 threads of 4 x 8: thread t has rows 4 (t / 16) .. and columns 8 (t % 16) .. .
 // Along the columns a block is a column of the tile: its maximum joins the four row groups of a wavefront by
 // lane swaps and the wavefronts through the LDS, which also turns the codes.
+// Workgroups go round the eight XCDs one by one: each XCD takes a run of tiles side by side (gated activation 8192 x 14336 125 ->
+// 121 us, its gradient 260 -> 243; the norm's codes along the columns, whose input is in the caches, in their own order).
+struct Tile {
+    int64_t m, n;
+};
+__device__ __forceinline__ Tile tile_of(int tiles_n)
+{
+    const unsigned each = gridDim.x / 8, b = blockIdx.x, id = b < 8 * each ? b % 8 * each + b / 8 : b;
+    return {id / (unsigned)tiles_n, id % (unsigned)tiles_n};
+}
+
 struct TileShared {
     uint32_t top[8][128];
     uint32_t scale[128];      // scale bytes as FP32's exponents

@@ -227,7 +227,7 @@ hipError_t forward(const ForwardArgs &args, hipStream_t stream)
 }
 
 // ------------------------------------------------------------------------------- backward -----
-constexpr int kGradBlocks = 512;   // workgroups, and so partial sums of dw
+constexpr int kGradBlocks = 512;   // most workgroups, and so partial sums of dw
 
 struct BackwardArgs {
     NormBackward p;
@@ -236,14 +236,36 @@ struct BackwardArgs {
     int64_t rows_per_block;
 };
 
-// A workgroup works rows_per_block rows one after the other, 1024 / TPR of them at a time, and keeps its sum of dw in
-// registers until the end.
-template <bool BF32, bool SF32, bool RAGGED, int TPR, int C>
-__global__ __launch_bounds__(1024) void norm_backward_kernel(BackwardArgs args)
+template <bool BF32, bool SF32, int C>
+struct GradRow {
+    Raw8<BF32> dy[C];
+    Raw8<SF32> h[C], dres[C];
+    float rstd;
+
+    template <bool RAGGED, int TPR>
+    __device__ __forceinline__ void load(const NormBackward &p, int64_t row, int64_t end, int lane)
+    {
+        const bool in = row < end;
+        rstd = in ? p.rstd[row] : 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = in ? (c * TPR + lane) * 8 : p.cols;      // behind the row: zeros
+            dy[c] = load_raw<BF32, RAGGED>(at<BF32>(p.dy.p, row * p.dy.ld), col, p.cols);
+            h[c] = load_raw<SF32, RAGGED>(at<SF32>(p.h.p, row * p.h.ld), col, p.cols);
+            dres[c] = load_raw<SF32, RAGGED>(at<SF32>(p.dres.p, row * p.dres.ld), p.dres.p ? col : p.cols, p.cols);
+        }
+    }
+};
+
+// A workgroup works rows_per_block rows, ROWS of them at a time in TPR threads each, and keeps its sum of dw in registers until
+// the end. With eight values a thread (C = 1) the next rows' loads are under way meanwhile: at 8192 x 4096 the kernel and the
+// joining of dw take 56 us with them, 75 with 16 values a thread in 256 and no such loads (58 with them, in 162 registers).
+template <bool BF32, bool SF32, bool RAGGED, int TPR, int C, int ROWS>
+__global__ __launch_bounds__(TPR *ROWS) void norm_backward_kernel(BackwardArgs args)
 {
-    constexpr int kRows = 1024 / TPR, kWaves = TPR / 64;
-    __shared__ float part[2][kRows][kWaves];
-    __shared__ float sums[kRows > 1 ? TPR * 8 : 1];
+    constexpr int kWaves = TPR / 64;
+    __shared__ float part[2][ROWS][kWaves];
+    __shared__ float sums[ROWS > 1 ? TPR * 8 : 1];
     const NormBackward &p = args.p;
     const int lane = (int)threadIdx.x % TPR, slot = (int)threadIdx.x / TPR;
     float w[C][8], dw[C][8];
@@ -259,38 +281,23 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(BackwardArgs args)
         for (int e = 0; e < 8; ++e) dw[c][e] = 0.0f;
     }
     const int64_t first = (int64_t)blockIdx.x * args.rows_per_block, end = min(first + args.rows_per_block, p.rows);
+    GradRow<BF32, SF32, C> next;
+    if constexpr (C == 1) next.template load<RAGGED, TPR>(p, first + slot, end, lane);
     int turn = 0;
-    for (int64_t base = first; base < end; base += kRows) {
+    for (int64_t base = first; base < end; base += ROWS) {
         const int64_t row = base + slot;
-        const bool in = row < end;
-        Raw8<BF32> dy[C];
-        Raw8<SF32> h[C], dres[C];
-        float rstd = 0.0f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            dy[c].zero();
-            h[c].zero();
-            dres[c].zero();
-        }
-        if (in) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int64_t col = (c * TPR + lane) * 8;
-                dy[c] = load_raw<BF32, RAGGED>(at<BF32>(p.dy.p, row * p.dy.ld), col, p.cols);
-                h[c] = load_raw<SF32, RAGGED>(at<SF32>(p.h.p, row * p.h.ld), col, p.cols);
-                if (p.dres.p) dres[c] = load_raw<SF32, RAGGED>(at<SF32>(p.dres.p, row * p.dres.ld), col, p.cols);
-            }
-            rstd = p.rstd[row];
-        }
+        if constexpr (C > 1) next.template load<RAGGED, TPR>(p, row, end, lane);
+        GradRow<BF32, SF32, C> r = next;
+        if constexpr (C == 1) next.template load<RAGGED, TPR>(p, row + ROWS, end, lane);
         float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float a[8], b[8];
-            dy[c].get(a);
-            h[c].get(b);
+            r.dy[c].get(a);
+            r.h[c].get(b);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float n = b[e] * rstd;
+                const float n = b[e] * r.rstd;
                 dw[c][e] = fmaf(a[e], n, dw[c][e]);
                 sum = fmaf(a[e] * w[c][e], n, sum);
             }
@@ -304,16 +311,18 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(BackwardArgs args)
             for (int i = 1; i < kWaves; ++i) sum += part[turn][slot][i];
             turn ^= 1;
         }
-        if (!in) continue;
+        if (row >= end) continue;
         const float mean = sum * args.inv_cols;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float a[8], b[8], d[8];
-            dy[c].get(a);
-            h[c].get(b);
-            dres[c].get(d);
+            r.dy[c].renew();
+            r.h[c].renew();
+            r.dy[c].get(a);
+            r.h[c].get(b);
+            r.dres[c].get(d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = fmaf(fmaf(-(b[e] * rstd), mean, a[e] * w[c][e]), rstd, d[e]);
+            for (int e = 0; e < 8; ++e) d[e] = fmaf(fmaf(-(b[e] * r.rstd), mean, a[e] * w[c][e]), r.rstd, d[e]);
             Raw8<SF32> out;
             out.set(d);
             store_raw<SF32, RAGGED>(out, at<SF32>(p.dh.p, row * p.dh.ld), (c * TPR + lane) * 8, p.cols);
@@ -324,8 +333,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(BackwardArgs args)
     float *to = args.part + (int64_t)blockIdx.x * p.cols;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        if constexpr (kRows > 1) {
-            for (int k = 0; k < kRows; ++k) {
+        if constexpr (ROWS > 1) {
+            for (int k = 0; k < ROWS; ++k) {
                 if (slot == k) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -397,19 +406,21 @@ __global__ __launch_bounds__(1024) void norm_backward_long_kernel(BackwardArgs a
     }
 }
 
-// dw: the workgroups' sums, in a fixed order: 64 columns a workgroup, 16 shares of the sums
+// dw: the workgroups' sums, in a fixed order: 32 columns a workgroup, 32 shares of the sums
 __global__ __launch_bounds__(1024) void norm_dw_kernel(const float *part, int count, int64_t cols, void *dw, int f32)
 {
-    __shared__ float sums[16][64];
-    const int lane = threadIdx.x & 63, share = threadIdx.x >> 6;
-    const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ float sums[32][32 + 1];
+    const int lane = threadIdx.x & 31, share = threadIdx.x >> 5;
+    const int64_t col = (int64_t)blockIdx.x * 32 + lane;
     float sum = 0.0f;
-    if (col < cols)
-        for (int i = share; i < count; i += 16) sum += part[(int64_t)i * cols + col];
+    if (col < cols) {
+#pragma unroll 8
+        for (int i = share; i < count; i += 32) sum += part[(int64_t)i * cols + col];
+    }
     sums[share][lane] = sum;
     __syncthreads();
     if (share || col >= cols) return;
-    for (int i = 1; i < 16; ++i) sum += sums[i][lane];
+    for (int i = 1; i < 32; ++i) sum += sums[i][lane];
     if (f32)
         static_cast<float *>(dw)[col] = sum;
     else
@@ -422,14 +433,14 @@ template <bool BF32, bool SF32, bool RAGGED>
 hipError_t pick_backward(const BackwardArgs &args, unsigned blocks, hipStream_t stream)
 {
     const int64_t cols = args.p.cols;
-    const dim3 grid(blocks), block(1024);
-    if (cols <= 512) return launch(norm_backward_kernel<BF32, SF32, RAGGED, 64, 1>, grid, block, 0, stream, args);
-    if (cols <= 1024) return launch(norm_backward_kernel<BF32, SF32, RAGGED, 128, 1>, grid, block, 0, stream, args);
-    if (cols <= 2048) return launch(norm_backward_kernel<BF32, SF32, RAGGED, 256, 1>, grid, block, 0, stream, args);
-    if (cols <= 4096) return launch(norm_backward_kernel<BF32, SF32, RAGGED, 256, 2>, grid, block, 0, stream, args);
-    if (cols <= 8192) return launch(norm_backward_kernel<BF32, SF32, RAGGED, 512, 2>, grid, block, 0, stream, args);
-    if (cols <= 16384) return launch(norm_backward_kernel<BF32, SF32, RAGGED, 1024, 2>, grid, block, 0, stream, args);
-    return launch(norm_backward_long_kernel<BF32, SF32>, grid, block, 0, stream, args);
+    const auto run = [&](auto kernel, int threads) { return launch(kernel, dim3(blocks), dim3(threads), 0, stream, args); };
+    if (cols <= 512) return run(norm_backward_kernel<BF32, SF32, RAGGED, 64, 1, 8>, 512);
+    if (cols <= 1024) return run(norm_backward_kernel<BF32, SF32, RAGGED, 128, 1, 4>, 512);
+    if (cols <= 2048) return run(norm_backward_kernel<BF32, SF32, RAGGED, 256, 1, 2>, 512);
+    if (cols <= 4096) return run(norm_backward_kernel<BF32, SF32, RAGGED, 512, 1, 1>, 512 * 1);
+    if (cols <= 8192) return run(norm_backward_kernel<BF32, SF32, RAGGED, 1024, 1, 1>, 1024);
+    if (cols <= 16384) return run(norm_backward_kernel<BF32, SF32, RAGGED, 1024, 2, 1>, 1024);
+    return run(norm_backward_long_kernel<BF32, SF32>, 1024);
 }
 template <bool BF32, bool SF32>
 hipError_t backward(const BackwardArgs &args, unsigned blocks, hipStream_t stream)
@@ -482,7 +493,7 @@ hipError_t launch_norm_backward(const NormBackward &p, void *ws, hipStream_t str
         if (e != hipSuccess) return e;
     }
     if (!p.dw) return hipSuccess;
-    return launch(norm_dw_kernel, dim3((unsigned)((p.cols + 63) / 64)), dim3(1024), 0, stream, static_cast<const float *>(ws),
+    return launch(norm_dw_kernel, dim3((unsigned)((p.cols + 31) / 32)), dim3(1024), 0, stream, static_cast<const float *>(ws),
                   (int)blocks, p.cols, p.dw, p.dw_f32 ? 1 : 0);
 }
 
