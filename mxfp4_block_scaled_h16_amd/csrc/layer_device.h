@@ -18,7 +18,7 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b)
 
 // -------------------------------------------------------------------- eight values of a row ---
 // As they lie in memory, so that a thread's loads can all be under way before the first is used. Rows are
-// aligned to their elements only. NT: loads that do not stay in the caches, for streams that are larger than those.
+// aligned to their elements only. NT: loads and stores that do not stay in the caches, for streams that are larger than those.
 template <bool F32>
 struct Raw8;
 template <>
@@ -33,7 +33,15 @@ struct Raw8<false> {
         const u32x4_any *at = reinterpret_cast<const u32x4_any *>(p);
         w = NT ? __builtin_nontemporal_load(at) : *at;
     }
-    __device__ __forceinline__ void store(void *p) const { *reinterpret_cast<u32x4_any *>(p) = w; }
+    template <bool NT>
+    __device__ __forceinline__ void store(void *p) const
+    {
+        u32x4_any *at = reinterpret_cast<u32x4_any *>(p);
+        if constexpr (NT)
+            __builtin_nontemporal_store(w, at);
+        else
+            *at = w;
+    }
     __device__ __forceinline__ void get(float (&v)[8]) const
     {
 #pragma unroll
@@ -61,10 +69,17 @@ struct Raw8<true> {
         a = NT ? __builtin_nontemporal_load(at) : *at;
         b = NT ? __builtin_nontemporal_load(next) : *next;
     }
+    template <bool NT>
     __device__ __forceinline__ void store(void *p) const
     {
-        *reinterpret_cast<f32x4_any *>(p) = a;
-        *reinterpret_cast<f32x4_any *>(static_cast<float *>(p) + 4) = b;
+        f32x4_any *at = reinterpret_cast<f32x4_any *>(p), *next = reinterpret_cast<f32x4_any *>(static_cast<float *>(p) + 4);
+        if constexpr (NT) {
+            __builtin_nontemporal_store(a, at);
+            __builtin_nontemporal_store(b, next);
+        } else {
+            *at = a;
+            *next = b;
+        }
     }
     __device__ __forceinline__ void get(float (&v)[8]) const
     {
@@ -123,11 +138,11 @@ __device__ __forceinline__ Raw8<F32> load_raw(const void *row, int64_t col, int6
     }
     return r;
 }
-template <bool F32, bool RAGGED>
+template <bool F32, bool RAGGED, bool NT = false>
 __device__ __forceinline__ void store_raw(const Raw8<F32> &r, void *row, int64_t col, int64_t cols)
 {
     if (RAGGED ? col + 8 <= cols : col < cols) {
-        r.store(at<F32>(row, col));
+        r.template store<NT>(at<F32>(row, col));
         return;
     }
     if constexpr (RAGGED) {

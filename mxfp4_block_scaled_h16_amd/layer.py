@@ -360,12 +360,13 @@ def _check_grad(g, o, index):
         raise TypeError("gradients and outputs must be bfloat16 or float32")
     if not _dense(g):
         raise ValueError("gradients must be dense")
-    if o is not g and (o.shape != g.shape or (o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous()))):
-        raise ValueError("an output must have its gradient's shape and strides")
+    if o is not g and (o.numel() != g.numel() if o.is_contiguous() and g.is_contiguous() else
+                       o.shape != g.shape or o.stride() != g.stride()):
+        raise ValueError("an output must have its gradient's shape and strides, or as many values where both are contiguous")
 
 
 _T = torch.Tensor
-_shape, _dtype = operator.attrgetter("shape"), operator.attrgetter("dtype")
+_dtype = operator.attrgetter("dtype")
 # types of a gradient and its output as the library's array holds them: two 32-bit words
 _TYPES = {(g, o): _IN[g] | _OUT[o] << 32 for g in _IN for o in _OUT}
 
@@ -384,9 +385,10 @@ def _grads(grads, out):
     # one question to all tensors at a time, in half the time of a loop over them; where one is not as usual, each by itself
     try:
         usual = {index} == set(map(_T.get_device, grads)) and index >= 0 and all(map(_T.is_contiguous, grads))
+        counts = array.array("q", map(_T.numel, grads))
         if usual and outs is not grads:
             usual = ({index} == set(map(_T.get_device, outs)) and all(map(_T.is_contiguous, outs))
-                     and list(map(_shape, grads)) == list(map(_shape, outs)))
+                     and counts == array.array("q", map(_T.numel, outs)))
         types = list(map(_TYPES.get, zip(map(_dtype, grads), map(_dtype, outs))))
     except (AttributeError, TypeError):
         usual, types = False, [None]
@@ -396,7 +398,7 @@ def _grads(grads, out):
     items = array.array("q", bytes(32 * len(grads)))
     items[0::4] = array.array("q", map(_T.data_ptr, grads))
     items[1::4] = items[0::4] if outs is grads else array.array("q", map(_T.data_ptr, outs))
-    items[2::4] = array.array("q", map(_T.numel, grads))
+    items[2::4] = counts
     items[3::4] = array.array("q", types)
     return grads[0].device, items, len(grads)
 
@@ -423,7 +425,8 @@ def grad_norm(grads, workspace=None, stream=None):
 
 def grad_scale(grads, sum_sq, max_norm, eps=1e-6, out=None, stream=None):
     """Multiplies the gradients by min(1, max_norm / (norm + eps)) with norm the root of sum_sq, float64 [] on their device: in
-    place, or into `out` (as many tensors of the same shapes and strides, bf16 or f32). Returns norm, FP32 []."""
+    place, or into `out` (bf16 or f32 tensors of the same shapes and strides; of contiguous ones also of other shapes, such as parts of
+    a flat buffer). Returns norm, FP32 []."""
     device, items, n = _grads(grads, out)
     if not isinstance(sum_sq, torch.Tensor) or sum_sq.dtype != torch.float64 or sum_sq.numel() != 1 or sum_sq.device != device:
         raise ValueError("sum_sq must be one float64 on the gradients' device")

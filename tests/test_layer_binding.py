@@ -129,7 +129,9 @@ def test_gradients_as_the_library_takes_them(recorded):
     for t in (_grad(4, 6)[:, :3], _grad(8)[::2], _grad(1).expand(4), _grad(3, 1).expand(3, 4)):
         with pytest.raises(ValueError):
             layer._grads([t], None)
-    for g, o in ((a, _grad(5, 3)), (c, _grad(6, 4)), (a, _grad(5, 3).t())):
+    _, items, n = layer._grads([a], [_grad(15)])                 # part of a flat buffer
+    assert n == 1 and items[2] == 15
+    for g, o in ((a, _grad(16)), (c, _grad(6, 4)), (c, _grad(24)), (a, _grad(5, 3).t())):
         with pytest.raises(ValueError):
             layer._grads([g], [o])
     for t in (_grad(4).half(), _grad(4).double()):
