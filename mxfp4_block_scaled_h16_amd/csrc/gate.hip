@@ -3,7 +3,12 @@
 //   s = 1 / (1 + exp(-g));  a = g s u
 //   du = da g s,  dg = da u s (1 + g (1 - s))
 //
-// One pass: a workgroup works a tile of 128 x 128 values, which holds whole blocks along both axes.
+// One pass: a workgroup works a tile of 128 x 128 values, which holds whole blocks along both axes, in registers.
+//
+// Bound by memory. 8192 x 14336 in bf16 with codes along both axes: forward 122 us (704 MB, 5.8 TB/s), the gradient 241 (1174 MB,
+// 4.9 TB/s; a kernel that only reads and writes as many streams 206 to 222). The scale bytes, one to a line, are 11 us of the
+// gradient's, the turning of the codes 2; more wavefronts (1024 threads of half the values, up to eight a SIMD) made
+// it 266, one pass through the LDS for both gradients no difference.
 #include <cfloat>
 
 #include "internal.h"
@@ -21,26 +26,30 @@ __device__ __forceinline__ float sigmoid(float g, float &e)
     return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// GRAD: the gradients, from da; DF32: da's type. F32: that of g and u.
-template <bool GRAD, bool DF32, bool F32, bool RAGGED, bool NT>
-__global__ __launch_bounds__(512, 4) void gate_kernel(Gate p, int tiles_n)
+// One tile. GRAD: the gradients, from da; DF32: da's type. F32: that of g and u. FULL: the tile lies inside the matrix, so that
+// nothing is checked and a row's address is the one before and a stride: 32 VALU operations a value of the gradient instead of
+// 38, which the large sizes do not notice, but the small ones do (256 x 512 forward 5.6 -> 4.3 us, the gradient of 1111 x 2001 in
+// FP32 18 -> 16).
+template <bool GRAD, bool DF32, bool F32, bool NT, bool FULL>
+__device__ __forceinline__ void gate_tile(const Gate &p, int64_t tm, int64_t tn, TileShared &sh)
 {
-    __shared__ TileShared sh;
-    const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
-    const auto [tm, tn] = tile_of(tiles_n);
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int64_t row0 = tm * 128 + 4 * rg, col0 = tn * 128 + 8 * cg;
     Raw8<F32> g[4], u[4];
     Raw8<DF32> d[4];
+    const void *gp = at<F32>(p.g.p, row0 * p.g.ld), *up = at<F32>(p.u.p, row0 * p.u.ld), *dp = at<DF32>(p.da.p, row0 * p.da.ld);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t row = row0 + i;
-        g[i].zero();
-        u[i].zero();
-        d[i].zero();
-        if (row >= p.rows) continue;
-        g[i] = load_raw<F32, RAGGED, NT>(at<F32>(p.g.p, row * p.g.ld), col0, p.cols);
-        u[i] = load_raw<F32, RAGGED, NT>(at<F32>(p.u.p, row * p.u.ld), col0, p.cols);
-        if constexpr (GRAD) d[i] = load_raw<DF32, RAGGED, NT>(at<DF32>(p.da.p, row * p.da.ld), col0, p.cols);
+        if constexpr (FULL) {
+            g[i].template load<NT>(at<F32>(gp, i * p.g.ld + col0));
+            u[i].template load<NT>(at<F32>(up, i * p.u.ld + col0));
+            if constexpr (GRAD) d[i].template load<NT>(at<DF32>(dp, i * p.da.ld + col0));
+        } else {
+            const int64_t cols = row0 + i < p.rows ? p.cols : 0;
+            g[i] = load_raw<F32, true, NT>(at<F32>(gp, i * p.g.ld), col0, cols);
+            u[i] = load_raw<F32, true, NT>(at<F32>(up, i * p.u.ld), col0, cols);
+            if constexpr (GRAD) d[i] = load_raw<DF32, true, NT>(at<DF32>(dp, i * p.da.ld), col0, cols);
+        }
     }
     float v[GRAD ? 2 : 1][4][8];
 #pragma unroll
@@ -57,27 +66,49 @@ __global__ __launch_bounds__(512, 4) void gate_kernel(Gate p, int tiles_n)
                 const float t = fminf(x, FLT_MAX) * s;
                 v[0][i][e] = c[e] * b[e] * (s * fmaf(a[e], t, 1.0f));
                 v[1][i][e] = c[e] * (a[e] * s);
-                // both now, while the inputs leave their registers: formed where they are used, they hold 186 instead
+                // now, while the inputs leave their registers: formed where it is used, the kernel holds 186 (345 us instead of
+                // 256 at 8192 x 14336)
                 asm volatile("" : "+v"(v[1][i][e]));
             } else {
                 v[0][i][e] = a[e] * s * b[e];
+                asm volatile("" : "+v"(v[0][i][e]));    // likewise: 76 registers instead of 87
             }
         }
     }
 #pragma unroll
     for (int k = 0; k < (GRAD ? 2 : 1); ++k) {
+        if (p.out[k].p) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = row0 + i;
-            if (row >= p.rows) break;
-            if (p.out[k].p)
-                store_any<RAGGED>(p.out_f32, v[k][i],
-                                  p.out_f32 ? at<true>(p.out[k].p, row * p.out[k].ld) : at<false>(p.out[k].p, row * p.out[k].ld),
-                                  col0, p.cols);
-            if (p.q1[k].q) store_row_codes(p.q1[k], row, col0, p.cols, v[k][i]);
+            for (int i = 0; i < 4; ++i)
+                store_any<!FULL>(p.out_f32, v[k][i],
+                                 p.out_f32 ? at<true>(p.out[k].p, (row0 + i) * p.out[k].ld) : at<false>(p.out[k].p, (row0 + i) * p.out[k].ld),
+                                 col0, FULL || row0 + i < p.rows ? p.cols : 0);
         }
-        if (p.q0[k].q) store_tile_columns(p.q0[k], tm, tn, p.cols, v[k], sh);
+        if (p.q1[k].q) {
+            uint8_t *q = p.q1[k].q + row0 * p.q1[k].ldq + col0, *to = p.q1[k].s + row0 * p.q1[k].lds + tn;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t s;
+                const u32x2 w = row_codes(v[k][i], s);
+                if (FULL || row0 + i < p.rows) {
+                    *reinterpret_cast<u32x2 *>(q + i * p.q1[k].ldq) = w;
+                    if (cg == 0) to[i * p.q1[k].lds] = (uint8_t)s;
+                }
+            }
+        }
+        if (p.q0[k].q) store_tile_columns(p.q0[k], tm, tn, FULL ? INT64_MAX : p.cols, v[k], sh);
     }
+}
+
+template <bool GRAD, bool DF32, bool F32, bool NT>
+__global__ __launch_bounds__(512, GRAD || F32 ? 4 : 6) void gate_kernel(Gate p, int tiles_n)
+{
+    __shared__ TileShared sh;
+    const auto [tm, tn] = tile_of(tiles_n);
+    if ((tm + 1) * 128 <= p.rows && (tn + 1) * 128 <= p.cols)
+        gate_tile<GRAD, DF32, F32, NT, true>(p, tm, tn, sh);
+    else
+        gate_tile<GRAD, DF32, F32, NT, false>(p, tm, tn, sh);
 }
 
 // Where inputs and outputs are more than the last cache holds, the inputs' loads do not stay in it: 8192 x 14336 (704 MB) 142 ->
@@ -92,9 +123,8 @@ hipError_t run(const Gate &p, hipStream_t stream)
     const dim3 grid((unsigned)((p.rows + 127) / 128 * tiles_n)), block(512);
     int64_t bytes = (F32 ? 8 : 4) + (GRAD ? DF32 ? 4 : 2 : 0);
     for (int k = 0; k < 2; ++k) bytes += (p.out[k].p ? p.out_f32 ? 4 : 2 : 0) + (p.q1[k].q ? 1 : 0) + (p.q0[k].q ? 1 : 0);
-    if (p.cols % 8) return launch(gate_kernel<GRAD, DF32, F32, true, false>, grid, block, 0, stream, p, (int)tiles_n);
-    return p.rows * p.cols > kLastCache / bytes ? launch(gate_kernel<GRAD, DF32, F32, false, true>, grid, block, 0, stream, p, (int)tiles_n)
-                                                : launch(gate_kernel<GRAD, DF32, F32, false, false>, grid, block, 0, stream, p, (int)tiles_n);
+    return p.rows * p.cols > kLastCache / bytes ? launch(gate_kernel<GRAD, DF32, F32, true>, grid, block, 0, stream, p, (int)tiles_n)
+                                                : launch(gate_kernel<GRAD, DF32, F32, false>, grid, block, 0, stream, p, (int)tiles_n);
 }
 
 }  // namespace

@@ -221,18 +221,20 @@ __device__ __forceinline__ uint32_t divide4_any(float a, float b, float c, float
     return s == 0xFFu ? 0u : encode4(a, b, c, d, inverse_scale(s));
 }
 
-// Eight values of a row in each of 16 lanes side by side, which are one block (col a multiple of 8, the block's
-// first lane at a multiple of 128): its codes, zeros behind the row's end up to the block's, and its scale.
+// Eight values of a row in each of 16 lanes side by side, which are one block: their codes, and the block's scale byte.
+__device__ __forceinline__ u32x2 row_codes(const float (&v)[8], uint32_t &s)
+{
+    s = e8m0_of(row16_max(largest(v)) & 0x7FFFFFFFu);
+    if (__any(special(s))) return u32x2{divide4_any(v[0], v[1], v[2], v[3], s), divide4_any(v[4], v[5], v[6], v[7], s)};
+    const float scale = __uint_as_float(s << 23);
+    return u32x2{divide4(v[0], v[1], v[2], v[3], scale), divide4(v[4], v[5], v[6], v[7], scale)};
+}
+// The same, written: col a multiple of 8, the block's first lane at a multiple of 128; zeros behind the row's end up to the
+// block's.
 __device__ __forceinline__ void store_row_codes(const Fp8Out &out, int64_t row, int64_t col, int64_t cols, const float (&v)[8])
 {
-    const uint32_t s = e8m0_of(row16_max(largest(v)) & 0x7FFFFFFFu);
-    u32x2 w;
-    if (__any(special(s))) {
-        w = u32x2{divide4_any(v[0], v[1], v[2], v[3], s), divide4_any(v[4], v[5], v[6], v[7], s)};
-    } else {
-        const float scale = __uint_as_float(s << 23);
-        w = u32x2{divide4(v[0], v[1], v[2], v[3], scale), divide4(v[4], v[5], v[6], v[7], scale)};
-    }
+    uint32_t s;
+    const u32x2 w = row_codes(v, s);
     if ((col & ~(int64_t)127) >= cols) return;
     *reinterpret_cast<u32x2 *>(out.q + row * out.ldq + col) = w;
     if ((col & 127) == 0) out.s[row * out.lds + (col >> 7)] = (uint8_t)s;

@@ -100,19 +100,20 @@ _here = contextlib.nullcontext()
 
 def _on(device, stream):
     """Makes `device` and `stream` the current ones, so that allocations and launches go there."""
-    if stream is None and torch.cuda.current_device() == device.index:
+    if stream is None and _current_device() == device.index:
         return _here
     return _other(device, stream)
 
 
-# the current stream's handle without a Stream object around it (a call costs a few microseconds of host
-# time in all, which is what small products take on the GPU)
+# the current device and the current stream's handle without a Stream object around it (a call costs a few microseconds of host
+# time in all, which is what small products take on the GPU); there are tensors on a device by then, so torch is initialised
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _current():
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
