@@ -1,10 +1,12 @@
 """Build the HIP libraries in-tree for gfx950 with hipcc: libmxfp4.so (the quantizers, GEMMs and
 C ABI), libmxfp4_train.so (8-bit products, the head's loss, the orthogonalised update),
 libmxfp4_layer.so (RMS norm, gated activation, the gradients' norm) and libmxfp4_ceiling.so (the HBM and matrix-core ceiling kernels the benchmark reports)."""
+import concurrent.futures
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -15,7 +17,7 @@ TRAIN_LIB = os.path.join(HERE, "libmxfp4_train.so")
 TRAIN_SOURCES = ["train_api.cpp", "fp8.hip", "xent.hip", "ortho.hip"]
 TRAIN_HEADERS = ["internal.h", "mx_device.h", "fp8_device.h", "host_checks.h", "slab_gemm.h", "train_internal.h"]
 LAYER_LIB = os.path.join(HERE, "libmxfp4_layer.so")
-LAYER_SOURCES = ["layer_api.cpp", "norm.hip", "gate.hip", "clip.hip"]
+LAYER_SOURCES = ["layer_api.cpp", "norm.hip", "norm_grad.hip", "gate.hip", "clip.hip"]
 LAYER_HEADERS = ["internal.h", "mx_device.h", "fp8_device.h", "host_checks.h", "layer_device.h", "layer_internal.h",
                  "train_internal.h"]
 CEILING_LIB = os.path.join(HERE, "libmxfp4_ceiling.so")
@@ -52,11 +54,20 @@ def is_stale() -> bool:
 
 
 def _compile(sources, out, verbose):
+    """The sources to objects, side by side, and those to a library."""
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + HIPCC_FLAGS + [os.path.join(CSRC, s) for s in sources] + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory() as folder:
+        objects = [os.path.join(folder, s + ".o") for s in sources]
+        compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+        with concurrent.futures.ThreadPoolExecutor(4) as pool:
+            list(pool.map(lambda so: run([hipcc()] + compile_flags + ["-c", os.path.join(CSRC, so[0]), "-o", so[1]]),
+                          zip(sources, objects)))
+        run([hipcc(), "--offload-arch=gfx950", "-shared"] + objects + ["-o", tmp])
     os.replace(tmp, out)
 
 

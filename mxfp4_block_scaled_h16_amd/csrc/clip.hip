@@ -21,7 +21,6 @@ namespace {
 constexpr int kTensors = 128;                   // a launch's tensors (28 bytes each of a kernel's 4 KB of arguments)
 constexpr int64_t kPiece = 8192;                // values that a workgroup of 256 threads works at a time
 constexpr int64_t kMostBlocks = 256;            // workgroups of a launch, and so partial sums
-constexpr int64_t kLastCache = (int64_t)256 << 20;
 
 struct Tensors {
     const void *g[kTensors];
@@ -180,7 +179,7 @@ hipError_t launch_scale(const GradItem *items, int64_t n, const double *part, in
 {
     int64_t bytes = 0;
     for (int64_t i = 0; i < n; ++i) bytes += items[i].count * ((items[i].f32 ? 4 : 2) + (items[i].out_f32 ? 4 : 2));
-    const auto kernel = bytes > kLastCache ? scale_kernel<true> : scale_kernel<false>;
+    const auto kernel = bytes > kStreamBytes ? scale_kernel<true> : scale_kernel<false>;
     // the launches too go from the last tensors to the first
     std::vector<int64_t> starts;
     Tensors t;

@@ -91,12 +91,12 @@ __device__ __forceinline__ void gate_tile(const Gate &p, int64_t tm, int64_t tn,
                 uint32_t s;
                 const u32x2 w = row_codes(v[k][i], s);
                 if (FULL || row0 + i < p.rows) {
-                    *reinterpret_cast<u32x2 *>(q + i * p.q1[k].ldq) = w;
+                    store_codes<NT>(w, q + i * p.q1[k].ldq);
                     if (cg == 0) to[i * p.q1[k].lds] = (uint8_t)s;
                 }
             }
         }
-        if (p.q0[k].q) store_tile_columns(p.q0[k], tm, tn, FULL ? INT64_MAX : p.cols, v[k], sh);
+        if (p.q0[k].q) store_tile_columns<false>(p.q0[k], tm, tn, FULL ? INT64_MAX : p.cols, v[k], sh);
     }
 }
 
@@ -111,11 +111,9 @@ __global__ __launch_bounds__(512, GRAD || F32 ? 4 : 6) void gate_kernel(Gate p, 
         gate_tile<GRAD, DF32, F32, NT, false>(p, tm, tn, sh);
 }
 
-// Where inputs and outputs are more than the last cache holds, the inputs' loads do not stay in it: 8192 x 14336 (704 MB) 142 ->
-// 121 us, 4096 x 14336 71 -> 63; where they fit, the input is mostly still there from the product that wrote it:
-// 2048 x 14336 (176 MB) 30 us, and 34 with such loads.
-constexpr int64_t kLastCache = (int64_t)256 << 20;
-
+// Streaming loads, and stores of the codes along the rows, where the call is more than the last cache takes: 4096 x 14336 (352 MB)
+// 73 -> 64 us, 8192 x 14336 141 -> 121, the gradient 126 -> 111 and 246 -> 236; at 1024 x 14336 (88 MB) 18.6 and 19.7. Such
+// stores of the codes along the columns as well: 151 and 268.
 template <bool GRAD, bool DF32, bool F32>
 hipError_t run(const Gate &p, hipStream_t stream)
 {
@@ -123,7 +121,7 @@ hipError_t run(const Gate &p, hipStream_t stream)
     const dim3 grid((unsigned)((p.rows + 127) / 128 * tiles_n)), block(512);
     int64_t bytes = (F32 ? 8 : 4) + (GRAD ? DF32 ? 4 : 2 : 0);
     for (int k = 0; k < 2; ++k) bytes += (p.out[k].p ? p.out_f32 ? 4 : 2 : 0) + (p.q1[k].q ? 1 : 0) + (p.q0[k].q ? 1 : 0);
-    return p.rows * p.cols > kLastCache / bytes ? launch(gate_kernel<GRAD, DF32, F32, true>, grid, block, 0, stream, p, (int)tiles_n)
+    return p.rows * p.cols > kStreamBytes / bytes ? launch(gate_kernel<GRAD, DF32, F32, true>, grid, block, 0, stream, p, (int)tiles_n)
                                                 : launch(gate_kernel<GRAD, DF32, F32, false>, grid, block, 0, stream, p, (int)tiles_n);
 }
 

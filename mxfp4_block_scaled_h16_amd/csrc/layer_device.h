@@ -229,14 +229,23 @@ __device__ __forceinline__ u32x2 row_codes(const float (&v)[8], uint32_t &s)
     const float scale = __uint_as_float(s << 23);
     return u32x2{divide4(v[0], v[1], v[2], v[3], scale), divide4(v[4], v[5], v[6], v[7], scale)};
 }
+template <bool NT>
+__device__ __forceinline__ void store_codes(const u32x2 &w, uint8_t *to)
+{
+    if constexpr (NT)
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x2 *>(to));
+    else
+        *reinterpret_cast<u32x2 *>(to) = w;
+}
 // The same, written: col a multiple of 8, the block's first lane at a multiple of 128; zeros behind the row's end up to the
 // block's.
+template <bool NT>
 __device__ __forceinline__ void store_row_codes(const Fp8Out &out, int64_t row, int64_t col, int64_t cols, const float (&v)[8])
 {
     uint32_t s;
     const u32x2 w = row_codes(v, s);
     if ((col & ~(int64_t)127) >= cols) return;
-    *reinterpret_cast<u32x2 *>(out.q + row * out.ldq + col) = w;
+    store_codes<NT>(w, out.q + row * out.ldq + col);
     if ((col & 127) == 0) out.s[row * out.lds + (col >> 7)] = (uint8_t)s;
 }
 
@@ -264,6 +273,7 @@ struct TileShared {
 
 // tm, tn: the tile's place. Values behind the matrix' ends are zeros. Every thread of the workgroup calls it, and may do so
 // again at once: what a call still reads behind its last barrier, the next one writes behind its first.
+template <bool NT>
 __device__ __forceinline__ void store_tile_columns(const Fp8Out &out, int64_t tm, int64_t tn, int64_t cols,
                                                    const float (&v)[4][8], TileShared &sh)
 {
@@ -316,8 +326,12 @@ __device__ __forceinline__ void store_tile_columns(const Fp8Out &out, int64_t tm
         const int col = 64 * p + (tid >> 3), chunk = tid & 7;
         const int64_t outer = tn * 128 + col;
         if (outer >= cols) continue;
-        *reinterpret_cast<u32x4 *>(out.q + outer * out.ldq + tm * 128 + 16 * chunk) =
-            *reinterpret_cast<const u32x4 *>(sh.turned + col * 128 + 16 * (chunk ^ ((col >> 3) & 7)));
+        const u32x4 w = *reinterpret_cast<const u32x4 *>(sh.turned + col * 128 + 16 * (chunk ^ ((col >> 3) & 7)));
+        u32x4 *to = reinterpret_cast<u32x4 *>(out.q + outer * out.ldq + tm * 128 + 16 * chunk);
+        if constexpr (NT)
+            __builtin_nontemporal_store(w, to);
+        else
+            *to = w;
         if (chunk == 0) out.s[outer * out.lds + tm] = (uint8_t)(sh.scale[col] >> 23);
     }
 }

@@ -19,6 +19,10 @@ struct OutRows {
 // tiles of 128 x 128 that a grid holds, 512 threads each
 constexpr int64_t kLayerTiles = kMaxItems / 512;
 
+// A call that reads and writes more than this goes past the caches where it can: the last one holds 256 MB, and something of the
+// call before and behind stays in it.
+constexpr int64_t kStreamBytes = (int64_t)192 << 20;
+
 // ------------------------------------------------------------------------------- RMS norm -----
 struct NormForward {
     Rows x, r;              // r.p == nullptr: h = x
