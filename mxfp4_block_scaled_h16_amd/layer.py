@@ -193,7 +193,7 @@ def rmsnorm_forward(x, weight=None, residual=None, eps=1e-5, axis=None, y_dtype=
     false), rstd FP32 [T], y of y_dtype (None: not formed) and the 8-bit outputs that `axis` asks for.
 
     x, residual and weight [K] bf16 or f32 each. `h` may be given, also residual itself (or x, the types being the same), and is
-    then updated in place; so may y. Codes along the columns need h."""
+    then updated in place; a y that is given overlaps no input. Codes along the columns need h."""
     device = _device("x weight residual h y", x, weight, residual, h, y)
     ldx = _first(x, "x")
     rows, cols = shape = x.shape
@@ -385,10 +385,10 @@ def _grads(grads, out):
     # one question to all tensors at a time, in half the time of a loop over them; where one is not as usual, each by itself
     try:
         usual = {index} == set(map(_T.get_device, grads)) and index >= 0 and all(map(_T.is_contiguous, grads))
-        counts = array.array("q", map(_T.numel, grads))
+        counts = list(map(_T.numel, grads))
         if usual and outs is not grads:
             usual = ({index} == set(map(_T.get_device, outs)) and all(map(_T.is_contiguous, outs))
-                     and counts == array.array("q", map(_T.numel, outs)))
+                     and counts == list(map(_T.numel, outs)))
         types = list(map(_TYPES.get, zip(map(_dtype, grads), map(_dtype, outs))))
     except (AttributeError, TypeError):
         usual, types = False, [None]
@@ -396,9 +396,9 @@ def _grads(grads, out):
         for g, o in zip(grads, outs):
             _check_grad(g, o, index)
     items = array.array("q", bytes(32 * len(grads)))
-    items[0::4] = array.array("q", map(_T.data_ptr, grads))
-    items[1::4] = items[0::4] if outs is grads else array.array("q", map(_T.data_ptr, outs))
-    items[2::4] = counts
+    items[0::4] = array.array("q", list(map(_T.data_ptr, grads)))
+    items[1::4] = items[0::4] if outs is grads else array.array("q", list(map(_T.data_ptr, outs)))
+    items[2::4] = array.array("q", counts)
     items[3::4] = array.array("q", types)
     return grads[0].device, items, len(grads)
 
