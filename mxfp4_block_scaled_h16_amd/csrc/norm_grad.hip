@@ -213,7 +213,17 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float *part, int co
         static_cast<uint16_t *>(dw)[col] = (uint16_t)bf16_pair(sum, 0.0f);
 }
 
-int64_t grad_blocks(int64_t rows) { return std::min<int64_t>(rows, kGradBlocks); }
+// How the rows are shared out: as many at a time as pick_backward's kernels take, every workgroup having some, so that every
+// partial sum is written.
+struct Shares {
+    int64_t blocks, rows;   // rows of a workgroup, the last one's fewer
+};
+Shares shares(int64_t rows, int64_t cols)
+{
+    const int64_t at_once = cols <= 512 ? 8 : cols <= 1024 ? 4 : cols <= 2048 ? 2 : 1;
+    const int64_t groups = (rows + at_once - 1) / at_once, each = std::max<int64_t>((groups + kGradBlocks - 1) / kGradBlocks, 1);
+    return {(groups + each - 1) / each, each * at_once};
+}
 
 template <bool BF32, bool SF32, bool RAGGED, bool NT>
 hipError_t pick_backward(const BackwardArgs &args, unsigned blocks, hipStream_t stream)
@@ -223,7 +233,7 @@ hipError_t pick_backward(const BackwardArgs &args, unsigned blocks, hipStream_t 
     if (cols <= 512) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 64, 1, 8>, 512);
     if (cols <= 1024) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 128, 1, 4>, 512);
     if (cols <= 2048) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 256, 1, 2>, 512);
-    if (cols <= 4096) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 512, 1, 1>, 512 * 1);
+    if (cols <= 4096) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 512, 1, 1>, 512);
     if (cols <= 8192) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 1024, 1, 1>, 1024);
     if (cols <= 16384) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 1024, 2, 1>, 1024);
     return run(norm_backward_long_kernel<BF32, SF32>, 1024);
@@ -244,13 +254,12 @@ hipError_t backward(const BackwardArgs &args, unsigned blocks, hipStream_t strea
 
 size_t norm_backward_workspace_bytes(int64_t rows, int64_t cols)
 {
-    return (size_t)(grad_blocks(rows) * cols) * sizeof(float);
+    return (size_t)(shares(rows, cols).blocks * cols) * sizeof(float);
 }
 
 hipError_t launch_norm_backward(const NormBackward &p, void *ws, hipStream_t stream)
 {
-    // every workgroup has a row, and so every partial sum is written
-    const int64_t per = p.rows ? (p.rows + grad_blocks(p.rows) - 1) / grad_blocks(p.rows) : 1, blocks = (p.rows + per - 1) / per;
+    const auto [blocks, per] = shares(p.rows, p.cols);
     if (blocks > 0) {
         const BackwardArgs args{p, static_cast<float *>(ws), (float)(1.0 / (double)p.cols), per};
         hipError_t e;
