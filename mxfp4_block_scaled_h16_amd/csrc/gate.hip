@@ -5,10 +5,10 @@
 //
 // One pass: a workgroup works a tile of 128 x 128 values, which holds whole blocks along both axes, in registers.
 //
-// Bound by memory. 8192 x 14336 in bf16 with codes along both axes: forward 122 us (704 MB, 5.8 TB/s), the gradient 241 (1174 MB,
-// 4.9 TB/s; a kernel that only reads and writes as many streams 206 to 222). The scale bytes, one to a line, are 11 us of the
-// gradient's, the turning of the codes 2; more wavefronts (1024 threads of half the values, up to eight a SIMD) made
-// it 266, one pass through the LDS for both gradients no difference.
+// Bound by memory. 8192 x 14336 in bf16 with codes along both axes: forward 121 to 125 us (704 MB, 5.7 TB/s; a kernel that only
+// reads and writes as many streams 117 to 134), the gradient 236 (1174 MB, 5.0 TB/s; such a kernel 206 to 222). The scale bytes, one
+// to a line, are 11 us of the gradient's, the turning of the codes 2; more wavefronts (1024 threads of half the values, up
+// to eight a SIMD) made it 266, one pass through the LDS for both gradients no difference.
 #include <cfloat>
 
 #include "internal.h"

@@ -4,7 +4,8 @@
 //
 // in FP32, dh as rstd (u - n mean_k(u_k n_k)) + dres with n = h rstd.
 //
-// Bound by memory: 8192 x 4096 in bf16 with dres 52 us for 268 MB (5.1 TB/s, a copy's rate), the joining of dw (3 us) included.
+// Bound by memory: 8192 x 4096 in bf16 with dres 52 to 54 us for 268 MB (a copy of as much 53), 50 in the rows' kernel and 5 to join dw.
+// Small calls are two launches: 16 x 8192 6.6 us, 1024 x 1024 6.9.
 #include <algorithm>
 
 #include "internal.h"
