@@ -171,25 +171,26 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(ForwardArgs arg
     }
 }
 
-// The codes along the columns, in tiles: a block's 128 rows need their rstd first.
-template <bool SF32, bool RAGGED, bool NT>
-__global__ __launch_bounds__(512) void norm_columns_kernel(NormForward p, Rows h, int tiles_n)
+// The codes along the columns, in tiles: a block's 128 rows need their rstd first. FULL: the tile lies inside the matrix.
+template <bool SF32, bool NT, bool FULL>
+__device__ __forceinline__ void norm_tile(const NormForward &p, const Rows &h, int64_t tm, int64_t tn, TileShared &sh)
 {
-    __shared__ TileShared sh;
-    const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
-    const int64_t tm = blockIdx.x / (unsigned)tiles_n, tn = blockIdx.x % (unsigned)tiles_n;
+    const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int64_t row0 = tm * 128 + 4 * rg, col0 = tn * 128 + 8 * cg;
+    const void *at0 = at<SF32>(h.p, row0 * h.ld);
     Raw8<SF32> raw[4];
     float rstd[4], w[8], v[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const bool in = row0 + i < p.rows;
-        raw[i].zero();
-        if (in) raw[i] = load_raw<SF32, RAGGED>(at<SF32>(h.p, (row0 + i) * h.ld), col0, p.cols);
+        const bool in = FULL || row0 + i < p.rows;
+        if constexpr (FULL)
+            raw[i].template load<false>(at<SF32>(at0, i * h.ld + col0));
+        else
+            raw[i] = load_raw<SF32, true>(at<SF32>(at0, i * h.ld), col0, in ? p.cols : 0);
         rstd[i] = in ? p.rstd[row0 + i] : 0.0f;
     }
     if (p.w) {
-        load_any<RAGGED>(p.w_f32, p.w, col0, p.cols, w);
+        load_any<!FULL>(p.w_f32, p.w, col0, p.cols, w);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = 1.0f;
@@ -198,9 +199,20 @@ __global__ __launch_bounds__(512) void norm_columns_kernel(NormForward p, Rows h
     for (int i = 0; i < 4; ++i) {
         raw[i].get(v[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = row0 + i < p.rows ? v[i][e] * rstd[i] * w[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) v[i][e] = FULL || row0 + i < p.rows ? v[i][e] * rstd[i] * w[e] : 0.0f;
     }
-    store_tile_columns<NT>(p.q0, tm, tn, p.cols, v, sh);
+    store_tile_columns<NT>(p.q0, tm, tn, FULL ? INT64_MAX : p.cols, v, sh);
+}
+
+template <bool SF32, bool NT>
+__global__ __launch_bounds__(512) void norm_columns_kernel(NormForward p, Rows h, int tiles_n)
+{
+    __shared__ TileShared sh;
+    const int64_t tm = blockIdx.x / (unsigned)tiles_n, tn = blockIdx.x % (unsigned)tiles_n;
+    if ((tm + 1) * 128 <= p.rows && (tn + 1) * 128 <= p.cols)
+        norm_tile<SF32, NT, true>(p, h, tm, tn, sh);
+    else
+        norm_tile<SF32, NT, false>(p, h, tm, tn, sh);
 }
 
 // Bytes of a call with codes or without.
@@ -256,13 +268,12 @@ hipError_t launch_norm_forward(const NormForward &p, hipStream_t stream)
         e = p.s_f32 ? forward<false, true, true>(args, nt, stream) : forward<false, false, true>(args, nt, stream);
     if (e != hipSuccess || !p.q0.q) return e;
     const Rows h = res ? Rows{p.h.p, p.h.ld} : p.x;
-    const bool f32 = res ? p.s_f32 : p.x_f32, ragged = p.cols % 8 != 0;
+    const bool f32 = res ? p.s_f32 : p.x_f32;
     const int64_t tiles_n = (p.cols + 127) / 128;
     const dim3 grid((unsigned)((p.rows + 127) / 128 * tiles_n)), block(512);
     const auto run = [&](auto kernel) { return launch(kernel, grid, block, 0, stream, p, h, (int)tiles_n); };
-    if (ragged) return run(f32 ? norm_columns_kernel<true, true, false> : norm_columns_kernel<false, true, false>);
-    if (f32) return run(nt ? norm_columns_kernel<true, false, true> : norm_columns_kernel<true, false, false>);
-    return run(nt ? norm_columns_kernel<false, false, true> : norm_columns_kernel<false, false, false>);
+    if (f32) return run(nt ? norm_columns_kernel<true, true> : norm_columns_kernel<true, false>);
+    return run(nt ? norm_columns_kernel<false, true> : norm_columns_kernel<false, false>);
 }
 
 }  // namespace mx

@@ -128,7 +128,10 @@ def _device(names, first, *others):
                 return first.device
     except AttributeError:
         pass
-    return _same_device(**dict(zip(names.split(), (first,) + others)))
+    names = names.split()
+    if first is None:
+        raise TypeError("%s must be a tensor on a HIP device" % names[0])
+    return _same_device(**dict(zip(names, (first,) + others)))
 
 
 def _ld(t, shape, dtypes, name):

@@ -91,6 +91,59 @@ def test_strides_alignment_and_in_place(rows, cols):
     assert torch.equal(mx.rmsnorm_forward(tall[:1], w.cuda()).y, base.y[:1])
 
 
+@pytest.mark.parametrize("cols", [300, 2048, 4096, 20000])
+@pytest.mark.parametrize("branch,stream", [(BF, BF), (BF, F32), (F32, F32)])
+def test_without_keeping_the_sum(cols, branch, stream):
+    mx = _mx()
+    x, r, w = _data(6, cols, branch, stream)
+    full = mx.rmsnorm_forward(x.cuda(), w.cuda(), r.cuda(), EPS, axis=1)
+    o = mx.rmsnorm_forward(x.cuda(), w.cuda(), r.cuda(), EPS, axis=1, need_h=False)
+    assert o.h is None and torch.equal(o.y, full.y) and torch.equal(o.rstd, full.rstd) and torch.equal(o.q1, full.q1)
+    nb = (cols + 127) // 128
+    assert torch.equal(o.s1[:, :nb], full.s1[:, :nb])
+    twice = x.cuda().clone()                                    # x + x in place
+    o = mx.rmsnorm_forward(twice, w.cuda(), twice, EPS, h=twice)
+    assert torch.equal(twice.cpu(), norm_stream(x, x)) and torch.equal(o.y, mx.rmsnorm_forward(twice, w.cuda(), eps=EPS).y)
+
+
+@pytest.mark.parametrize("rows,cols", [(130, 700), (3, 4100), (2, 17000)])
+def test_blocks_of_tiny_values_and_of_zeros(rows, cols):
+    """Scale bytes of 0 (a block's maximum below 448 * 2^-127) beside ordinary ones, along both axes, and values below FP32's normal
+    range."""
+    mx = _mx()
+    x, _, w = _data(rows, cols, F32, F32)
+    w = w.float()
+    for k, scale in ((0, 2.0 ** -119), (1, 0.0), (2, 2.0 ** -126), (3, 2.0 ** -135), (4, 2.0 ** 100)):
+        w[128 * k:128 * k + 128] *= scale                       # whole blocks along the rows, and columns
+        w[128 * k + 5] = 2.0 ** -130
+    x[rows // 2] = 0.0
+    announce("norm tiny", rows, cols)
+    o = mx.rmsnorm_forward(x.cuda(), w.cuda(), eps=EPS, axis="both", y_dtype=F32)
+    y = norm_y32(x, o.rstd.cpu(), w)
+    assert torch.equal(o.y.cpu(), y)
+    check_axes(o, y, "both")
+    assert int((o.s1[:, :(cols + 127) // 128] == 0).sum()) > rows and bool((o.s0[:700, 0] == 0).any())
+
+
+def test_single_outputs_of_the_library():
+    """Each output alone, which the binding does not ask for: rstd, h, y."""
+    mx = _mx()
+    L = mx.layer_lib()
+    for cols in (512, 4096, 20000):
+        x, r, w = (t.cuda() for t in _data(5, cols, BF, BF))
+        full = mx.rmsnorm_forward(x, w, r, EPS)
+        h, y, rstd = torch.zeros_like(r), torch.zeros_like(x), torch.zeros(5, device="cuda")
+        stream = torch.cuda.current_stream().cuda_stream
+
+        def call(h=None, rstd=None, y=None):
+            at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+            return L.mxfp4_rmsnorm_forward(x.data_ptr(), 0, cols, r.data_ptr(), cols, 0, w.data_ptr(), 0, 5, cols, EPS, at(h), cols, at(rstd),
+                                           at(y), 1, cols, None, 0, None, 0, None, 0, None, 0, stream)
+        assert call(h=h) == 0 and torch.equal(h, full.h)
+        assert call(rstd=rstd) == 0 and torch.equal(rstd, full.rstd)
+        assert call(y=y) == 0 and torch.equal(y, full.y)
+
+
 def test_no_rows():
     mx = _mx()
     x, w = torch.zeros(0, 300, dtype=BF).cuda(), torch.ones(300).cuda()

@@ -113,6 +113,55 @@ def test_halves_strides_and_in_place():
             assert torch.equal((d[:, :cols], d[:, cols:])[k], base.a)
 
 
+@pytest.mark.parametrize("rows,cols", [(130, 256), (5, 300)])
+def test_single_outputs_of_the_library(rows, cols):
+    """Each gradient alone and each kind of codes of one of them, which the binding does not ask for."""
+    mx = _mx()
+    L = mx.layer_lib()
+    gate, up, da = _data(rows, cols, BF)
+    dev = da.to(BF).cuda(), gate.cuda(), up.cuda()
+    full = mx.swiglu_backward(*dev, axis="both", joined=False)
+    stream = torch.cuda.current_stream().cuda_stream
+    lq1, ls1, lq0, ls0 = full.gate.q1.stride(0), full.gate.s1.stride(0), full.gate.q0.stride(0), full.gate.s0.stride(0)
+
+    def call(dgate=None, dup=None, q1=(None, None), s1=(None, None), q0=(None, None), s0=(None, None)):
+        at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        status = L.mxfp4_swiglu_backward(at(dev[0]), 0, cols, at(dev[1]), cols, at(dev[2]), cols, 0, rows, cols, at(dgate), cols, at(dup), cols,
+                                         1, *map(at, q1), lq1, *map(at, s1), ls1, *map(at, q0), lq0, *map(at, s0), ls0, stream)
+        assert status == 0
+    new = lambda t: torch.full_like(t, 77)  # noqa: E731
+    for name in ("dgate", "dup"):
+        t = new(full.dgate)
+        call(**{name: t})
+        assert torch.equal(t, getattr(full, name))
+    for k, want in enumerate((full.gate, full.up)):
+        q, s = new(want.q1), new(want.s1)
+        call(q1=(q, None) if k == 0 else (None, q), s1=(s, None) if k == 0 else (None, s))
+        nb = (cols + 127) // 128
+        assert torch.equal(q, want.q1) and torch.equal(s[:, :nb], want.s1[:, :nb]) and bool((s[:, nb:] == 77).all())
+        q, s = new(want.q0), new(want.s0)
+        call(q0=(q, None) if k == 0 else (None, q), s0=(s, None) if k == 0 else (None, s))
+        nb = (rows + 127) // 128
+        assert torch.equal(q, want.q0) and torch.equal(s[:, :nb], want.s0[:, :nb]) and bool((s[:, nb:] == 77).all())
+
+
+@pytest.mark.parametrize("rows,cols", [(256, 384), (130, 700)])
+def test_blocks_of_tiny_values_and_of_zeros(rows, cols):
+    """Scale bytes of 0 beside ordinary ones, along both axes, in whole tiles and at the ends."""
+    mx = _mx()
+    gate, up, _ = _data(rows, cols, F32)
+    gate = gate.clamp(min=-5)
+    for k, scale in ((0, 2.0 ** -119), (1, 0.0), (2, 2.0 ** -126)):
+        up[:, 128 * k:128 * k + 100] *= scale
+    up[rows // 2], up[3, ::2] = 0.0, 2.0 ** -149
+    announce("gate tiny", rows, cols)
+    o = mx.swiglu_forward(gate.cuda(), up.cuda(), axis="both", out_dtype=F32)
+    check_axes(o, o.a.cpu(), "both")
+    exact = gate_forward(gate, up)
+    assert_within(o.a, exact, _own(gate) * exact.abs() + 2.0 ** -149)
+    assert bool((o.s0[:, 0] == 0).any()) and bool((o.s0[:, 0] > 0).any())
+
+
 def test_empty():
     mx = _mx()
     for shape in ((0, 300), (5, 0)):
