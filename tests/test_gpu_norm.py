@@ -271,3 +271,19 @@ def test_many_rows():
     g = mx.rmsnorm_backward(x, x, o.rstd)
     dw = (h * h * o.rstd.double()[:, None]).sum(dim=0)
     assert bool(((g.dweight.double() - dw).abs() <= U * (68 + rows / 64) * dw).all())
+
+
+def test_many_rows_of_several_wavefronts():
+    """A workgroup works several rows one after the other, each joined over its wavefronts."""
+    mx = _mx()
+    rows, cols = (1 << 20) + 3000, 1032
+    x = torch.randn(rows, cols, device="cuda").to(BF)
+    announce("norm rows", rows, cols)
+    o = mx.rmsnorm_forward(x, eps=EPS, axis=1)
+    for at in (0, 2990, (1 << 20) - 10, 1 << 20, rows - 20):     # rows of the first and of the second turn
+        p = mx.rmsnorm_forward(x[at:at + 20], eps=EPS, axis=1)
+        assert torch.equal(p.rstd, o.rstd[at:at + 20]) and torch.equal(p.y, o.y[at:at + 20]) and torch.equal(p.q1, o.q1[at:at + 20])
+    n = torch.zeros(rows, dtype=torch.float64, device="cuda")
+    for part, to in zip(x.split(1 << 17), n.split(1 << 17)):
+        to.copy_((part.double().square().mean(dim=1) + EPS).rsqrt())
+    assert bool(((o.rstd.double() - n).abs() <= n * U * 1.0001).all())

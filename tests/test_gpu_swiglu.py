@@ -169,6 +169,10 @@ def test_empty():
         o = mx.swiglu_forward(z, z, axis="both")
         assert o.a.shape == shape
         mx.swiglu_backward(z, z, z, axis="both", joined=False)
+        d = mx.swiglu_backward(z, z, z, axis=0)
+        assert d.q0.shape == (2 * shape[1], 0 if shape[0] == 0 else 128)
+    z = torch.zeros(0, 256, dtype=BF).cuda()
+    assert mx.swiglu_backward(z, z, z, axis="both").q1.shape == (0, 512)
 
 
 def test_ends_of_the_range():
