@@ -30,36 +30,46 @@ struct ForwardArgs {
     double inv_cols;
 };
 
-// TPR threads work a row of at most 8 C TPR values, held in registers from the load to the codes.
-template <bool XF32, bool SF32, bool RES, bool RAGGED, bool NT, int TPR, int C>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_forward_kernel(ForwardArgs args)
+// TPR threads work a row of at most 8 C TPR values, held in registers from the load to the codes: a wavefront (WAVE; four of them a
+// workgroup), or a workgroup of as many wavefronts as the row needs.
+template <bool XF32, bool SF32, bool RES, Ends E, bool NT, bool WAVE, int C>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void norm_forward_kernel(ForwardArgs args)
 {
-    constexpr int kThreads = TPR < 256 ? 256 : TPR, kRows = kThreads / TPR, kWaves = TPR / 64;
-    __shared__ double part[2][kWaves];
+    constexpr int kRows = WAVE ? 4 : 1;
+    __shared__ double part[2][16];
     const NormForward &p = args.p;
-    const int lane = (int)threadIdx.x % TPR;
+    const int TPR = WAVE ? 64 : (int)blockDim.x, lane = WAVE ? (int)threadIdx.x % 64 : (int)threadIdx.x;
     float w[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         if (p.w) {
-            load_any<RAGGED>(p.w_f32, p.w, (c * TPR + lane) * 8, p.cols, w[c]);
+            load_any<E != kWhole>(p.w_f32, p.w, (c * TPR + lane) * 8, p.cols, w[c]);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[c][e] = 1.0f;
         }
     }
     int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * kRows + (int)threadIdx.x / TPR; row < p.rows;
+    for (int64_t row = (int64_t)blockIdx.x * kRows + (WAVE ? (int)threadIdx.x / 64 : 0); row < p.rows;
          row += (int64_t)gridDim.x * kRows) {
         Raw8<XF32> x[C];
         Raw8<SF32> s[C];
+        const auto eight = [&](int c) { return Eight<E>((c * TPR + lane) * 8, p.cols); };
+        const void *xr = at<XF32>(p.x.p, row * p.x.ld), *rr = at<SF32>(p.r.p, row * p.r.ld);
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            x[c] = load_raw<XF32, RAGGED, NT>(at<XF32>(p.x.p, row * p.x.ld), (c * TPR + lane) * 8, p.cols);
+        for (int c = 0; c < C; ++c) x[c] = eight(c).template load<XF32, NT>(xr);
         if constexpr (RES) {
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                s[c] = load_raw<SF32, RAGGED, NT>(at<SF32>(p.r.p, row * p.r.ld), (c * TPR + lane) * 8, p.cols);
+            for (int c = 0; c < C; ++c) s[c] = eight(c).template load<SF32, NT>(rr);
+        }
+        if constexpr (E == kWithin) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if (const int gone = eight(c).gone()) {
+                    x[c].drop(gone);
+                    if constexpr (RES) s[c].drop(gone);
+                }
+            }
         }
         float h[C][8];
         double sum = 0.0;
@@ -73,19 +83,18 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_forward_kernel(For
                 for (int e = 0; e < 8; ++e) r[e] += h[c][e];
                 s[c].set(r);
                 s[c].get(h[c]);
-                if (p.h.p) store_raw<SF32, RAGGED>(s[c], at<SF32>(p.h.p, row * p.h.ld), (c * TPR + lane) * 8, p.cols);
+                if (p.h.p) store_raw<SF32, E != kWhole>(s[c], at<SF32>(p.h.p, row * p.h.ld), (c * TPR + lane) * 8, p.cols);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum = fma((double)h[c][e], (double)h[c][e], sum);
         }
         sum = wave_sum(sum);
-        if constexpr (kWaves > 1) {
+        if constexpr (!WAVE) {
             // one barrier a row: the next row's sums go to the other half
             if ((lane & 63) == 0) part[turn][lane >> 6] = sum;
             __syncthreads();
             sum = part[turn][0];
-#pragma unroll
-            for (int i = 1; i < kWaves; ++i) sum += part[turn][i];
+            for (int i = 1; i < TPR / 64; ++i) sum += part[turn][i];
             turn ^= 1;
         }
         const float rstd = rsqrt64(fma(sum, args.inv_cols, (double)p.eps));
@@ -97,7 +106,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_forward_kernel(For
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = h[c][e] * rstd * w[c][e];
             if (p.y.p)
-                store_any<RAGGED>(p.y_f32, y, p.y_f32 ? at<true>(p.y.p, row * p.y.ld) : at<false>(p.y.p, row * p.y.ld), col, p.cols);
+                store_any<E != kWhole>(p.y_f32, y, p.y_f32 ? at<true>(p.y.p, row * p.y.ld) : at<false>(p.y.p, row * p.y.ld), col, p.cols);
             if (p.q1.q) store_row_codes<NT>(p.q1, row, col, p.cols, y);
         }
     }
@@ -222,35 +231,32 @@ int64_t forward_bytes(const NormForward &p)
     return p.rows * p.cols * (x + (p.r.p ? s : 0) + (p.h.p ? s : 0) + (p.y.p ? p.y_f32 ? 4 : 2 : 0) + (p.q1.q ? 1 : 0) + (p.q0.q ? 1 : 0));
 }
 
-template <bool XF32, bool SF32, bool RES, bool RAGGED, bool NT, int TPR, int C>
-hipError_t run_forward(const ForwardArgs &args, hipStream_t stream)
-{
-    constexpr int kThreads = TPR < 256 ? 256 : TPR, kRows = kThreads / TPR;
-    const int64_t blocks = std::min<int64_t>((args.p.rows + kRows - 1) / kRows, (int64_t)1 << 20);
-    return launch(norm_forward_kernel<XF32, SF32, RES, RAGGED, NT, TPR, C>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, args);
-}
-// Threads of a row: 4096 columns in 256 threads of 16 values 57 us (8192 rows, with the codes along the columns), in 512 of 8 59, in
-// 128 of 32 59, in 64 of 64, which need no barrier, 73.
-template <bool XF32, bool SF32, bool RES, bool RAGGED, bool NT>
+template <bool XF32, bool SF32, bool RES, Ends E, bool NT>
 hipError_t pick_forward(const ForwardArgs &args, hipStream_t stream)
 {
-    const int64_t cols = args.p.cols;
-    if (cols <= 512) return run_forward<XF32, SF32, RES, RAGGED, NT, 64, 1>(args, stream);
-    if (cols <= 1024) return run_forward<XF32, SF32, RES, RAGGED, NT, 64, 2>(args, stream);
-    if (cols <= 2048) return run_forward<XF32, SF32, RES, RAGGED, NT, 256, 1>(args, stream);
-    if (cols <= 4096) return run_forward<XF32, SF32, RES, RAGGED, NT, 256, 2>(args, stream);
-    if (cols <= 8192) return run_forward<XF32, SF32, RES, RAGGED, NT, 512, 2>(args, stream);
-    if (cols <= 16384) return run_forward<XF32, SF32, RES, RAGGED, NT, 1024, 2>(args, stream);
-    const int64_t blocks = std::min<int64_t>(args.p.rows, (int64_t)1 << 20);
-    return launch(norm_forward_long_kernel<XF32, SF32, RES>, dim3((unsigned)blocks), dim3(1024), 0, stream, args);
+    const int64_t rows = args.p.rows, cols = args.p.cols, most = (int64_t)1 << 20;
+    const auto run = [&](auto kernel, int64_t blocks, int64_t threads) {
+        return launch(kernel, dim3((unsigned)std::min(blocks, most)), dim3((unsigned)threads), 0, stream, args);
+    };
+    if (E == kFew || cols <= 512) return run(norm_forward_kernel<XF32, SF32, RES, E, NT, true, 1>, (rows + 3) / 4, 256);
+    if constexpr (E != kFew) {
+        if (cols <= 1024) return run(norm_forward_kernel<XF32, SF32, RES, E, NT, true, 2>, (rows + 3) / 4, 256);
+        // 16 values a thread: 4096 columns (8192 rows, codes along both axes) 57 us, with 8 values 59, with 32 59, in one wavefront, which
+        // needs no barrier, 73
+        if (cols <= 16384) return run(norm_forward_kernel<XF32, SF32, RES, E, NT, false, 2>, rows, (cols + 1023) / 1024 * 64);
+    }
+    return run(norm_forward_long_kernel<XF32, SF32, RES>, rows, 1024);
 }
 // Streaming loads of x and r and stores of the codes, where the call is more than the last cache takes: 8192 x 4096 (268 MB) 62 ->
-// 58 us, 16384 x 4096 130 -> 106; 4096 x 4096 (134 MB) 32.7 and 32.2, 2048 x 4096 in FP32 (101 MB) 26 and 29.
+// 58 us, 16384 x 4096 130 -> 106; 4096 x 4096 (134 MB) 32.7 and 32.2, 2048 x 4096 in FP32 (101 MB) 26 and 29. They are for rows
+// of whole 16 bytes: a line that two loads share is read twice (15232 x 5627 202 us, and 212 with them).
 template <bool XF32, bool SF32, bool RES>
 hipError_t forward(const ForwardArgs &args, bool nt, hipStream_t stream)
 {
-    if (args.p.cols % 8) return pick_forward<XF32, SF32, RES, true, false>(args, stream);
-    return nt ? pick_forward<XF32, SF32, RES, false, true>(args, stream) : pick_forward<XF32, SF32, RES, false, false>(args, stream);
+    const int64_t cols = args.p.cols;
+    if (cols % 8)
+        return cols < 8 ? pick_forward<XF32, SF32, RES, kFew, false>(args, stream) : pick_forward<XF32, SF32, RES, kWithin, false>(args, stream);
+    return nt ? pick_forward<XF32, SF32, RES, kWhole, true>(args, stream) : pick_forward<XF32, SF32, RES, kWhole, false>(args, stream);
 }
 
 }  // namespace

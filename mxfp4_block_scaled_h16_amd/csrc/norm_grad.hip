@@ -23,23 +23,42 @@ struct BackwardArgs {
     int64_t rows_per_block;
 };
 
-template <bool BF32, bool SF32, int C>
+template <bool BF32, bool SF32, Ends E, int TPR, int C>
 struct GradRow {
     Raw8<BF32> dy[C];
     Raw8<SF32> h[C], dres[C];
     float rstd;
 
-    template <bool RAGGED, bool NT, int TPR>
+    static __device__ __forceinline__ Eight<E> eight(const NormBackward &p, int c, int lane) { return {(c * TPR + lane) * 8, p.cols}; }
+
+    // A row behind the end is read as the last one, or not at all; settle() makes zeros of it (dh may be dres, and the last row be
+    // written meanwhile: nothing of what is read here is used then).
+    template <bool NT>
     __device__ __forceinline__ void load(const NormBackward &p, int64_t row, int64_t end, int lane)
     {
-        const bool in = row < end;
-        rstd = in ? p.rstd[row] : 0.0f;
+        row = min(row, end - 1);
+        rstd = p.rstd[row];
+        const void *at_dy = at<BF32>(p.dy.p, row * p.dy.ld), *at_h = at<SF32>(p.h.p, row * p.h.ld), *at_dres = at<SF32>(p.dres.p, row * p.dres.ld);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t col = in ? (c * TPR + lane) * 8 : p.cols;      // behind the row: zeros
-            dy[c] = load_raw<BF32, RAGGED, NT>(at<BF32>(p.dy.p, row * p.dy.ld), col, p.cols);
-            h[c] = load_raw<SF32, RAGGED, NT>(at<SF32>(p.h.p, row * p.h.ld), col, p.cols);
-            dres[c] = load_raw<SF32, RAGGED, NT>(at<SF32>(p.dres.p, row * p.dres.ld), p.dres.p ? col : p.cols, p.cols);
+            dy[c] = eight(p, c, lane).template load<BF32, NT>(at_dy);
+            h[c] = eight(p, c, lane).template load<SF32, NT>(at_h);
+            if (p.dres.p)
+                dres[c] = eight(p, c, lane).template load<SF32, NT>(at_dres);
+            else
+                dres[c].zero();
+        }
+    }
+    __device__ __forceinline__ void settle(const NormBackward &p, bool in, int lane)
+    {
+        if (!in) rstd = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (const int gone = in ? eight(p, c, lane).gone() : 8) {
+                dy[c].drop(gone);
+                h[c].drop(gone);
+                dres[c].drop(gone);
+            }
         }
     }
 };
@@ -47,7 +66,7 @@ struct GradRow {
 // A workgroup works rows_per_block rows, ROWS of them at a time in TPR threads each, and keeps its sum of dw in registers until
 // the end. With eight values a thread (C = 1) the next rows' loads are under way meanwhile: at 8192 x 4096 the kernel and the
 // joining of dw take 56 us with them, 75 with 16 values a thread in 256 and no such loads (58 with them, in 162 registers).
-template <bool BF32, bool SF32, bool RAGGED, bool NT, int TPR, int C, int ROWS>
+template <bool BF32, bool SF32, Ends E, bool NT, int TPR, int C, int ROWS>
 __global__ __launch_bounds__(TPR *ROWS) void norm_backward_kernel(BackwardArgs args)
 {
     constexpr int kWaves = TPR / 64;
@@ -59,7 +78,7 @@ __global__ __launch_bounds__(TPR *ROWS) void norm_backward_kernel(BackwardArgs a
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         if (p.w) {
-            load_any<RAGGED>(p.w_f32, p.w, (c * TPR + lane) * 8, p.cols, w[c]);
+            load_any<E != kWhole>(p.w_f32, p.w, (c * TPR + lane) * 8, p.cols, w[c]);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[c][e] = 1.0f;
@@ -68,14 +87,16 @@ __global__ __launch_bounds__(TPR *ROWS) void norm_backward_kernel(BackwardArgs a
         for (int e = 0; e < 8; ++e) dw[c][e] = 0.0f;
     }
     const int64_t first = (int64_t)blockIdx.x * args.rows_per_block, end = min(first + args.rows_per_block, p.rows);
-    GradRow<BF32, SF32, C> next;
-    if constexpr (C == 1) next.template load<RAGGED, NT, TPR>(p, first + slot, end, lane);
+    GradRow<BF32, SF32, E, TPR, C> next;
+    if constexpr (C == 1) next.template load<NT>(p, first + slot, end, lane);
     int turn = 0;
     for (int64_t base = first; base < end; base += ROWS) {
         const int64_t row = base + slot;
-        if constexpr (C > 1) next.template load<RAGGED, NT, TPR>(p, row, end, lane);
-        GradRow<BF32, SF32, C> r = next;
-        if constexpr (C == 1) next.template load<RAGGED, NT, TPR>(p, row + ROWS, end, lane);
+        if constexpr (C > 1) next.template load<NT>(p, row, end, lane);
+        GradRow<BF32, SF32, E, TPR, C> r = next;
+        if constexpr (C == 1)
+            if (__builtin_amdgcn_readfirstlane((int)(row + ROWS < end))) next.template load<NT>(p, row + ROWS, end, lane);
+        r.settle(p, row < end, lane);
         float sum = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -112,7 +133,7 @@ __global__ __launch_bounds__(TPR *ROWS) void norm_backward_kernel(BackwardArgs a
             for (int e = 0; e < 8; ++e) d[e] = fmaf(fmaf(-(b[e] * r.rstd), mean, a[e] * w[c][e]), r.rstd, d[e]);
             Raw8<SF32> out;
             out.set(d);
-            store_raw<SF32, RAGGED>(out, at<SF32>(p.dh.p, row * p.dh.ld), (c * TPR + lane) * 8, p.cols);
+            store_raw<SF32, E != kWhole>(out, at<SF32>(p.dh.p, row * p.dh.ld), (c * TPR + lane) * 8, p.cols);
         }
     }
     if (!p.dw) return;
@@ -137,7 +158,7 @@ __global__ __launch_bounds__(TPR *ROWS) void norm_backward_kernel(BackwardArgs a
             }
             __syncthreads();
         }
-        if (slot == 0) store_any<RAGGED>(true, dw[c], to, (c * TPR + lane) * 8, p.cols);
+        if (slot == 0) store_any<E != kWhole>(true, dw[c], to, (c * TPR + lane) * 8, p.cols);
     }
 }
 
@@ -226,29 +247,32 @@ Shares shares(int64_t rows, int64_t cols)
     return {(groups + each - 1) / each, each * at_once};
 }
 
-template <bool BF32, bool SF32, bool RAGGED, bool NT>
+template <bool BF32, bool SF32, Ends E, bool NT>
 hipError_t pick_backward(const BackwardArgs &args, unsigned blocks, hipStream_t stream)
 {
     const int64_t cols = args.p.cols;
     const auto run = [&](auto kernel, int threads) { return launch(kernel, dim3(blocks), dim3(threads), 0, stream, args); };
-    if (cols <= 512) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 64, 1, 8>, 512);
-    if (cols <= 1024) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 128, 1, 4>, 512);
-    if (cols <= 2048) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 256, 1, 2>, 512);
-    if (cols <= 4096) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 512, 1, 1>, 512);
-    if (cols <= 8192) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 1024, 1, 1>, 1024);
-    if (cols <= 16384) return run(norm_backward_kernel<BF32, SF32, RAGGED, NT, 1024, 2, 1>, 1024);
+    if (E == kFew || cols <= 512) return run(norm_backward_kernel<BF32, SF32, E, NT, 64, 1, 8>, 512);
+    if constexpr (E != kFew) {
+        if (cols <= 1024) return run(norm_backward_kernel<BF32, SF32, E, NT, 128, 1, 4>, 512);
+        if (cols <= 2048) return run(norm_backward_kernel<BF32, SF32, E, NT, 256, 1, 2>, 512);
+        if (cols <= 4096) return run(norm_backward_kernel<BF32, SF32, E, NT, 512, 1, 1>, 512);
+        if (cols <= 8192) return run(norm_backward_kernel<BF32, SF32, E, NT, 1024, 1, 1>, 1024);
+        if (cols <= 16384) return run(norm_backward_kernel<BF32, SF32, E, NT, 1024, 2, 1>, 1024);
+    }
     return run(norm_backward_long_kernel<BF32, SF32>, 1024);
 }
 // Streaming loads where the call is more than the last cache takes: 8192 x 4096 (268 MB) 60 -> 52 us, 16384 x 4096 110 -> 98; 4096 x
-// 4096 (134 MB) 30 both ways, 2048 x 4096 18 and 23.
+// 4096 (134 MB) 30 both ways, 2048 x 4096 18 and 23. Rows of whole 16 bytes only: a line that two loads share is read twice.
 template <bool BF32, bool SF32>
 hipError_t backward(const BackwardArgs &args, unsigned blocks, hipStream_t stream)
 {
     const NormBackward &p = args.p;
-    if (p.cols % 8) return pick_backward<BF32, SF32, true, false>(args, blocks, stream);
     const int64_t bytes = p.rows * p.cols * ((BF32 ? 4 : 2) + (SF32 ? 4 : 2) * (p.dres.p ? 3 : 2));
-    return bytes > kStreamBytes ? pick_backward<BF32, SF32, false, true>(args, blocks, stream)
-                                : pick_backward<BF32, SF32, false, false>(args, blocks, stream);
+    if (p.cols % 8)
+        return p.cols < 8 ? pick_backward<BF32, SF32, kFew, false>(args, blocks, stream) : pick_backward<BF32, SF32, kWithin, false>(args, blocks, stream);
+    return bytes > kStreamBytes ? pick_backward<BF32, SF32, kWhole, true>(args, blocks, stream)
+                                : pick_backward<BF32, SF32, kWhole, false>(args, blocks, stream);
 }
 
 }  // namespace

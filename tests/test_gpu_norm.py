@@ -11,7 +11,7 @@ EPS = 1e-5
 TYPES = [(BF, BF), (BF, F32), (F32, F32), (F32, BF)]        # branch, stream
 # a single value, less than eight, ends inside eight and inside a block, every way of working a row, and rows too long for registers
 SIZES = [(1, 1), (3, 7), (1, 4096), (5, 129), (130, 384), (2, 512), (7, 513), (129, 1000), (3, 1024), (2, 1100), (9, 2001), (3, 2056),
-         (300, 256), (5, 4097), (2, 8200), (3, 16384), (2, 16390), (2, 33000)]
+         (300, 256), (5, 4097), (2, 8200), (3, 9001), (3, 16384), (2, 16383), (12, 8), (2, 16390), (2, 33000)]
 
 
 @pytest.fixture(scope="module", autouse=True)
