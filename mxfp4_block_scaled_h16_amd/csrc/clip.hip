@@ -14,13 +14,13 @@
 namespace mx {
 namespace {
 
-// A launch has at most one workgroup a CU, and all of them are at neighbouring pieces at any time: of 872 MB of FP32 values into
-// bf16 ones the sums take 133 us (6.5 TB/s; with eight workgroups a CU, each at a run of pieces of its own, 171) and the
-// scaling 218 (249). The scaling goes from the last piece to the first: it begins with what the sums have left in the last
-// cache, and what it writes does not stay there if that is too much (372 us in all; 397 without such stores).
+// A launch has at most two workgroups a CU, and all of them are at neighbouring pieces at any time: 872 MB of FP32 values into bf16
+// ones take 355 us (with eight workgroups a CU, each at a run of pieces of its own, 423; with one 352, but then 105 million bf16
+// values 126 instead of 101). The scaling goes from the last piece to the first: it begins with what the sums have left in the last
+// cache, and what it writes does not stay there if that is too much (372 us; 397 without such stores).
 constexpr int kTensors = 128;                   // a launch's tensors (28 bytes each of a kernel's 4 KB of arguments)
 constexpr int64_t kPiece = 8192;                // values that a workgroup of 256 threads works at a time
-constexpr int64_t kMostBlocks = 256;            // workgroups of a launch, and so partial sums
+constexpr int64_t kMostBlocks = 512;            // workgroups of a launch, and so partial sums
 
 struct Tensors {
     const void *g[kTensors];
