@@ -6,7 +6,7 @@
 // One pass: a workgroup works a tile of 128 x 128 values, which holds whole blocks along both axes, in registers.
 //
 // Bound by memory. 8192 x 14336 in bf16 with codes along both axes: forward 121 to 125 us (704 MB, 5.7 TB/s; a kernel that only
-// reads and writes as many streams 117 to 134), the gradient 236 (1174 MB, 5.0 TB/s; such a kernel 206 to 222). The scale bytes, one
+// reads and writes as many streams 117 to 134), the gradient 235 (1174 MB, 5.0 TB/s; such a kernel 206 to 222). The scale bytes, one
 // to a line, are 11 us of the gradient's, the turning of the codes 2; more wavefronts (1024 threads of half the values, up
 // to eight a SIMD) made it 266, one pass through the LDS for both gradients no difference.
 #include <cfloat>
@@ -26,18 +26,23 @@ __device__ __forceinline__ float sigmoid(float g, float &e)
     return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// One tile. GRAD: the gradients, from da; DF32: da's type. F32: that of g and u. FULL: the tile lies inside the matrix, so that
+// One tile. GRAD: the gradients, from da; DF32: da's type. F32: that of g and u. kWhole: the tile lies inside the matrix, so that
 // nothing is checked and a row's address is the one before and a stride: 32 VALU operations a value of the gradient instead of
 // 38, which the large sizes do not notice, but the small ones do (256 x 512 forward 5.6 -> 4.3 us, the gradient of 1111 x 2001 in
-// FP32 18 -> 16).
-template <bool GRAD, bool DF32, bool F32, bool NT, bool FULL>
+// FP32 18 -> 16). kWithin, of the forward pass only: all that a thread has at the matrix' ends is read without branches, the
+// last row again behind it (1111 x 2001 9.3 -> 8.0 us, in FP32 9.9 -> 8.4); the gradient would spill (17 -> 27). kFew: value by value.
+template <bool GRAD, bool DF32, bool F32, bool NT, Ends E>
 __device__ __forceinline__ void gate_tile(const Gate &p, int64_t tm, int64_t tn, TileShared &sh)
 {
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int64_t row0 = tm * 128 + 4 * rg, col0 = tn * 128 + 8 * cg;
-    // rows whose loads are under way together: FP32's four take the registers of the values (8192 x 7168 in FP32 with codes along
-    // both axes, gradient 244 us and 222 with two, forward 146 and 137; bf16's 237 and 236)
-    constexpr int BATCH = F32 || DF32 ? 2 : 4;
+    constexpr bool FULL = E == kWhole;
+    // rows that are loaded and formed together: one in FP32 and two in bf16, as more at once take the registers of the values and
+    // come no sooner (8192 x 7168 in FP32 with codes along both axes: gradient 213 us, 225 with two rows and 253 with four, forward 131,
+    // 139 and 149; 8192 x 14336 in bf16: 235 and 121, with four 236 and 122, with one 236 and 125). At the ends, where a thread
+    // may read value by value, all four (the gradient of 1111 x 2001 in FP32 17 us, with two 29: spilled registers)
+    constexpr int BATCH = !FULL ? 4 : F32 || DF32 ? 1 : 2;
+    const Eight<E> eight(col0, p.cols);
     const void *gp = at<F32>(p.g.p, row0 * p.g.ld), *up = at<F32>(p.u.p, row0 * p.u.ld), *dp = at<DF32>(p.da.p, row0 * p.da.ld);
     float v[GRAD ? 2 : 1][4][8];
 #pragma unroll
@@ -52,6 +57,10 @@ __device__ __forceinline__ void gate_tile(const Gate &p, int64_t tm, int64_t tn,
                 g[j].template load<NT>(at<F32>(gp, i * p.g.ld + col0));
                 u[j].template load<NT>(at<F32>(up, i * p.u.ld + col0));
                 if constexpr (GRAD) d[j].template load<NT>(at<DF32>(dp, i * p.da.ld + col0));
+            } else if constexpr (E == kWithin) {
+                const int64_t row = min((int64_t)i, p.rows - 1 - row0);
+                g[j] = eight.template load<F32, NT>(at<F32>(gp, row * p.g.ld));
+                u[j] = eight.template load<F32, NT>(at<F32>(up, row * p.u.ld));
             } else {
                 const int64_t cols = row0 + i < p.rows ? p.cols : 0;
                 g[j] = load_raw<F32, true, NT>(at<F32>(gp, i * p.g.ld), col0, cols);
@@ -62,6 +71,13 @@ __device__ __forceinline__ void gate_tile(const Gate &p, int64_t tm, int64_t tn,
 #pragma unroll
         for (int j = 0; j < BATCH; ++j) {
             const int i = first + j;
+            if constexpr (E == kWithin) {
+                const int gone = row0 + i < p.rows ? eight.gone() : 8;
+                if (gone) {
+                    g[j].drop(gone);
+                    u[j].drop(gone);
+                }
+            }
             float a[8], b[8], c[8];
             g[j].get(a);
             u[j].get(b);
@@ -115,9 +131,11 @@ __global__ __launch_bounds__(512, GRAD || F32 ? 4 : 6) void gate_kernel(Gate p, 
     __shared__ TileShared sh;
     const auto [tm, tn] = tile_of(tiles_n);
     if ((tm + 1) * 128 <= p.rows && (tn + 1) * 128 <= p.cols)
-        gate_tile<GRAD, DF32, F32, NT, true>(p, tm, tn, sh);
-    else
-        gate_tile<GRAD, DF32, F32, NT, false>(p, tm, tn, sh);
+        gate_tile<GRAD, DF32, F32, NT, kWhole>(p, tm, tn, sh);
+    else if (GRAD || p.cols < 8)
+        gate_tile<GRAD, DF32, F32, NT, kFew>(p, tm, tn, sh);
+    else if constexpr (!GRAD)
+        gate_tile<GRAD, DF32, F32, NT, kWithin>(p, tm, tn, sh);
 }
 
 // Streaming loads, and stores of the codes along the rows, where the call is more than the last cache takes: 4096 x 14336 (352 MB)

@@ -180,13 +180,17 @@ __global__ __launch_bounds__(1024) void norm_forward_long_kernel(ForwardArgs arg
     }
 }
 
-// The codes along the columns, in tiles: a block's 128 rows need their rstd first. FULL: the tile lies inside the matrix.
-template <bool SF32, bool NT, bool FULL>
+// The codes along the columns, in tiles: a block's 128 rows need their rstd first. kWhole: the tile lies inside the
+// matrix. kWithin: what is read at its ends is read without branches, the last row again behind it (1111 x 2001 in FP32, both
+// kernels, 14.9 -> 14.6 us, 128 x 4095 in bf16 12.4 -> 10.7, 100 x 60 9.3 -> 8.1). kFew: value by value.
+template <bool SF32, bool NT, Ends E>
 __device__ __forceinline__ void norm_tile(const NormForward &p, const Rows &h, int64_t tm, int64_t tn, TileShared &sh)
 {
     const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int64_t row0 = tm * 128 + 4 * rg, col0 = tn * 128 + 8 * cg;
     const void *at0 = at<SF32>(h.p, row0 * h.ld);
+    constexpr bool FULL = E == kWhole;
+    const Eight<E> eight(col0, p.cols);
     Raw8<SF32> raw[4];
     float rstd[4], w[8], v[4][8];
 #pragma unroll
@@ -194,6 +198,8 @@ __device__ __forceinline__ void norm_tile(const NormForward &p, const Rows &h, i
         const bool in = FULL || row0 + i < p.rows;
         if constexpr (FULL)
             raw[i].template load<false>(at<SF32>(at0, i * h.ld + col0));
+        else if constexpr (E == kWithin)
+            raw[i] = eight.template load<SF32, false>(at<SF32>(at0, min((int64_t)i, p.rows - 1 - row0) * h.ld));
         else
             raw[i] = load_raw<SF32, true>(at<SF32>(at0, i * h.ld), col0, in ? p.cols : 0);
         rstd[i] = in ? p.rstd[row0 + i] : 0.0f;
@@ -206,6 +212,9 @@ __device__ __forceinline__ void norm_tile(const NormForward &p, const Rows &h, i
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        if constexpr (E == kWithin) {
+            if (const int gone = eight.gone()) raw[i].drop(gone);
+        }
         raw[i].get(v[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] = FULL || row0 + i < p.rows ? v[i][e] * rstd[i] * w[e] : 0.0f;
@@ -219,9 +228,11 @@ __global__ __launch_bounds__(512) void norm_columns_kernel(NormForward p, Rows h
     __shared__ TileShared sh;
     const int64_t tm = blockIdx.x / (unsigned)tiles_n, tn = blockIdx.x % (unsigned)tiles_n;
     if ((tm + 1) * 128 <= p.rows && (tn + 1) * 128 <= p.cols)
-        norm_tile<SF32, NT, true>(p, h, tm, tn, sh);
+        norm_tile<SF32, NT, kWhole>(p, h, tm, tn, sh);
+    else if (p.cols >= 8)
+        norm_tile<SF32, NT, kWithin>(p, h, tm, tn, sh);
     else
-        norm_tile<SF32, NT, false>(p, h, tm, tn, sh);
+        norm_tile<SF32, NT, kFew>(p, h, tm, tn, sh);
 }
 
 // Bytes of a call with codes or without.

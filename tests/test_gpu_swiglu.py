@@ -113,6 +113,20 @@ def test_halves_strides_and_in_place():
             assert torch.equal((d[:, :cols], d[:, cols:])[k], base.a)
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 3), (2, 8), (131, 9), (126, 135), (257, 1001)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_forward_in_place_at_the_ends(rows, cols, dtype):
+    """a over gate or up, where threads at the matrix' ends read values that others write."""
+    mx = _mx()
+    gate, up, _ = _data(rows, cols, dtype)
+    announce("gate in place", rows, cols, dtype)
+    base = mx.swiglu_forward(gate.cuda(), up.cuda(), axis="both", out_dtype=dtype)
+    for k in (0, 1):
+        at = gate.cuda(), up.cuda()
+        o = mx.swiglu_forward(*at, axis="both", a=at[k])
+        assert torch.equal(at[k], base.a) and torch.equal(o.q1, base.q1) and torch.equal(o.q0, base.q0)
+
+
 @pytest.mark.parametrize("rows,cols", [(130, 256), (5, 300)])
 def test_single_outputs_of_the_library(rows, cols):
     """Each gradient alone and each kind of codes of one of them, which the binding does not ask for."""
