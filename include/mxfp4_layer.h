@@ -125,7 +125,7 @@ mxfp4_status_t mxfp4_swiglu_backward(const void *da, mxfp4_dtype_t da_dtype, int
  *   sum_sq  [1] on the device, the sum of the squares: written by grad_norm (or NULL), read by grad_scale
  *   norm    FP32 [1] on the device, or NULL
  * The arrays of mxfp4_grad_t are host memory and only read during the call; tensors go to the device in the
- * kernels' arguments, 128 a launch.
+ * kernels' arguments, 224 a launch for the sums and 160 for the scaling.
  * Requirements: 0 <= n < 2^20; 0 <= count <= 2^37; max_norm > 0 and finite, eps >= 0 and finite. In mxfp4_grad_scale and
  * mxfp4_grad_clip no out may overlap another out or another tensor's g (MXFP4_ERR_ARG). ws: at least
  * mxfp4_grad_norm_workspace_bytes() bytes.

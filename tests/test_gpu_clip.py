@@ -29,7 +29,7 @@ def _norm(grads):
 
 
 LISTS = [[1], [7], [8192], [8193, 1, 16384], [0, 5, 0, 3], [100000, 3, 20001, 1 << 20], [1 + 37 * k % 9000 for k in range(128)],
-         [1 + 53 * k % 3000 for k in range(129)], [5] * 700]
+         [1 + 53 * k % 3000 for k in range(129)], [1 + 4099 * k % 25000 for k in range(161)], [8192 * (k % 3) + (k % 2) for k in range(230)], [5] * 700]
 
 
 @pytest.mark.parametrize("counts", LISTS, ids=lambda c: "%d-%d" % (len(c), sum(c)))

@@ -37,8 +37,8 @@ def run(tmp_path_factory):
 def test_launches_of_ordinary_sizes(run):
     want = {("norm", 8192, 4096, ROWS): 1, ("norm", 8192, 4096, ROWS + COLS): 2, ("norm", 1, 100000, ROWS): 1, ("normgrad", 8192, 4096, 0): 2,
             ("normgrad", 0, 300, 0): 1, ("gate", 8192, 14336, ROWS + COLS): 1, ("gategrad", 8192, 14336, ROWS + COLS): 1,
-            ("gate", 0, 300, ROWS): 0, ("clip", 1, 1000, 0): 2, ("clip", 128, 10, 0): 2, ("clip", 129, 10, 0): 4, ("clip", 0, 1, 0): 1,
-            ("clip", 128 * 17, 1 << 24, 0): 2 * 17 + 1, ("scale", 300, 1000, 0): 3, ("scale", 0, 1, 0): 1, ("sum", 300, 1000, 0): 4, ("sum", 0, 1, 0): 1}
+            ("gate", 0, 300, ROWS): 0, ("clip", 1, 1000, 0): 2, ("clip", 160, 10, 0): 2, ("clip", 161, 10, 0): 3, ("clip", 224, 10, 0): 3, ("clip", 225, 10, 0): 4, ("clip", 0, 1, 0): 1,
+            ("clip", 224 * 9, 1 << 24, 0): 9 + 1 + 13, ("scale", 321, 1000, 0): 3, ("scale", 0, 1, 0): 1, ("sum", 300, 1000, 0): 3, ("sum", 0, 1, 0): 1}
     for (line, launches), got in zip(want.items(), run(list(want))):
         assert got[:3] == (OK, launches, 0), (line, got)
 
