@@ -9,26 +9,36 @@
 // reads and writes as many streams 117 to 134), the gradient 235 (1174 MB, 5.0 TB/s; such a kernel 206 to 222). The scale bytes, one
 // to a line, are 11 us of the gradient's, the turning of the codes 2; more wavefronts (1024 threads of half the values, up
 // to eight a SIMD) made it 266, one pass through the LDS for both gradients no difference.
-#include <cfloat>
-
 #include "internal.h"
 #include "layer_device.h"
 
 namespace mx {
 namespace {
 
-// s = 1 / (1 + e) and 1 - s = e s, e = exp(-g). The hardware's exponential and reciprocal are off by 2^-23 each, and the
-// exponent's rounding, |g| 2^-24, is one of e: s and 1 - s are off by at most (8 + 1.3 |g|) 2^-24 of themselves, the larger of the
-// two by far less. Below g = -88 e is infinite and s zero, where it is below 2^-126 (1 - s is multiplied with it).
+constexpr float kLn2 = 0.69314718055994530942f;                                   // ln 2, rounded
+constexpr float kLn2Low = (float)(0.69314718055994530942 - (double)kLn2);        // and what the rounding left
+
+// s = 1 / (1 + e) and 1 - s = e s, e = exp(-g). exp2's argument k = -g log2(e) is rounded by up to |k| 2^-24, which the exponential would
+// multiply by: -g = k ln 2 + r gives r, and e = 2^k (1 + r). The reciprocal is the hardware's with a Newton step, whose remainder 1 - s -
+// e s knows e as it was before 1 + e rounded it. In units of 2^-24 of the value at most: e 3.1 (the hardware's 2, the last sum's 1), s
+// 4.6 (e's, half for 1 - s, the last sum's 1), 1 - s 5.6; measured 3.5 for g s. 11 operations where the hardware's functions alone are 4, which
+// are off by up to 16 at g = -16 and 65 at -80: no difference in time (8192 x 14336 121 us, the gradient 235).
+// e stays finite, and s is zero from 1 + e = 2^126 on, as the reciprocal has no subnormal results: so an infinite g gives what the
+// formulas do, and a NaN, for which e is some number, comes back in the products with g.
 __device__ __forceinline__ float sigmoid(float g, float &e)
 {
-    e = __builtin_amdgcn_exp2f(g * -1.44269504088896340736f);
-    return __builtin_amdgcn_rcpf(1.0f + e);
+    const float x = __builtin_amdgcn_fmed3f(g, -88.5f, 128.0f);
+    const float k = x * -1.44269504088896340736f;
+    const float r = fmaf(k, -kLn2Low, fmaf(k, -kLn2, -x));
+    e = __builtin_amdgcn_exp2f(k);
+    e = fmaf(e, r, e);
+    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    return fmaf(fmaf(-e, s, 1.0f - s), s, s);
 }
 
 // One tile. GRAD: the gradients, from da; DF32: da's type. F32: that of g and u. kWhole: the tile lies inside the matrix, so that
-// nothing is checked and a row's address is the one before and a stride: 32 VALU operations a value of the gradient instead of
-// 38, which the large sizes do not notice, but the small ones do (256 x 512 forward 5.6 -> 4.3 us, the gradient of 1111 x 2001 in
+// nothing is checked and a row's address is the one before and a stride: six VALU operations a value fewer in the gradient,
+// which the large sizes do not notice, but the small ones do (256 x 512 forward 5.6 -> 4.3 us, the gradient of 1111 x 2001 in
 // FP32 18 -> 16). kWithin, of the forward pass only: all that a thread has at the matrix' ends is read without branches, the
 // last row again behind it (1111 x 2001 9.3 -> 8.0 us, in FP32 9.9 -> 8.4); the gradient would spill (17 -> 27). kFew: value by value.
 template <bool GRAD, bool DF32, bool F32, bool NT, Ends E>
@@ -87,9 +97,10 @@ __device__ __forceinline__ void gate_tile(const Gate &p, int64_t tm, int64_t tn,
                 float x;
                 const float s = sigmoid(a[e], x);
                 if constexpr (GRAD) {
-                    const float t = fminf(x, FLT_MAX) * s;
-                    v[0][i][e] = c[e] * (b[e] * (s * fmaf(a[e], t, 1.0f)));
-                    v[1][i][e] = c[e] * (a[e] * s);
+                    // s (1 + g (1 - s)) as s + (g s) (1 - s): one rounding less
+                    const float f = a[e] * s;
+                    v[0][i][e] = c[e] * (b[e] * fmaf(f, x * s, s));
+                    v[1][i][e] = c[e] * f;
                     // now, while the inputs leave their registers: formed where it is used, the kernel holds 186 (345 us instead
                     // of 256 at 8192 x 14336)
                     asm volatile("" : "+v"(v[1][i][e]));
