@@ -415,8 +415,6 @@ def grad_norm(grads, workspace=None, stream=None):
     """The norm over all values of the gradients (dense tensors, bf16 or f32 in any mixture) together. Returns (sum_sq, norm): the
     sum of squares, float64 [], which ranks that hold parts of the gradients add up, and its root, FP32 []."""
     device, items, n = _grads(grads, None)
-    if workspace is not None:
-        _same_device(grads=grads[0], workspace=workspace)
     with _on(device, stream):
         L, at = layer_lib(), items.buffer_info()[0]
         ws = _room(workspace, L.mxfp4_grad_norm_workspace_bytes(at, n) if workspace is None else 0, device)
