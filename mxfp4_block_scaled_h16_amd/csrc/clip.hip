@@ -104,8 +104,9 @@ __global__ __launch_bounds__(256) void join_kernel(const double *part, int count
     if (norm) *norm = (float)sqrt(sum);
 }
 
+// values times c 2^e2
 template <bool F32, bool OUT, bool NT>
-__device__ __forceinline__ void scale_piece(const void *g, void *out, int64_t at0, int count, float c)
+__device__ __forceinline__ void scale_piece(const void *g, void *out, int64_t at0, int count, float c, int e2)
 {
     g = at<F32>(g, at0);
     out = at<OUT>(out, at0);
@@ -119,6 +120,10 @@ __device__ __forceinline__ void scale_piece(const void *g, void *out, int64_t at
         r[k].get(v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= c;
+        if (e2) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = ldexpf(v[e], e2);
+        }
         Raw8<OUT> o;
         o.set(v);
         store_raw<OUT, true, NT>(o, out, k * 2048 + 8 * (int)threadIdx.x, count);
@@ -133,21 +138,25 @@ __global__ __launch_bounds__(256) void scale_kernel(Pairs t, const double *part,
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
     // a norm that is NaN makes everything NaN
     const double q = max_norm / (n + eps);
-    const float c = q > 1.0 ? 1.0f : (float)q;
+    // a factor below FP32's normal range would lose bits that the products have: its exponent is applied to them (for all lanes
+    // or none, so that other factors pay nothing)
+    int e2 = 0;
+    const float c = q > 1.0 ? 1.0f : (float)(q < 0x1p-126 ? frexp(q, &e2) : q);
+    e2 = __builtin_amdgcn_readfirstlane(e2);
     const int end = (int)t.first[t.n];
     int i = end - 1 - (int)blockIdx.x;
     for (int k = tensor_of(t, (uint32_t)max(i, 0)); i >= 0; i -= (int)gridDim.x) {
         while (t.first[k] > (uint32_t)i) --k;
-        if (c == 1.0f && t.g[k] == t.out[k]) continue;      // in place and nothing to do
+        if (c == 1.0f && e2 == 0 && t.g[k] == t.out[k]) continue;      // in place and nothing to do
         const int64_t at0 = (int64_t)((uint32_t)i - t.first[k]) * kPiece;
         const int count = t.count((uint32_t)i, k);
         const bool f32 = (t.f32[k / 32] >> (k % 32)) & 1, o32 = (t.out_f32[k / 32] >> (k % 32)) & 1;
         if (f32)
-            o32 ? scale_piece<true, true, NT>(t.g[k], t.out[k], at0, count, c)
-                : scale_piece<true, false, NT>(t.g[k], t.out[k], at0, count, c);
+            o32 ? scale_piece<true, true, NT>(t.g[k], t.out[k], at0, count, c, e2)
+                : scale_piece<true, false, NT>(t.g[k], t.out[k], at0, count, c, e2);
         else
-            o32 ? scale_piece<false, true, NT>(t.g[k], t.out[k], at0, count, c)
-                : scale_piece<false, false, NT>(t.g[k], t.out[k], at0, count, c);
+            o32 ? scale_piece<false, true, NT>(t.g[k], t.out[k], at0, count, c, e2)
+                : scale_piece<false, false, NT>(t.g[k], t.out[k], at0, count, c, e2);
     }
 }
 
