@@ -48,8 +48,8 @@ __device__ __forceinline__ void gate_tile(const Gate &p, int64_t tm, int64_t tn,
     const int64_t row0 = tm * 128 + 4 * rg, col0 = tn * 128 + 8 * cg;
     constexpr bool FULL = E == kWhole;
     // rows that are loaded and formed together: one in FP32 and two in bf16, as more at once take the registers of the values and
-    // come no sooner (8192 x 7168 in FP32 with codes along both axes: gradient 213 us, 225 with two rows and 253 with four, forward 131,
-    // 139 and 149; 8192 x 14336 in bf16: 235 and 121, with four 236 and 122, with one 236 and 125). At the ends, where a thread
+    // come no sooner (8192 x 7168 in FP32 with codes along both axes: gradient 200 us, 204 with two rows and 211 with four, forward 122,
+    // 121 and 126; 8192 x 14336 in bf16: 235 and 121, with four 236 and 122, with one 236 and 125). At the ends, where a thread
     // may read value by value, all four (the gradient of 1111 x 2001 in FP32 17 us, with two 29: spilled registers)
     constexpr int BATCH = !FULL ? 4 : F32 || DF32 ? 1 : 2;
     const Eight<E> eight(col0, p.cols);
@@ -149,18 +149,26 @@ __global__ __launch_bounds__(512, GRAD || F32 ? 4 : 6) void gate_kernel(Gate p, 
         gate_tile<GRAD, DF32, F32, NT, kWithin>(p, tm, tn, sh);
 }
 
-// Streaming loads, and stores of the codes along the rows, where the call is more than the last cache takes: 4096 x 14336 (352 MB)
-// 73 -> 64 us, 8192 x 14336 141 -> 121, the gradient 126 -> 111 and 246 -> 236; at 1024 x 14336 (88 MB) 18.6 and 19.7. Such
-// stores of the codes along the columns as well: 151 and 268.
+// bf16 rows that all start at multiples of 16 bytes (or none: the forward pass has no da)
+bool lines(const Rows &r) { return (uintptr_t)r.p % 16 == 0 && r.ld % 8 == 0; }
+
+// Streaming loads, and stores of the codes along the rows, where the call is more than the last cache takes, all of it is bf16 and rows
+// start at multiples of 16 bytes (a line that two loads share is read twice): 4096 x 14336 with codes along both axes (352 MB) 74 -> 67 us,
+// 8192 x 14336 143 -> 138, the gradient 126 -> 121 and 244 -> 237 (separate matrices, outputs in new memory); at 1024 x 14336 (88 MB) 18.6 and 19.7. Such
+// stores of the codes along the columns as well: 151 and 268. Rows that start elsewhere: 8192 x 14336 148 and 159, 255 and 261, bf16
+// results alone 136 and 157, 230 and 260. FP32: 8192 x 7168 122 and 129, 200 and 217.
 template <bool GRAD, bool DF32, bool F32>
 hipError_t run(const Gate &p, hipStream_t stream)
 {
     const int64_t tiles_n = (p.cols + 127) / 128;
     const dim3 grid((unsigned)((p.rows + 127) / 128 * tiles_n)), block(512);
-    int64_t bytes = (F32 ? 8 : 4) + (GRAD ? DF32 ? 4 : 2 : 0);
-    for (int k = 0; k < 2; ++k) bytes += (p.out[k].p ? p.out_f32 ? 4 : 2 : 0) + (p.q1[k].q ? 1 : 0) + (p.q0[k].q ? 1 : 0);
-    return p.rows * p.cols > kStreamBytes / bytes ? launch(gate_kernel<GRAD, DF32, F32, true>, grid, block, 0, stream, p, (int)tiles_n)
-                                                : launch(gate_kernel<GRAD, DF32, F32, false>, grid, block, 0, stream, p, (int)tiles_n);
+    if constexpr (!DF32 && !F32) {
+        int64_t bytes = GRAD ? 6 : 4;
+        for (int k = 0; k < 2; ++k) bytes += (p.out[k].p ? p.out_f32 ? 4 : 2 : 0) + (p.q1[k].q ? 1 : 0) + (p.q0[k].q ? 1 : 0);
+        if (p.rows * p.cols > kStreamBytes / bytes && lines(p.g) && lines(p.u) && lines(p.da))
+            return launch(gate_kernel<GRAD, DF32, F32, true>, grid, block, 0, stream, p, (int)tiles_n);
+    }
+    return launch(gate_kernel<GRAD, DF32, F32, false>, grid, block, 0, stream, p, (int)tiles_n);
 }
 
 }  // namespace
