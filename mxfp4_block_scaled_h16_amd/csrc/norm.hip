@@ -258,16 +258,22 @@ hipError_t pick_forward(const ForwardArgs &args, hipStream_t stream)
     }
     return run(norm_forward_long_kernel<XF32, SF32, RES>, rows, 1024);
 }
-// Streaming loads of x and r and stores of the codes, where the call is more than the last cache takes: 8192 x 4096 (268 MB) 62 ->
-// 58 us, 16384 x 4096 130 -> 106; 4096 x 4096 (134 MB) 32.7 and 32.2, 2048 x 4096 in FP32 (101 MB) 26 and 29. They are for rows
-// of whole 16 bytes: a line that two loads share is read twice (15232 x 5627 202 us, and 212 with them).
+// Streaming loads of x and r and stores of the codes, where the call is more than the last cache takes (outputs in new memory; where rows
+// start at multiples of 16 bytes, and where not): 8192 x 4096 in bf16 with codes along both axes (268 MB) 63 -> 60 us and 69 -> 65, 5000 x
+// 8192 76 -> 69 and 82 -> 78, 32768 x 1024 61 -> 58 and 61 -> 58, with a bf16 result alone no difference; 4096 x 4096 (134 MB) 32.2 and 32.7.
+// With an FP32 stream only for codes along the columns, which read h again (8192 x 8192 207 -> 193 and 212 -> 200; a bf16 result alone
+// 153 and 158), and not for x in FP32 (8192 x 4096 109 and 112, with a bf16 result alone 85 and 93). Not for rows that end within eight
+// values: 15232 x 5627 202 us, and 212 with them.
 template <bool XF32, bool SF32, bool RES>
 hipError_t forward(const ForwardArgs &args, bool nt, hipStream_t stream)
 {
     const int64_t cols = args.p.cols;
     if (cols % 8)
         return cols < 8 ? pick_forward<XF32, SF32, RES, kFew, false>(args, stream) : pick_forward<XF32, SF32, RES, kWithin, false>(args, stream);
-    return nt ? pick_forward<XF32, SF32, RES, kWhole, true>(args, stream) : pick_forward<XF32, SF32, RES, kWhole, false>(args, stream);
+    if constexpr (!XF32) {
+        if (nt) return pick_forward<XF32, SF32, RES, kWhole, true>(args, stream);
+    }
+    return pick_forward<XF32, SF32, RES, kWhole, false>(args, stream);
 }
 
 }  // namespace
@@ -275,7 +281,8 @@ hipError_t forward(const ForwardArgs &args, bool nt, hipStream_t stream)
 hipError_t launch_norm_forward(const NormForward &p, hipStream_t stream)
 {
     const ForwardArgs args{p, 1.0 / (double)p.cols};
-    const bool res = p.r.p != nullptr, nt = forward_bytes(p) > kStreamBytes;
+    const bool res = p.r.p != nullptr;
+    const bool nt = forward_bytes(p) > kStreamBytes && !p.x_f32 && !(res && p.s_f32 && !p.q0.q);
     hipError_t e;
     if (!res)
         e = p.x_f32 ? forward<true, true, false>(args, nt, stream) : forward<false, false, false>(args, nt, stream);

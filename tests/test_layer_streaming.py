@@ -50,3 +50,18 @@ def test_gate(kernels, name, out):
     for a, b in ((F32, F32), (F32, BF), (BF, F32)):
         if name == "gategrad" or a == F32:
             assert _streams(kernels, name, 8192, 14336, 0, 0, a, b, out) == [False]
+
+
+def test_norm(kernels):
+    """x in bf16, and an FP32 stream only for codes along the columns; the kernel of those goes with the first one."""
+    for pad, off in ((0, 0), (1, 1)):
+        assert _streams(kernels, "norm", 16384, 4096, pad, off, BF, BF, WIDE) == [True]
+        assert _streams(kernels, "norm", 16384, 4096, pad, off, BF, BF, ROWS) == [True]
+        assert _streams(kernels, "norm", 16384, 4096, pad, off, BF, BF, BOTH) == [True, True]
+        assert _streams(kernels, "norm", 16384, 4096, pad, off, BF, F32, BOTH) == [True, True]
+        for a, b, out in ((BF, F32, WIDE), (BF, F32, ROWS), (F32, F32, WIDE), (F32, BF, ROWS)):
+            assert _streams(kernels, "norm", 16384, 4096, pad, off, a, b, out) == [False]
+        for b in (F32, BF):
+            assert _streams(kernels, "norm", 16384, 4096, pad, off, F32, b, BOTH) == [False, False]
+    assert _streams(kernels, "norm", 4096, 4096, 0, 0, BF, BF, BOTH) == [False, False]
+    assert _streams(kernels, "norm", 16384, 4095, 1, 0, BF, BF, WIDE) == [False]
