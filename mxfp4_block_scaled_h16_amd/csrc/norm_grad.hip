@@ -262,17 +262,22 @@ hipError_t pick_backward(const BackwardArgs &args, unsigned blocks, hipStream_t 
     }
     return run(norm_backward_long_kernel<BF32, SF32>, 1024);
 }
-// Streaming loads where the call is more than the last cache takes: 8192 x 4096 (268 MB) 60 -> 52 us, 16384 x 4096 110 -> 98; 4096 x
-// 4096 (134 MB) 30 both ways, 2048 x 4096 18 and 23. Rows of whole 16 bytes only: a line that two loads share is read twice.
+// Streaming loads where the call is more than the last cache takes and the stream is bf16 (outputs in new memory; where rows start at
+// multiples of 16 bytes, and where not): 8192 x 4096 (268 MB) 61 -> 58 us and 60 -> 59, with dy in FP32 74 -> 69 and 74 -> 73, 5000 x 8192
+// 72 -> 71 and 83 -> 82, 32768 x 1024 58 -> 56 and 58 -> 58; 4096 x 4096 (134 MB) 30 both ways, 2048 x 4096 18 and 23. With an FP32 stream
+// 8192 x 8192 takes 189 and 187, and 189 and 192; dy in FP32 as well 8192 x 4096 110 and 112, and 111 and 115. Not for rows that end within
+// eight values: a line that two loads share is read twice.
 template <bool BF32, bool SF32>
 hipError_t backward(const BackwardArgs &args, unsigned blocks, hipStream_t stream)
 {
     const NormBackward &p = args.p;
-    const int64_t bytes = p.rows * p.cols * ((BF32 ? 4 : 2) + (SF32 ? 4 : 2) * (p.dres.p ? 3 : 2));
     if (p.cols % 8)
         return p.cols < 8 ? pick_backward<BF32, SF32, kFew, false>(args, blocks, stream) : pick_backward<BF32, SF32, kWithin, false>(args, blocks, stream);
-    return bytes > kStreamBytes ? pick_backward<BF32, SF32, kWhole, true>(args, blocks, stream)
-                                : pick_backward<BF32, SF32, kWhole, false>(args, blocks, stream);
+    if constexpr (!SF32) {
+        const int64_t bytes = p.rows * p.cols * ((BF32 ? 4 : 2) + (p.dres.p ? 6 : 4));
+        if (bytes > kStreamBytes) return pick_backward<BF32, SF32, kWhole, true>(args, blocks, stream);
+    }
+    return pick_backward<BF32, SF32, kWhole, false>(args, blocks, stream);
 }
 
 }  // namespace

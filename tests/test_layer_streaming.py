@@ -65,3 +65,12 @@ def test_norm(kernels):
             assert _streams(kernels, "norm", 16384, 4096, pad, off, F32, b, BOTH) == [False, False]
     assert _streams(kernels, "norm", 4096, 4096, 0, 0, BF, BF, BOTH) == [False, False]
     assert _streams(kernels, "norm", 16384, 4095, 1, 0, BF, BF, WIDE) == [False]
+
+
+def test_norm_gradient(kernels):
+    """The stream in bf16."""
+    for pad, off in ((0, 0), (1, 1)):
+        for dy in (BF, F32):
+            assert _streams(kernels, "normgrad", 16384, 4096, pad, off, dy, BF, WIDE) == [True]
+            assert _streams(kernels, "normgrad", 16384, 4096, pad, off, dy, F32, WIDE) == [False]
+    assert _streams(kernels, "normgrad", 4096, 4096, 0, 0, BF, BF, WIDE) == [False]
