@@ -93,8 +93,10 @@ mxfp4_status_t mxfp4_rmsnorm_backward(const void *dy, mxfp4_dtype_t dy_dtype, in
  * q0_up = q0_gate + cols * ldq0, s0_up = s0_gate + cols * lds0 one of 2 cols rows (with any cols). q1_gate and q1_up
  * have one ldq1 and lds1, q0_gate and q0_up one ldq0 and lds0.
  * a may be gate or up, and dgate and dup may be any two of gate, up and da, with the same type and row stride.
- * All of it in FP32. a and dup are off by at most 2^-21 of themselves and dgate by 2^-20 of |da up s| (1 + |gate (1 - s)|),
- * before the rounding to their types; an s or 1 - s below 2^-126 may be lost (gates beyond 87).
+ * All of it in FP32, the products as (gate s) up, da (gate s) and da (up (s (1 + gate (1 - s)))). Where the results and what stands
+ * in brackets are in FP32's normal range, a and dup are off by at most 2^-21 of themselves and dgate by 2^-20 of
+ * |da up s| (1 + |gate (1 - s)|), before the rounding to their types (da up alone may overflow); an s or 1 - s below
+ * 2^-126 may be lost (gates beyond 87).
  * NaN as in the formulas.
  * Requirements: 0 <= rows, cols < 2^31; fewer than 2^23 tiles of 128 x 128.
  */
