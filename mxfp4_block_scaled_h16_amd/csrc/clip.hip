@@ -15,7 +15,7 @@ namespace mx {
 namespace {
 
 // A launch has at most two workgroups a CU, and all of them are at neighbouring pieces at any time: 872 MB of FP32 values into bf16
-// ones take 355 to 363 us (with eight workgroups a CU, each at a run of pieces of its own, 423; with one 352, but then 105 million bf16
+// ones take 355 to 365 us (with eight workgroups a CU, each at a run of pieces of its own, 423; with one 352, but then 105 million bf16
 // values 126 instead of 101). The scaling goes from the last piece to the first: it begins with what the sums have left in the last
 // cache, and what it writes does not stay there if that is too much (372 us; 397 without such stores).
 constexpr int64_t kPiece = 8192;                // values that a workgroup of 256 threads works at a time

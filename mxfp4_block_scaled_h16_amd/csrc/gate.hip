@@ -6,7 +6,7 @@
 // One pass: a workgroup works a tile of 128 x 128 values, which holds whole blocks along both axes, in registers.
 //
 // Bound by memory. 8192 x 14336 in bf16 with codes along both axes: forward 121 to 125 us (704 MB, 5.7 TB/s; a kernel that only
-// reads and writes as many streams 117 to 134), the gradient 235 (1174 MB, 5.0 TB/s; such a kernel 206 to 222). The scale bytes, one
+// reads and writes as many streams 117 to 134), the gradient 236 (1174 MB, 5.0 TB/s; such a kernel 206 to 222). The scale bytes, one
 // to a line, are 11 us of the gradient's, the turning of the codes 2; more wavefronts (1024 threads of half the values, up
 // to eight a SIMD) made it 266, one pass through the LDS for both gradients no difference.
 #include "internal.h"
@@ -22,7 +22,7 @@ constexpr float kLn2Low = (float)(0.69314718055994530942 - (double)kLn2);       
 // multiply by: -g = k ln 2 + r gives r, and e = 2^k (1 + r). The reciprocal is the hardware's with a Newton step, whose remainder 1 - s -
 // e s knows e as it was before 1 + e rounded it. In units of 2^-24 of the value at most: e 3.1 (the hardware's 2, the last sum's 1), s
 // 4.6 (e's, half for 1 - s, the last sum's 1), 1 - s 5.6; measured 3.5 for g s. 11 operations where the hardware's functions alone are 4, which
-// are off by up to 16 at g = -16 and 65 at -80: no difference in time (8192 x 14336 121 us, the gradient 235).
+// are off by up to 16 at g = -16 and 65 at -80; 8192 x 14336 takes 121 us with either, the gradient 235 and 236, 256 x 512 4.9 instead of 4.2.
 // e stays finite, and s is zero from 1 + e = 2^126 on, as the reciprocal has no subnormal results: so an infinite g gives what the
 // formulas do, and a NaN, for which e is some number, comes back in the products with g.
 __device__ __forceinline__ float sigmoid(float g, float &e)
@@ -38,9 +38,9 @@ __device__ __forceinline__ float sigmoid(float g, float &e)
 
 // One tile. GRAD: the gradients, from da; DF32: da's type. F32: that of g and u. kWhole: the tile lies inside the matrix, so that
 // nothing is checked and a row's address is the one before and a stride: six VALU operations a value fewer in the gradient,
-// which the large sizes do not notice, but the small ones do (256 x 512 forward 5.6 -> 4.3 us, the gradient of 1111 x 2001 in
-// FP32 18 -> 16). kWithin, of the forward pass only: all that a thread has at the matrix' ends is read without branches, the
-// last row again behind it (1111 x 2001 9.3 -> 8.0 us, in FP32 9.9 -> 8.4); the gradient would spill (17 -> 27). kFew: value by value.
+// which the large sizes do not notice, but the small ones do (256 x 512 forward 5.1 -> 4.9 us, the gradient of 1111 x 2001 in
+// FP32 17.3 -> 16.6). kWithin, of the forward pass only: all that a thread has at the matrix' ends is read without branches, the
+// last row again behind it (1111 x 2001 9.5 -> 8.1 us, in FP32 10.0 -> 8.5); the gradient would spill (17 -> 27). kFew: value by value.
 template <bool GRAD, bool DF32, bool F32, bool NT, Ends E>
 __device__ __forceinline__ void gate_tile(const Gate &p, int64_t tm, int64_t tn, TileShared &sh)
 {

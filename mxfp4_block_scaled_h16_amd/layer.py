@@ -440,7 +440,8 @@ def grad_scale(grads, sum_sq, max_norm, eps=1e-6, out=None, stream=None):
 
 def grad_clip(grads, max_norm, eps=1e-6, out=None, workspace=None, stream=None):
     """grad_norm and grad_scale in one: scales the gradients so that their norm is at most max_norm, in place or into
-    `out`, and returns the norm that they had, FP32 []. An infinite norm makes finite values 0, one that is NaN all values."""
+    `out`, and returns the norm that they had, FP32 []. An infinite norm makes finite values 0, one that is NaN all values.
+    max_norm and eps count as FP32 holds them, here and in grad_scale."""
     device, items, n = _grads(grads, out)
     with _on(device, stream):
         L, at = layer_lib(), items.buffer_info()[0]
