@@ -154,9 +154,9 @@ bool lines(const Rows &r) { return (uintptr_t)r.p % 16 == 0 && r.ld % 8 == 0; }
 
 // Streaming loads, and stores of the codes along the rows, where the call is more than the last cache takes, all of it is bf16 and rows
 // start at multiples of 16 bytes (a line that two loads share is read twice): 4096 x 14336 with codes along both axes (352 MB) 74 -> 67 us,
-// 8192 x 14336 143 -> 138, the gradient 126 -> 121 and 244 -> 237 (separate matrices, outputs in new memory); at 1024 x 14336 (88 MB) 18.6 and 19.7. Such
-// stores of the codes along the columns as well: 151 and 268. Rows that start elsewhere: 8192 x 14336 148 and 159, 255 and 261, bf16
-// results alone 136 and 157, 230 and 260. FP32: 8192 x 7168 122 and 129, 200 and 217.
+// 8192 x 14336 143 -> 138, the gradient 126 -> 121 and 244 -> 237 (separate matrices, outputs in new memory); at 1024 x 14336 (88 MB)
+// 18.6 and 19.7. Such stores of the codes along the columns as well: 151 and 268. Rows that start elsewhere: 8192 x 14336 148 and 159,
+// 255 and 261, bf16 results alone 136 and 157, 230 and 260. FP32: 8192 x 7168 122 and 129, 200 and 217.
 template <bool GRAD, bool DF32, bool F32>
 hipError_t run(const Gate &p, hipStream_t stream)
 {
